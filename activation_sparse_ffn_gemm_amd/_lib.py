@@ -24,9 +24,14 @@ DEV_TILE_OVERFLOW, DEV_OVF_CAPACITY, DEV_BAD_INDEX = 1, 2, 4
 EXPORTS = ("twell_gate_pack", "twell_gate_workspace_bytes", "twell_ffn_fwd", "twell_fwd_workspace_bytes", "twell_decode_fwd",
            "twell_decode_workspace_bytes", "twell_to_hybrid", "hybrid_ffn_fwd",
            "hybrid_fwd_workspace_bytes", "hybrid_ffn_bwd", "hybrid_bwd_workspace_bytes",
-           "twell_status_str", "twell_decode_fwd_noalloc")
+           "twell_status_str", "twell_decode_fwd_noalloc", "twell_rmsnorm_fwd",
+           "twell_rmsnorm_bwd", "twell_rmsnorm_bwd_workspace_bytes", "twell_fp8_quant",
+           "twell_fp8_matmul", "twell_fp8_matmul_workspace_bytes")
 STATIC_SCRATCH_BYTES = 12 << 20  # twell_decode_fwd_noalloc's scratch per GPU
 DECODE_T = 64  # most tokens twell_decode_fwd takes (few-token kernels up to here)
+FP8_BLOCK = 128  # columns that share a scale of an 8-bit matrix
+NORM_COLS = 16384  # widest row the norm takes
+SUMS_F32, SUMS_FP8 = 0, 1  # how twell_fp8_matmul adds products
 
 c_i32, c_sz, c_p = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
 
@@ -82,6 +87,16 @@ class HybridC(ctypes.Structure):
                 ("ell_val", c_p), ("ovf_rows", c_p), ("dense", c_p), ("n_ovf", c_p)]
 
 
+class MatC(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("cols", c_i32), ("ld", ctypes.c_int64),
+                ("dtype", ctypes.c_int), ("data", c_p)]
+
+
+class Fp8C(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("cols", c_i32), ("block_rows", c_i32), ("q", c_p),
+                ("scale", c_p)]
+
+
 _lib = None
 
 
@@ -122,10 +137,20 @@ def load() -> ctypes.CDLL:
     L.hybrid_fwd_workspace_bytes.restype = S
     L.hybrid_bwd_workspace_bytes.argtypes = [ctypes.c_int, I, I, I, I, I]
     L.hybrid_bwd_workspace_bytes.restype = S
+    M, Q, F = ctypes.POINTER(MatC), ctypes.POINTER(Fp8C), ctypes.c_float
+    L.twell_rmsnorm_fwd.argtypes = [M, M, P, ctypes.c_int, F, M, M, Q, P, P]
+    L.twell_rmsnorm_bwd.argtypes = [M, M, P, ctypes.c_int, F, M, M, P, P, S, P, P]
+    L.twell_rmsnorm_bwd_workspace_bytes.argtypes = [I, I]
+    L.twell_rmsnorm_bwd_workspace_bytes.restype = S
+    L.twell_fp8_quant.argtypes = [M, Q, Q, P, P]
+    L.twell_fp8_matmul.argtypes = [Q, Q, M, I, P, S, P, P]
+    L.twell_fp8_matmul_workspace_bytes.argtypes = [I, I, I]
+    L.twell_fp8_matmul_workspace_bytes.restype = S
     L.twell_status_str.argtypes = [ctypes.c_int]
     L.twell_status_str.restype = ctypes.c_char_p
     for f in ("twell_gate_pack", "twell_ffn_fwd", "twell_decode_fwd", "twell_to_hybrid",
-              "hybrid_ffn_fwd", "hybrid_ffn_bwd", "twell_decode_fwd_noalloc"):
+              "hybrid_ffn_fwd", "hybrid_ffn_bwd", "twell_decode_fwd_noalloc", "twell_rmsnorm_fwd",
+              "twell_rmsnorm_bwd", "twell_fp8_quant", "twell_fp8_matmul"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L
@@ -549,4 +574,206 @@ def ffn_bwd(x, dy, hy: Hybrid, wg_t, wu_t, wd, out=None, workspace=None, status=
                                  _ptr(dwu),
                                  _ptr(dwd), _ptr(workspace), nbytes, _ptr(status),
                                  _timing(timing), _stream(x.device)), "hybrid_ffn_bwd")
+    return out
+
+
+# ---- the residual stream's norm and the 8-bit products around the layer
+@dataclass
+class Fp8:
+    """A matrix [rows][cols] in 8 bits: element (r, c) stands for
+    q[r][c] * scale[c // 128][r // block_rows]."""
+
+    q: torch.Tensor      # [rows][cols rounded up to 128] float8_e4m3fn, zeros past cols
+    scale: torch.Tensor  # [ceil(cols / 128)][ceil(rows / block_rows)] float32
+    cols: int
+    block_rows: int = 1
+
+    @property
+    def rows(self):
+        return self.q.shape[0]
+
+    def c(self) -> Fp8C:
+        return Fp8C(self.q.shape[0], self.cols, self.block_rows, self.q.data_ptr(),
+                    self.scale.data_ptr())
+
+    def float(self) -> torch.Tensor:
+        """The float32 values the matrix stands for."""
+        s = self.scale.t().repeat_interleave(self.block_rows, 0)[:self.rows]
+        return (self.q.float() * s.repeat_interleave(FP8_BLOCK, 1))[:, :self.cols]
+
+
+def empty_fp8(rows, cols, block_rows, device) -> Fp8:
+    nb = -(-cols // FP8_BLOCK)
+    return Fp8(torch.empty((rows, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=device),
+               torch.empty((nb, -(-rows // block_rows)), dtype=torch.float32, device=device),
+               cols, block_rows)
+
+
+def _check_fp8(m, name, rows=None, cols=None):
+    if not isinstance(m, Fp8):
+        raise TwellError(f"{name}: expected an Fp8")
+    if m.block_rows not in (1, FP8_BLOCK):
+        raise TwellError(f"{name}.block_rows: {m.block_rows}, expected 1 or {FP8_BLOCK}")
+    if not isinstance(m.q, torch.Tensor) or m.q.dim() != 2:
+        raise TwellError(f"{name}.q: expected a [rows][cols up to 128] tensor")
+    rows = m.q.shape[0] if rows is None else rows
+    cols = m.cols if cols is None else cols
+    if m.cols != cols:
+        raise TwellError(f"{name}: {m.cols} columns, expected {cols}")
+    nb = -(-cols // FP8_BLOCK)
+    _req(m.q, f"{name}.q", (rows, nb * FP8_BLOCK), torch.float8_e4m3fn)
+    _req(m.scale, f"{name}.scale", (nb, -(-rows // m.block_rows)), torch.float32)
+
+
+def _mat(t, name, shape=None, dtype=None) -> MatC:
+    """A [rows][cols] float32 or bfloat16 tensor whose columns are
+    consecutive; its rows may be any stride apart (a slice of columns)."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise TwellError(f"{name}: expected a [rows][cols] tensor")
+    r, c = t.shape
+    if shape is not None and (r, c) != tuple(shape):
+        raise TwellError(f"{name}: shape {(r, c)}, expected {tuple(shape)}")
+    dt = _dt(t)
+    if dtype is not None and t.dtype != dtype:
+        raise TwellError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    ld, sc = t.stride()
+    if (sc != 1 and c > 1) or (r > 1 and ld < c):
+        raise TwellError(f"{name}: columns must be consecutive and rows must not overlap")
+    return MatC(r, c, max(ld, c) if r <= 1 else ld, dt, t.data_ptr())
+
+
+def _gain(gain, d):
+    if not isinstance(gain, torch.Tensor):
+        raise TwellError("gain: expected a tensor")
+    _req(gain, "gain", (d,), gain.dtype)
+    return _dt(gain)
+
+
+def rmsnorm_fwd(x, gain, residual=None, eps: float = 1e-6, out_dtype=torch.bfloat16, h=None,
+                out=None, timing: KernelTimer | None = None):
+    """h = residual + x and its root-mean-square norm n times gain; returns
+    (n, h). n is a tensor of out_dtype (float32 or bfloat16), or an Fp8 for
+    float8_e4m3fn; h has residual's dtype (without a residual h is x). h and
+    out, if given, are written (h may be residual or x, out may be x, in place)."""
+    mx = _mat(x, "x")
+    T, d = mx.rows, mx.cols
+    gdt = _gain(gain, d)
+    mr = mh = mn = m8 = None
+    if residual is not None:
+        mr = _mat(residual, "residual", (T, d))
+        if h is None:
+            h = torch.empty((T, d), dtype=residual.dtype, device=x.device)
+        mh = _mat(h, "h", (T, d), residual.dtype)
+    elif h is not None:
+        raise TwellError("h: written only with a residual")
+    if out_dtype == torch.float8_e4m3fn:
+        if out is None:
+            out = empty_fp8(T, d, 1, x.device)
+        else:
+            _check_fp8(out, "out", T, d)
+        m8 = out.c()
+        on = (("out.q", out.q), ("out.scale", out.scale))
+    else:
+        if out is None:
+            out = torch.empty((T, d), dtype=out_dtype, device=x.device)
+        mn = _mat(out, "out", (T, d), out_dtype)
+        on = (("out", out),)
+    dev = _on_gpu(("x", x), ("gain", gain), ("residual", residual), ("h", h), *on)
+    ref = ctypes.byref
+    _check(load().twell_rmsnorm_fwd(ref(mx), mr and ref(mr), _ptr(gain), gdt, eps,
+                                    mh and ref(mh), mn and ref(mn), m8 and ref(m8),
+                                    _timing(timing), _stream(dev)), "twell_rmsnorm_fwd")
+    return out, (x if residual is None else h)
+
+
+def rmsnorm_bwd_workspace_bytes(T, d) -> int:
+    return int(load().twell_rmsnorm_bwd_workspace_bytes(T, d))
+
+
+def rmsnorm_bwd(dn, h, gain, dres=None, eps: float = 1e-6, dh_dtype=torch.float32, dh=None,
+                dgain=None, workspace=None, timing: KernelTimer | None = None):
+    """Gradients of rmsnorm_fwd from dn: (dh, dgain). h is the stream the
+    forward normed (its h), dres the gradient reaching h past the norm."""
+    md = _mat(dn, "dn")
+    T, d = md.rows, md.cols
+    mh = _mat(h, "h", (T, d))
+    gdt = _gain(gain, d)
+    mr = None if dres is None else _mat(dres, "dres", (T, d))
+    if dh is None:
+        dh = torch.empty((T, d), dtype=dh_dtype, device=dn.device)
+    mo = _mat(dh, "dh", (T, d))
+    if dgain is None:
+        dgain = torch.empty(d, dtype=torch.float32, device=dn.device)
+    _req(dgain, "dgain", (d,), torch.float32)
+    dev = _on_gpu(("dn", dn), ("h", h), ("gain", gain), ("dres", dres), ("dh", dh),
+                  ("dgain", dgain), ("workspace", workspace))
+    workspace = _ws(workspace, rmsnorm_bwd_workspace_bytes(T, d), dev)
+    nbytes = 0 if workspace is None else workspace.numel()
+    ref = ctypes.byref
+    _check(load().twell_rmsnorm_bwd(ref(md), ref(mh), _ptr(gain), gdt, eps, mr and ref(mr),
+                                    ref(mo), _ptr(dgain), _ptr(workspace), nbytes,
+                                    _timing(timing), _stream(dev)), "twell_rmsnorm_bwd")
+    return dh, dgain
+
+
+def fp8_quant(x, block_rows: int = 1, layout: str = "rows", out: Fp8 | None = None,
+              out_t: Fp8 | None = None, timing: KernelTimer | None = None):
+    """x in 8 bits with block scales; returns (of x, of its transpose), None
+    for the one that layout ("rows", "cols" or "both") leaves out."""
+    mx = _mat(x, "x")
+    R, C = mx.rows, mx.cols
+    if layout not in ("rows", "cols", "both"):
+        raise TwellError(f"layout: {layout!r}, expected 'rows', 'cols' or 'both'")
+    if block_rows not in (1, FP8_BLOCK):
+        raise TwellError(f"block_rows: {block_rows}, expected 1 or {FP8_BLOCK}")
+    on = []
+    if layout == "cols":
+        if out is not None:
+            raise TwellError("out: not written with layout 'cols'")
+    elif out is None:
+        out = empty_fp8(R, C, block_rows, x.device)
+    if layout == "rows":
+        if out_t is not None:
+            raise TwellError("out_t: not written with layout 'rows'")
+    elif out_t is None:
+        out_t = empty_fp8(C, R, block_rows, x.device)
+    for name, m, shape in (("out", out, (R, C)), ("out_t", out_t, (C, R))):
+        if m is not None:
+            _check_fp8(m, name, *shape)
+            if m.block_rows != block_rows:
+                raise TwellError(f"{name}: block_rows {m.block_rows}, expected {block_rows}")
+            on += [(name + ".q", m.q), (name + ".scale", m.scale)]
+    dev = _on_gpu(("x", x), *on)
+    c, ct = (None if m is None else ctypes.byref(m.c()) for m in (out, out_t))
+    _check(load().twell_fp8_quant(ctypes.byref(mx), c, ct, _timing(timing), _stream(dev)),
+           "twell_fp8_quant")
+    return out, out_t
+
+
+def fp8_matmul_workspace_bytes(M, N, K) -> int:
+    return int(load().twell_fp8_matmul_workspace_bytes(M, N, K))
+
+
+def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=torch.bfloat16, fast_sums: bool = False,
+               workspace=None, timing: KernelTimer | None = None):
+    """out [a.rows][b.rows] = a b^T of two 8-bit matrices, out in float32 or
+    bfloat16. Products are added in float32, or, with fast_sums, by the 8-bit
+    matrix instruction at up to twice the rate (errors of about 2^-16 of the
+    sum of the terms' sizes: right for a bfloat16 result, short for float32)."""
+    _check_fp8(a, "a")
+    _check_fp8(b, "b")
+    M, N, K = a.rows, b.rows, a.cols
+    if b.cols != K:
+        raise TwellError(f"b: {b.cols} columns, a has {K}")
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.q.device)
+    mo = _mat(out, "out", (M, N), out_dtype)
+    dev = _on_gpu(("a.q", a.q), ("a.scale", a.scale), ("b.q", b.q), ("b.scale", b.scale),
+                  ("out", out), ("workspace", workspace))
+    workspace = _ws(workspace, fp8_matmul_workspace_bytes(M, N, K), dev)
+    nbytes = 0 if workspace is None else workspace.numel()
+    ref = ctypes.byref
+    _check(load().twell_fp8_matmul(ref(a.c()), ref(b.c()), ref(mo),
+                                   SUMS_FP8 if fast_sums else SUMS_F32, _ptr(workspace), nbytes,
+                                   _timing(timing), _stream(dev)), "twell_fp8_matmul")
     return out

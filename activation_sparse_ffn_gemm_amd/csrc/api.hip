@@ -27,6 +27,19 @@ hipError_t launch_dec_layer(twell_dtype dt, const void *x, const void *wg_t, con
                             const void *wd, int dm, const twell_t *o, float *y, void *ws,
                             int32_t *status, twell_timing_t *timing, hipStream_t s);
 
+hipError_t launch_rmsnorm_fwd(const twell_mat_t *x, const twell_mat_t *res, const void *gain,
+                              int dtg, float eps, const twell_mat_t *h, const twell_mat_t *n,
+                              const twell_fp8_t *n8, twell_timing_t *timing, hipStream_t s);
+size_t rmsnorm_bwd_workspace(int T, int d);
+hipError_t launch_rmsnorm_bwd(const twell_mat_t *dn, const twell_mat_t *h, const void *gain,
+                              int dtg, float eps, const twell_mat_t *dres, const twell_mat_t *dh,
+                              float *dgain, void *ws, twell_timing_t *timing, hipStream_t s);
+hipError_t launch_fp8_quant(const twell_mat_t *x, const twell_fp8_t *o, const twell_fp8_t *ot,
+                            twell_timing_t *timing, hipStream_t s);
+size_t fp8_mm_workspace(int M, int N, int K);
+hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out,
+                         int sums, void *ws, twell_timing_t *timing, hipStream_t s);
+
 namespace {
 
 bool a16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -95,6 +108,46 @@ int check_hybrid(const hybrid_t *h, twell_dtype dt)
 }
 
 int hip_rc(hipError_t e) { return e == hipSuccess ? TWELL_OK : TWELL_E_HIP; }
+
+bool aligned(const void *p, uintptr_t n) { return (uintptr_t)p % n == 0; }
+bool aligned_dt(const void *p, int dt) { return aligned(p, dt == TWELL_BF16 ? 2 : 4); }
+
+// a matrix of rows x cols
+int check_mat(const twell_mat_t *m, int32_t rows, int32_t cols)
+{
+    if (!dtype_ok(m->dtype))
+        return TWELL_E_DTYPE;
+    if (m->rows != rows || m->cols != cols || (rows > 1 && m->ld < cols) || m->ld < 0 ||
+        m->ld > ((int64_t)1 << 31))
+        return TWELL_E_SHAPE;
+    if (rows > 0 && cols > 0 && !m->data)
+        return TWELL_E_NULL;
+    return aligned_dt(m->data, m->dtype) ? TWELL_OK : TWELL_E_ALIGN;
+}
+
+int check_fp8(const twell_fp8_t *m)
+{
+    if (m->rows < 0 || m->rows > TWELL_MAX_ROWS || m->cols < 0 || m->cols > TWELL_MAX_ROWS ||
+        (m->block_rows != 1 && m->block_rows != TWELL_FP8_BLOCK))
+        return TWELL_E_SHAPE;
+    if (m->rows > 0 && m->cols > 0 && (!m->q || !m->scale))
+        return TWELL_E_NULL;
+    return a16(m->q) && aligned(m->scale, 4) ? TWELL_OK : TWELL_E_ALIGN;
+}
+
+bool eps_ok(float eps) { return eps >= 0.f && eps <= 3.4e38f; }
+
+// rows and columns of the norm
+bool norm_sizes_ok(int32_t rows, int32_t cols)
+{
+    return rows >= 0 && rows <= TWELL_MAX_ROWS && cols >= 1 && cols <= TWELL_NORM_COLS;
+}
+
+// 128 x 128 (or finer) tiles of a launch are numbered in 31 bits
+bool tiles_ok(int64_t rows, int64_t cols, int64_t tr, int64_t tc)
+{
+    return ((rows + tr - 1) / tr) * ((cols + tc - 1) / tc) <= INT32_MAX;
+}
 
 } // namespace
 
@@ -319,6 +372,124 @@ int hybrid_ffn_bwd(twell_dtype dt, const void *x, const void *dy, const hybrid_t
         return TWELL_E_SHAPE;
     return hip_rc(launch_bwd(dt, x, dy, h, wg_t, wu_t, wd, d_model, l1, dx, dwg_t, dwu_t, dwd,
                              workspace, dev_status, timing, (hipStream_t)stream));
+}
+
+int twell_rmsnorm_fwd(const twell_mat_t *x, const twell_mat_t *residual, const void *gain,
+                      twell_dtype gain_dtype, float eps, const twell_mat_t *h,
+                      const twell_mat_t *n, const twell_fp8_t *n8, twell_timing_t *timing,
+                      void *stream)
+{
+    if (!x || !gain || (residual && !h) || (!n && !n8))
+        return TWELL_E_NULL;
+    if (!dtype_ok(gain_dtype))
+        return TWELL_E_DTYPE;
+    if (!norm_sizes_ok(x->rows, x->cols) || (h && !residual) || (n && n8) || !eps_ok(eps))
+        return TWELL_E_SHAPE;
+    const int32_t T = x->rows, d = x->cols;
+    for (const twell_mat_t *m : {x, residual, h, n})
+        if (m)
+            if (int rc = check_mat(m, T, d))
+                return rc;
+    if (residual && h->dtype != residual->dtype)
+        return TWELL_E_DTYPE;
+    if (n8) {
+        if (n8->rows != T || n8->cols != d || n8->block_rows != 1)
+            return TWELL_E_SHAPE;
+        if (int rc = check_fp8(n8))
+            return rc;
+    }
+    if (!aligned_dt(gain, gain_dtype))
+        return TWELL_E_ALIGN;
+    if (T == 0)
+        return TWELL_OK;
+    return hip_rc(launch_rmsnorm_fwd(x, residual, gain, gain_dtype, eps, h, n, n8, timing,
+                                     (hipStream_t)stream));
+}
+
+size_t twell_rmsnorm_bwd_workspace_bytes(int32_t rows, int32_t cols)
+{
+    return norm_sizes_ok(rows, cols) ? rmsnorm_bwd_workspace(rows, cols) : 0;
+}
+
+int twell_rmsnorm_bwd(const twell_mat_t *dn, const twell_mat_t *h, const void *gain,
+                      twell_dtype gain_dtype, float eps, const twell_mat_t *dres,
+                      const twell_mat_t *dh, float *dgain, void *workspace,
+                      size_t workspace_bytes, twell_timing_t *timing, void *stream)
+{
+    if (!dn || !h || !gain || !dh || !dgain)
+        return TWELL_E_NULL;
+    if (!dtype_ok(gain_dtype))
+        return TWELL_E_DTYPE;
+    if (!norm_sizes_ok(dn->rows, dn->cols) || !eps_ok(eps))
+        return TWELL_E_SHAPE;
+    const int32_t T = dn->rows, d = dn->cols;
+    for (const twell_mat_t *m : {dn, h, dres, dh})
+        if (m)
+            if (int rc = check_mat(m, T, d))
+                return rc;
+    if (!aligned_dt(gain, gain_dtype) || !aligned(dgain, 4) || !a16(workspace))
+        return TWELL_E_ALIGN;
+    const size_t need = twell_rmsnorm_bwd_workspace_bytes(T, d);
+    if (workspace_bytes < need || (need && !workspace))
+        return TWELL_E_WORKSPACE;
+    return hip_rc(launch_rmsnorm_bwd(dn, h, gain, gain_dtype, eps, dres, dh, dgain, workspace,
+                                     timing, (hipStream_t)stream));
+}
+
+int twell_fp8_quant(const twell_mat_t *x, const twell_fp8_t *out, const twell_fp8_t *out_t,
+                    twell_timing_t *timing, void *stream)
+{
+    if (!x || (!out && !out_t))
+        return TWELL_E_NULL;
+    if (x->rows < 0 || x->rows > TWELL_MAX_ROWS || x->cols < 0 || x->cols > TWELL_MAX_ROWS)
+        return TWELL_E_SHAPE;
+    const int32_t R = x->rows, C = x->cols;
+    if (int rc = check_mat(x, R, C))
+        return rc;
+    if ((out && (out->rows != R || out->cols != C)) ||
+        (out_t && (out_t->rows != C || out_t->cols != R)) ||
+        (out && out_t && out->block_rows != out_t->block_rows) ||
+        !tiles_ok(R, C, TWELL_FP8_BLOCK, TWELL_FP8_BLOCK))
+        return TWELL_E_SHAPE;
+    for (const twell_fp8_t *m : {out, out_t})
+        if (m)
+            if (int rc = check_fp8(m))
+                return rc;
+    if (R == 0 || C == 0)
+        return TWELL_OK;
+    return hip_rc(launch_fp8_quant(x, out, out_t, timing, (hipStream_t)stream));
+}
+
+size_t twell_fp8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K)
+{
+    if (M < 0 || M > TWELL_MAX_ROWS || N < 0 || N > TWELL_MAX_ROWS || K < 0 ||
+        K > TWELL_MAX_ROWS || !tiles_ok(M, N, 16, 16))
+        return 0;
+    return fp8_mm_workspace(M, N, K);
+}
+
+int twell_fp8_matmul(const twell_fp8_t *a, const twell_fp8_t *b, const twell_mat_t *out,
+                     int32_t sums, void *workspace, size_t workspace_bytes, twell_timing_t *timing,
+                     void *stream)
+{
+    if (!a || !b || !out)
+        return TWELL_E_NULL;
+    for (const twell_fp8_t *m : {a, b})
+        if (int rc = check_fp8(m))
+            return rc;
+    if (a->cols != b->cols || !tiles_ok(a->rows, b->rows, 16, 16) ||
+        (sums != TWELL_SUMS_F32 && sums != TWELL_SUMS_FP8))
+        return TWELL_E_SHAPE;
+    if (int rc = check_mat(out, a->rows, b->rows))
+        return rc;
+    if (!a16(workspace))
+        return TWELL_E_ALIGN;
+    const size_t need = twell_fp8_matmul_workspace_bytes(a->rows, b->rows, a->cols);
+    if (workspace_bytes < need || (need && !workspace))
+        return TWELL_E_WORKSPACE;
+    if (a->rows == 0 || b->rows == 0)
+        return TWELL_OK;
+    return hip_rc(launch_fp8_mm(a, b, out, sums, workspace, timing, (hipStream_t)stream));
 }
 
 } // extern "C"

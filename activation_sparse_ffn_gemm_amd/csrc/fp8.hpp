@@ -1,0 +1,214 @@
+// Device helpers of the 8-bit (e4m3) matrices and of the row-wise kernels
+// that write them: rows of any length and alignment in float32 or bfloat16,
+// held in registers as chunks of eight elements per lane.
+#pragma once
+
+#include "common.hpp"
+
+// twell_fp8_t: a scale for each FP8_BLK columns; |q| <= FP8_MAX (the largest
+// finite e4m3 value); amax is taken as at least FP8_AMAX_MIN, so a block of
+// zeros has a positive scale and no scale is denormal.
+constexpr int FP8_BLK = TWELL_FP8_BLOCK;
+constexpr float FP8_MAX = 448.f;
+constexpr float FP8_AMAX_MIN = 0x1p-64f;
+
+__host__ __device__ inline int fp8_blocks(int cols) { return (int)(((int64_t)cols + FP8_BLK - 1) / FP8_BLK); }
+__host__ __device__ inline int64_t fp8_pitch(int cols) { return (int64_t)fp8_blocks(cols) * FP8_BLK; }
+
+// Four values to four e4m3 bytes, nearest, ties to even (low byte first).
+DEVI uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d)
+{
+    int r = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, r, true);
+}
+
+// Maximum over each group of 16 lanes, in every lane of the group (DPP moves
+// within the 16-lane rows, as in wave_sum). Used on the bits of absolute
+// values: as integers these order like the floats, with infinity above every
+// finite value and NaN above infinity, so a NaN in a block reaches its scale.
+DEVI uint32_t row16_umax(uint32_t v)
+{
+    auto step = [&](uint32_t o) { v = o > v ? o : v; };
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));
+    return v;
+}
+DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Scale of a block from the bits of its largest absolute value.
+DEVI float fp8_scale(uint32_t amax_bits)
+{
+    const uint32_t floor_bits = __float_as_uint(FP8_AMAX_MIN);
+    return __uint_as_float(amax_bits > floor_bits ? amax_bits : floor_bits) / FP8_MAX;
+}
+
+// v / s rounded to float32 as a division rounds it, from inv = 1 / s: the
+// product's error is one fused step away (v - q s is exact in the fused
+// multiply-add), three instructions in place of a division's ten. s is a
+// block's scale and |v| <= 448 s up to rounding, so nothing overflows; where
+// s is infinite or NaN the results are NaN, as the quotients of the block's
+// own largest values are.
+DEVI float div_by_scale(float v, float s, float inv)
+{
+    const float q = v * inv;
+    return fmaf(fmaf(-q, s, v), inv, q);
+}
+
+// Eight values of one block -> eight bytes.
+DEVI uint2 quant8(const float *v, float s, float inv)
+{
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        q[i] = div_by_scale(v[i], s, inv);
+    return make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
+                      f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
+}
+
+// ---- rows of any alignment
+// 16 bytes at an address that is only element-aligned: gfx950 takes unaligned
+// vector accesses, so one instruction serves every row stride.
+struct __attribute__((packed, aligned(2), may_alias)) bytes16 {
+    uint32_t x, y, z, w;
+};
+DEVI uint4 ldg16u(const void *p)
+{
+    const bytes16 v = *(const bytes16 *)p;
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+DEVI void stg16u(void *p, uint4 v)
+{
+    *(bytes16 *)p = bytes16{v.x, v.y, v.z, v.w};
+}
+
+// A row of d elements spread over LPR lanes: lane l holds elements
+// 8 (l + LPR c) .. + 7 for c < C, zeros past d. Loads leave the raw bits in
+// the registers (bf16: the first four words), so that the loads of several
+// arrays are in flight together; widen() makes them floats in place.
+template <int LPR, int C> struct Row {
+    float v[C][8];
+
+    DEVI void put(int c, int i, uint4 q)
+    {
+        v[c][i] = __uint_as_float(q.x), v[c][i + 1] = __uint_as_float(q.y);
+        v[c][i + 2] = __uint_as_float(q.z), v[c][i + 3] = __uint_as_float(q.w);
+    }
+    DEVI uint4 bits(int c, int i) const
+    {
+        return make_uint4(__float_as_uint(v[c][i]), __float_as_uint(v[c][i + 1]),
+                          __float_as_uint(v[c][i + 2]), __float_as_uint(v[c][i + 3]));
+    }
+
+    DEVI void load(const void *row, int dt, int d, int lane)
+    {
+        if (dt == TWELL_BF16) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int j = 8 * (lane + LPR * c);
+                uint4 q = make_uint4(0, 0, 0, 0);
+                if (j + 8 <= d)
+                    q = ldg16u((const uint16_t *)row + j);
+                put(c, 0, q);
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int j = 8 * (lane + LPR * c);
+                uint4 q = make_uint4(0, 0, 0, 0), r = q;
+                if (j + 8 <= d) {
+                    q = ldg16u((const float *)row + j);
+                    r = ldg16u((const float *)row + j + 4);
+                }
+                put(c, 0, q);
+                put(c, 4, r);
+            }
+        }
+    }
+
+    // Floats from the raw bits; the last d % 8 elements, which no whole chunk
+    // covers, are read here, one by one.
+    DEVI void widen(const void *row, int dt, int d, int lane)
+    {
+        if (dt == TWELL_BF16) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint4 q = bits(c, 0);
+                elem<TWELL_BF16>::widen(q, v[c]);
+            }
+        }
+        if (d & 7) {
+            const int n = d >> 3, ct = n / LPR; // the chunk that ends past d
+            if (lane == n % LPR) {
+                float t[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    t[i] = i >= (d & 7)       ? 0.f
+                           : dt == TWELL_BF16 ? elem<TWELL_BF16>::load1(row, 8 * n + i)
+                                              : elem<TWELL_F32>::load1(row, 8 * n + i);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (c == ct) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            v[c][i] = t[i];
+                    }
+            }
+        }
+    }
+
+    // bf16: rounded to nearest, ties to even
+    DEVI void store(void *row, int dt, int d, int lane) const
+    {
+        if (dt == TWELL_BF16) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int j = 8 * (lane + LPR * c);
+                if (j + 8 <= d)
+                    stg16u((uint16_t *)row + j,
+                           make_uint4(f32x2_to_bf16x2(v[c][0], v[c][1]),
+                                      f32x2_to_bf16x2(v[c][2], v[c][3]),
+                                      f32x2_to_bf16x2(v[c][4], v[c][5]),
+                                      f32x2_to_bf16x2(v[c][6], v[c][7])));
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int j = 8 * (lane + LPR * c);
+                if (j + 8 <= d) {
+                    stg16u((float *)row + j, bits(c, 0));
+                    stg16u((float *)row + j + 4, bits(c, 4));
+                }
+            }
+        }
+        if (d & 7) {
+            const int n = d >> 3, ct = n / LPR;
+            if (lane == n % LPR) {
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    if (c == ct) {
+#pragma unroll
+                        for (int i = 0; i < 7; ++i)
+                            if (i < (d & 7)) {
+                                if (dt == TWELL_BF16)
+                                    ((uint16_t *)row)[8 * n + i] =
+                                        (uint16_t)f32x2_to_bf16x2(v[c][i], 0.f);
+                                else
+                                    ((float *)row)[8 * n + i] = v[c][i];
+                            }
+                    }
+            }
+        }
+    }
+};
+
+// Element address of row r of a matrix of leading dimension ld.
+DEVI const void *row_ptr(const void *p, int dt, int64_t ld, int64_t r)
+{
+    return (const uint8_t *)p + r * ld * (dt == TWELL_BF16 ? 2 : 4);
+}
+DEVI void *row_ptr(void *p, int dt, int64_t ld, int64_t r)
+{
+    return (uint8_t *)p + r * ld * (dt == TWELL_BF16 ? 2 : 4);
+}
