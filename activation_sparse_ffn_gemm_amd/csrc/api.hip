@@ -462,8 +462,8 @@ int twell_fp8_quant(const twell_mat_t *x, const twell_fp8_t *out, const twell_fp
 
 size_t twell_fp8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K)
 {
-    if (M < 0 || M > TWELL_MAX_ROWS || N < 0 || N > TWELL_MAX_ROWS || K < 0 ||
-        K > TWELL_MAX_ROWS || !tiles_ok(M, N, 16, 16))
+    if (M < 0 || M > TWELL_MAX_ROWS || N < 0 || N > TWELL_MAX_ROWS || K < 0 || K > TWELL_MAX_K ||
+        !tiles_ok(M, N, 16, 16))
         return 0;
     return fp8_mm_workspace(M, N, K);
 }
@@ -477,7 +477,7 @@ int twell_fp8_matmul(const twell_fp8_t *a, const twell_fp8_t *b, const twell_mat
     for (const twell_fp8_t *m : {a, b})
         if (int rc = check_fp8(m))
             return rc;
-    if (a->cols != b->cols || !tiles_ok(a->rows, b->rows, 16, 16) ||
+    if (a->cols != b->cols || a->cols > TWELL_MAX_K || !tiles_ok(a->rows, b->rows, 16, 16) ||
         (sums != TWELL_SUMS_F32 && sums != TWELL_SUMS_FP8))
         return TWELL_E_SHAPE;
     if (int rc = check_mat(out, a->rows, b->rows))

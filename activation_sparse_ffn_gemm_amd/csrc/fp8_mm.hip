@@ -19,6 +19,7 @@
 // consecutive n. Which k a lane's 32 bytes are does not matter as long as
 // both operands agree, so each lane takes 32 consecutive bytes of its row.
 #include "fp8.hpp"
+#include "ntgemm.hpp"
 
 namespace {
 
@@ -32,6 +33,8 @@ struct MmArgs {
     int M, N, nkb, dto;
     int ra, rb;   // rows of a scale block (1 or 128) of A and of B
     int nsa, nsb; // scales per block of k
+    float *part;  // split contraction: [parts][M][N] float32 partial sums
+    int parts, per; // parts, blocks of k in each
 };
 
 DEVI intx8_t frag32(const uint8_t *p)
@@ -70,6 +73,225 @@ template <int SUMS> DEVI floatx4_t block_sum(intx8_t a, intx8_t b)
     return SUMS == TWELL_SUMS_FP8 ? mfma_e4m3(a, b) : mfma_wide(a, b);
 }
 
+// ---------------------------------------------------------------- large products
+// One workgroup computes BM tokens x BN n. A block of 128 k is one step: its
+// 128-byte rows of both operands, and their scales, go straight from global
+// memory to LDS (NST steps resident), each row's 16-byte chunks XOR-swizzled so
+// that the 16 rows a fragment read touches lie on distinct banks; a wave reads
+// WN x WM of it as 16-row fragments of 32 bytes a lane.
+template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
+    static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
+    static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 16, NI = WN / 16;
+    static constexpr int ROWS = BM + BN;                 // B rows first, then A rows
+    static constexpr int WB = ROWS / 8 / NWV;            // 1 KB loads (eight rows) per wave
+    static constexpr int WS = ROWS / 64 / NWV;           // 64-scale loads per wave
+    static constexpr int SCALES = ROWS * FP8_BLK;        // byte offset of a stage's scales
+    static constexpr int STAGE = SCALES + ROWS * 4;
+    static constexpr int OUTB = WM * (WN * 2 + 16) * NWV; // the epilogue's bf16 rows
+    static constexpr int LDS = NST * STAGE > OUTB ? NST * STAGE : OUTB;
+    static_assert(ROWS % (64 * NWV) == 0 && BN % (8 * WB) == 0 && BN % 64 == 0, "whole loads");
+    static_assert(WN <= FP8_BLK && FP8_BLK % WN == 0, "a wave's n share one 128-row scale block");
+    static_assert((NST - 1) * (WB + WS) < 64, "loads in flight must fit the vmcnt counter");
+};
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// Lane l's 16 (4) bytes at base + off go to LDS byte lds + 16 l (4 l). As
+// assembly for the reason given at ng::lds_dma16.
+DEVI void dma16(const uint8_t *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "m0");
+}
+DEVI void dma4(const float *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(lds)
+                 : "m0");
+}
+#pragma clang diagnostic pop
+
+// BLKB: B's scale block is 128 rows, so a wave's n share one scale per step.
+template <class C, int SUMS, bool BLKB>
+__global__ __launch_bounds__(C::NT, 1) void fp8_mm_tile_kernel(MmArgs a)
+{
+    __shared__ __attribute__((aligned(16))) uint8_t L[C::LDS];
+    // XCD-aware order: XCD k takes the k-th contiguous run of a grouped tile
+    // order (GM token tiles x all n tiles per group, token tile fastest)
+    constexpr int GM = 8;
+    const int n_nt = (a.N + C::BN - 1) / C::BN, n_mt = (a.M + C::BM - 1) / C::BM;
+    const int64_t total = (int64_t)n_nt * n_mt * a.parts;
+    const int64_t per = (total + NXCD - 1) / NXCD;
+    const int64_t q0 = (blockIdx.x % NXCD) * per + blockIdx.x / NXCD;
+    if (blockIdx.x / NXCD >= per || q0 >= total)
+        return;
+    const int part = (int)(q0 / ((int64_t)n_nt * n_mt));
+    const int q = (int)(q0 % ((int64_t)n_nt * n_mt));
+    const int64_t gsz = (int64_t)GM * n_nt;
+    const int grp = (int)(q / gsz), grows = min(GM, n_mt - grp * GM), gr = (int)(q % gsz);
+    const int m0 = (grp * GM + gr % grows) * C::BM, n0 = gr / grows * C::BN;
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const int wm = w / C::WGN, wn = w % C::WGN, l16 = lane & 15, q4 = lane >> 4;
+    const int kb0 = part * a.per, kb1 = min(a.nkb, kb0 + a.per);
+
+    // this wave's loads: eight rows of one operand each, lane l byte 16 l of
+    // the 1 KB, i.e. the chunk that the swizzle puts there. Rows past an
+    // operand read its last row (their outputs are dropped).
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(ng::lds_u8 *)L;
+    const bool isb = w * C::WB * 8 < C::BN;
+    const uint8_t *src = isb ? a.qb + (int64_t)n0 * a.pitch : a.qa + (int64_t)m0 * a.pitch;
+    const int last = isb ? a.N - 1 - n0 : a.M - 1 - m0;
+    uint32_t off[C::WB];
+#pragma unroll
+    for (int i = 0; i < C::WB; ++i) {
+        const int r = (w * C::WB + i) * 8 + lane / 8 - (isb ? 0 : C::BN);
+        const int chunk = (lane & 7) ^ ((r >> 1) & 7);
+        off[i] = (uint32_t)min(r, last) * (uint32_t)a.pitch + chunk * 16;
+    }
+    const bool sisb = w * C::WS * 64 < C::BN;
+    const float *ssrc = sisb ? a.sb : a.sa;
+    const int ns = sisb ? a.nsb : a.nsa;
+    uint32_t soff[C::WS];
+#pragma unroll
+    for (int i = 0; i < C::WS; ++i) {
+        const int r = (w * C::WS + i) * 64 + lane - (sisb ? 0 : C::BN);
+        const int row = sisb ? min(n0 + r, a.N - 1) : min(m0 + r, a.M - 1);
+        soff[i] = (uint32_t)(row / (sisb ? a.rb : a.ra)) * 4u;
+    }
+    auto issue = [&](int kb) {
+        const uint32_t dst = lds0 + (uint32_t)((kb - kb0) % C::NST) * C::STAGE;
+        const uint8_t *p = src + (int64_t)kb * FP8_BLK;
+        const float *ps = ssrc + (int64_t)kb * ns;
+#pragma unroll
+        for (int i = 0; i < C::WB; ++i)
+            dma16(p, off[i], dst + (w * C::WB + i) * 1024);
+#pragma unroll
+        for (int i = 0; i < C::WS; ++i)
+            dma4(ps, soff[i], dst + C::SCALES + (w * C::WS + i) * 256);
+    };
+
+    floatx4_t acc[C::NI][C::MI];
+#pragma unroll
+    for (int i = 0; i < C::NI; ++i)
+#pragma unroll
+        for (int j = 0; j < C::MI; ++j)
+            acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    // byte of this lane's two chunks (q4 and q4 + 4) in a 16-row fragment
+    const int f0 = l16 * FP8_BLK + ((q4 ^ ((l16 >> 1) & 7)) << 4), f1 = f0 ^ 64;
+    auto frag = [&](const uint8_t *p) {
+        const uint4 u = *(const uint4 *)(p + f0), v = *(const uint4 *)(p + f1);
+        return intx8_t{(int)u.x, (int)u.y, (int)u.z, (int)u.w,
+                       (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+    };
+#pragma unroll
+    for (int s = 0; s < C::NST - 1; ++s)
+        if (kb0 + s < kb1)
+            issue(kb0 + s);
+    for (int kb = kb0; kb < kb1; ++kb) {
+        // this wave's loads of the step are in once at most the later steps' pend
+        ng::wait_vm_steps<C::WB + C::WS, C::NST - 2>(min(kb1 - 1, kb + C::NST - 2) - kb);
+        __syncthreads(); // every wave's loads are in, and the last step is consumed
+        if (kb + C::NST - 1 < kb1)
+            issue(kb + C::NST - 1);
+        const uint8_t *S = L + (kb - kb0) % C::NST * C::STAGE;
+        const uint8_t *Bs = S + wn * C::WN * FP8_BLK, *As = S + (C::BN + wm * C::WM) * FP8_BLK;
+        const float *sbs = (const float *)(S + C::SCALES) + wn * C::WN;
+        const float *sas = (const float *)(S + C::SCALES) + C::BN + wm * C::WM;
+        intx8_t fa[C::MI];
+        float sa[C::MI];
+#pragma unroll
+        for (int j = 0; j < C::MI; ++j) {
+            fa[j] = frag(As + j * 16 * FP8_BLK);
+            sa[j] = sas[j * 16 + l16];
+        }
+        if (BLKB) {
+            const float sb = sbs[0];
+#pragma unroll
+            for (int j = 0; j < C::MI; ++j)
+                sa[j] *= sb;
+        }
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) {
+            const intx8_t fb = frag(Bs + i * 16 * FP8_BLK);
+            floatx4_t sb4 = {1.f, 1.f, 1.f, 1.f};
+            if (!BLKB)
+                sb4 = *(const floatx4_t *)(sbs + i * 16 + q4 * 4);
+#pragma unroll
+            for (int j = 0; j < C::MI; ++j) {
+                const floatx4_t p = block_sum<SUMS>(fb, fa[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = fmaf(p[e], BLKB ? sa[j] : sa[j] * sb4[e], acc[i][j][e]);
+            }
+        }
+    }
+    // ---- epilogue: lane's element e of tile (i, j) is token j * 16 + l16,
+    // n i * 16 + q4 * 4 + e of the wave's part
+    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN;
+    if (a.parts > 1 || a.dto == TWELL_F32) {
+        float *out = a.parts > 1 ? a.part + (int64_t)part * a.M * a.N : (float *)a.out;
+        const int64_t ld = a.parts > 1 ? a.N : a.ldo;
+#pragma unroll
+        for (int j = 0; j < C::MI; ++j) {
+            const int m = mw + j * 16 + l16;
+            if (m >= a.M)
+                continue;
+            float *row = out + m * ld;
+#pragma unroll
+            for (int i = 0; i < C::NI; ++i) {
+                const int n = nw + i * 16 + q4 * 4;
+                const floatx4_t v = acc[i][j];
+                if (n + 4 <= a.N) {
+                    stg16u(row + n, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                               __float_as_uint(v[2]), __float_as_uint(v[3])));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < a.N)
+                            row[n + e] = v[e];
+                }
+            }
+        }
+        return;
+    }
+    // bf16: the wave's rows through its own piece of LDS, so that a store
+    // instruction writes whole rows of WN values
+    __syncthreads(); // every wave is done with the stages
+    constexpr int RB = C::WN * 2 + 16; // padded row: 16 rows start on 16 distinct banks
+    uint8_t *buf = L + w * C::WM * RB;
+#pragma unroll
+    for (int j = 0; j < C::MI; ++j)
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i)
+            *(uint2 *)(buf + (j * 16 + l16) * RB + (i * 16 + q4 * 4) * 2) =
+                make_uint2(f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]),
+                           f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]));
+    constexpr int LPR = C::WN / 8; // lanes of a row, eight values each
+    const int c8 = lane % LPR, rr = lane / LPR, n = nw + c8 * 8;
+#pragma unroll
+    for (int r0 = 0; r0 < C::WM; r0 += 64 / LPR) {
+        const int m = mw + r0 + rr;
+        const uint4 v = *(const uint4 *)(buf + (r0 + rr) * RB + c8 * 16);
+        if (m >= a.M || n >= a.N)
+            continue;
+        uint16_t *row = (uint16_t *)a.out + m * a.ldo;
+        if (n + 8 <= a.N) {
+            stg16u(row + n, v);
+        } else {
+            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n + e < a.N)
+                    row[n + e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- few tokens
 constexpr int WV = 8; // waves of a workgroup: each takes every eighth block of k
 
 // TB tiles of 16 tokens by 16 n per workgroup.
@@ -151,6 +373,31 @@ template <int SUMS> void launch_rows(const MmArgs &a, hipStream_t s)
         fp8_mm_rows_kernel<4, SUMS><<<grid, 64 * WV, 0, s>>>(a);
 }
 
+using T256 = TileCfg<256, 256, 4, 2, 2>; // waves of 64 tokens x 128 n
+using T128 = TileCfg<128, 128, 2, 2, 2>; // waves of 64 x 64
+
+template <class C, int SUMS> void launch_tile(const MmArgs &a, hipStream_t s)
+{
+    const int64_t total = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.M + C::BM - 1) / C::BM) *
+                          a.parts;
+    const dim3 grid((uint32_t)((total + NXCD - 1) / NXCD * NXCD));
+    if (a.rb == FP8_BLK)
+        fp8_mm_tile_kernel<C, SUMS, true><<<grid, C::NT, 0, s>>>(a);
+    else
+        fp8_mm_tile_kernel<C, SUMS, false><<<grid, C::NT, 0, s>>>(a);
+}
+
+template <int SUMS> void launch_sums(const MmArgs &a, hipStream_t s)
+{
+    const int64_t t256 = (int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256);
+    if (a.M <= 64)
+        launch_rows<SUMS>(a, s);
+    else if (t256 >= 128)
+        launch_tile<T256, SUMS>(a, s);
+    else
+        launch_tile<T128, SUMS>(a, s);
+}
+
 } // namespace
 
 size_t fp8_mm_workspace(int M, int N, int K) { return 0; }
@@ -166,10 +413,11 @@ hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell
     a.ra = A->block_rows, a.rb = B->block_rows;
     a.nsa = (a.M + a.ra - 1) / a.ra, a.nsb = (a.N + a.rb - 1) / a.rb;
     Timer tm(timing, s);
+    a.parts = 1, a.per = a.nkb;
     if (sums == TWELL_SUMS_FP8)
-        launch_rows<TWELL_SUMS_FP8>(a, s);
+        launch_sums<TWELL_SUMS_FP8>(a, s);
     else
-        launch_rows<TWELL_SUMS_F32>(a, s);
-    tm.mark("fp8_mm_rows");
+        launch_sums<TWELL_SUMS_F32>(a, s);
+    tm.mark("fp8_mm");
     return hipGetLastError();
 }

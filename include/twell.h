@@ -322,6 +322,7 @@ typedef struct {
 } twell_mat_t;
 
 #define TWELL_FP8_BLOCK 128   /* columns that share a scale */
+#define TWELL_MAX_K (1 << 24) /* longest contraction of twell_fp8_matmul */
 #define TWELL_NORM_COLS 16384 /* widest row the norm takes (it stays in registers) */
 
 /*
@@ -410,7 +411,7 @@ int twell_fp8_quant(const twell_mat_t *x, const twell_fp8_t *out, const twell_fp
  * For a layer y = x W^T
  * with x [T][K] and W [N][K]:
  *   y = (x, W),  dx = (dy, W transposed),  dW = (dy transposed, x transposed)
- * on the matrices twell_fp8_quant makes.
+ * on the matrices twell_fp8_quant makes. a.cols = b.cols <= TWELL_MAX_K.
  *   workspace: at least twell_fp8_matmul_workspace_bytes(...) bytes, 0 (and
  *   workspace may be NULL) where the contraction is not split.
  * Errors: NULL / SHAPE / DTYPE / ALIGN / WORKSPACE / HIP.
