@@ -59,65 +59,93 @@ DEVI bf16x8_t widen8(int lo, int hi)
     p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, true);
     return bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
-DEVI floatx4_t mfma_wide(intx8_t a, intx8_t b)
-{
-    floatx4_t c = {0.f, 0.f, 0.f, 0.f};
+// A 16-row fragment of one block of k, and the block's sums of two of them.
+template <int SUMS> struct Frag;
+template <> struct Frag<TWELL_SUMS_FP8> {
+    intx8_t v;
+    DEVI void set(intx8_t x) { v = x; }
+    DEVI static floatx4_t mul(const Frag &a, const Frag &b) { return mfma_e4m3(a.v, b.v); }
+};
+template <> struct Frag<TWELL_SUMS_F32> {
+    bf16x8_t v[4];
+    DEVI void set(intx8_t x)
+    {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2)
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(a[i], a[i + 1]), widen8(b[i], b[i + 1]),
-                                                    c, 0, 0, 0);
-    return c;
-}
-template <int SUMS> DEVI floatx4_t block_sum(intx8_t a, intx8_t b)
-{
-    return SUMS == TWELL_SUMS_FP8 ? mfma_e4m3(a, b) : mfma_wide(a, b);
-}
+        for (int i = 0; i < 4; ++i)
+            v[i] = widen8(x[2 * i], x[2 * i + 1]);
+    }
+    DEVI static floatx4_t mul(const Frag &a, const Frag &b)
+    {
+        floatx4_t c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], c, 0, 0, 0);
+        return c;
+    }
+};
 
 // ---------------------------------------------------------------- large products
 // One workgroup computes BM tokens x BN n. A block of 128 k is one step: its
 // 128-byte rows of both operands, and their scales, go straight from global
-// memory to LDS (NST steps resident), each row's 16-byte chunks XOR-swizzled so
-// that the 16 rows a fragment read touches lie on distinct banks; a wave reads
-// WN x WM of it as 16-row fragments of 32 bytes a lane.
-template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
-    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
+// memory to LDS, two steps resident, each row's 16-byte chunks XOR-swizzled so
+// that the 16 rows a fragment read touches lie on distinct banks. A wave owns
+// WN x WM of the tile: NI fragments of B rows by MI of A rows, 32 bytes a lane.
+//
+// The order within a step is written out (a scheduling barrier after every
+// matrix product), because the two waves of a SIMD have little else to hide
+// behind each other:
+// - A fragment of B is read one row of products before its own.
+// - A product's four results are scaled into the accumulators three products
+//   later, when they have left the matrix unit.
+// - The next step's loads go out one by one beside the step's first products,
+//   into the stage that the step before has left.
+// - The step's one barrier stands before its last row of products. By then
+//   every read of its stage is done and the next stage's loads are in, so the
+//   next step's first fragments are read beside that last row.
+template <int BM_, int BN_, int WGM_, int WGN_> struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
     static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
     static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 16, NI = WN / 16;
     static constexpr int ROWS = BM + BN;                 // B rows first, then A rows
-    static constexpr int WB = ROWS / 8 / NWV;            // 1 KB loads (eight rows) per wave
-    static constexpr int WS = ROWS / 64 / NWV;           // 64-scale loads per wave
+    static constexpr int WBB = BN / 8 / NWV, WBA = BM / 8 / NWV; // 1 KB loads (eight rows) a wave
+    static constexpr int WB = WBB + WBA;
+    static constexpr int NSC = ROWS / 64;                // 64-scale loads: waves 0 .. NSC - 1
     static constexpr int SCALES = ROWS * FP8_BLK;        // byte offset of a stage's scales
     static constexpr int STAGE = SCALES + ROWS * 4;
     static constexpr int OUTB = WM * (WN * 2 + 16) * NWV; // the epilogue's bf16 rows
-    static constexpr int LDS = NST * STAGE > OUTB ? NST * STAGE : OUTB;
-    static_assert(ROWS % (64 * NWV) == 0 && BN % (8 * WB) == 0 && BN % 64 == 0, "whole loads");
+    static constexpr int LDS = 2 * STAGE > OUTB ? 2 * STAGE : OUTB;
+    static_assert(BN % (8 * NWV) == 0 && BM % (8 * NWV) == 0 && BN % 64 == 0 && BM % 64 == 0 &&
+                      NSC <= NWV, "whole loads");
     static_assert(WN <= FP8_BLK && FP8_BLK % WN == 0, "a wave's n share one 128-row scale block");
-    static_assert((NST - 1) * (WB + WS) < 64, "loads in flight must fit the vmcnt counter");
+    static_assert(NI % 2 == 0, "two fragments of B in turn");
 };
 
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// Lane l's 16 (4) bytes at base + off go to LDS byte lds + 16 l (4 l). As
-// assembly for the reason given at ng::lds_dma16.
-DEVI void dma16(const uint8_t *base, uint32_t off, uint32_t lds)
+// If kb < kb1: lane l's 16 (4) bytes at base + off go to LDS byte lds + 16 l
+// (4 l). As assembly for the reason given at ng::lds_dma16; the test is inside
+// it so that the step stays one block for the compiler.
+DEVI void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int kb, int kb1)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lskip%=\n\t"
+                 "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n.Lskip%=:"
                  :
-                 : "v"(off), "s"(base), "s"(lds)
-                 : "m0");
+                 : "v"(off), "s"(base), "s"(lds), "s"(kb), "s"(kb1)
+                 : "m0", "scc");
 }
-DEVI void dma4(const float *base, uint32_t off, uint32_t lds)
+DEVI void dma4(const float *base, uint32_t off, uint32_t lds, int kb, int kb1)
 {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
+    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lskip%=\n\t"
+                 "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1\n.Lskip%=:"
                  :
-                 : "v"(off), "s"(base), "s"(lds)
-                 : "m0");
+                 : "v"(off), "s"(base), "s"(lds), "s"(kb), "s"(kb1)
+                 : "m0", "scc");
 }
 #pragma clang diagnostic pop
 
 // BLKB: B's scale block is 128 rows, so a wave's n share one scale per step.
 template <class C, int SUMS, bool BLKB>
-__global__ __launch_bounds__(C::NT, 1) void fp8_mm_tile_kernel(MmArgs a)
+__global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t L[C::LDS];
     // XCD-aware order: XCD k takes the k-th contiguous run of a grouped tile
@@ -142,36 +170,31 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_mm_tile_kernel(MmArgs a)
     // the 1 KB, i.e. the chunk that the swizzle puts there. Rows past an
     // operand read its last row (their outputs are dropped).
     const uint32_t lds0 = (uint32_t)(uintptr_t)(ng::lds_u8 *)L;
-    const bool isb = w * C::WB * 8 < C::BN;
-    const uint8_t *src = isb ? a.qb + (int64_t)n0 * a.pitch : a.qa + (int64_t)m0 * a.pitch;
-    const int last = isb ? a.N - 1 - n0 : a.M - 1 - m0;
+    const uint8_t *srcb = a.qb + (int64_t)n0 * a.pitch, *srca = a.qa + (int64_t)m0 * a.pitch;
     uint32_t off[C::WB];
 #pragma unroll
-    for (int i = 0; i < C::WB; ++i) {
-        const int r = (w * C::WB + i) * 8 + lane / 8 - (isb ? 0 : C::BN);
-        const int chunk = (lane & 7) ^ ((r >> 1) & 7);
-        off[i] = (uint32_t)min(r, last) * (uint32_t)a.pitch + chunk * 16;
+    for (int g = 0; g < C::WB; ++g) {
+        const int r = (g < C::WBB ? w * C::WBB + g : w * C::WBA + g - C::WBB) * 8 + lane / 8;
+        const int last = g < C::WBB ? a.N - 1 - n0 : a.M - 1 - m0;
+        off[g] = (uint32_t)min(r, last) * (uint32_t)a.pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
-    const bool sisb = w * C::WS * 64 < C::BN;
+    const bool sisb = w * 64 < C::BN;
     const float *ssrc = sisb ? a.sb : a.sa;
     const int ns = sisb ? a.nsb : a.nsa;
-    uint32_t soff[C::WS];
-#pragma unroll
-    for (int i = 0; i < C::WS; ++i) {
-        const int r = (w * C::WS + i) * 64 + lane - (sisb ? 0 : C::BN);
-        const int row = sisb ? min(n0 + r, a.N - 1) : min(m0 + r, a.M - 1);
-        soff[i] = (uint32_t)(row / (sisb ? a.rb : a.ra)) * 4u;
-    }
-    auto issue = [&](int kb) {
-        const uint32_t dst = lds0 + (uint32_t)((kb - kb0) % C::NST) * C::STAGE;
-        const uint8_t *p = src + (int64_t)kb * FP8_BLK;
-        const float *ps = ssrc + (int64_t)kb * ns;
-#pragma unroll
-        for (int i = 0; i < C::WB; ++i)
-            dma16(p, off[i], dst + (w * C::WB + i) * 1024);
-#pragma unroll
-        for (int i = 0; i < C::WS; ++i)
-            dma4(ps, soff[i], dst + C::SCALES + (w * C::WS + i) * 256);
+    const int srow = sisb ? min(n0 + w * 64 + lane, a.N - 1)
+                          : min(m0 + w * 64 - C::BN + lane, a.M - 1);
+    const uint32_t soff = (uint32_t)(srow / (sisb ? a.rb : a.ra)) * 4u;
+    // load g of this wave (g == WB: its scales) for step kb into stage st
+    const int sb1 = __builtin_amdgcn_readfirstlane(w < C::NSC ? kb1 : INT_MIN);
+    auto load = [&](int g, int kb, int st) {
+        const uint32_t dst = lds0 + (uint32_t)st * C::STAGE;
+        if (g < C::WBB)
+            dma16(srcb + (int64_t)kb * FP8_BLK, off[g], dst + (w * C::WBB + g) * 1024, kb, kb1);
+        else if (g < C::WB)
+            dma16(srca + (int64_t)kb * FP8_BLK, off[g],
+                  dst + C::BN * FP8_BLK + (w * C::WBA + g - C::WBB) * 1024, kb, kb1);
+        else
+            dma4(ssrc + (int64_t)kb * ns, soff, dst + C::SCALES + w * 256, kb, sb1);
     };
 
     floatx4_t acc[C::NI][C::MI];
@@ -187,47 +210,94 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_mm_tile_kernel(MmArgs a)
         return intx8_t{(int)u.x, (int)u.y, (int)u.z, (int)u.w,
                        (int)v.x, (int)v.y, (int)v.z, (int)v.w};
     };
+    const uint8_t *Bw = L + wn * C::WN * FP8_BLK, *Aw = L + (C::BN + wm * C::WM) * FP8_BLK;
+    const float *sbw = (const float *)(L + C::SCALES) + wn * C::WN;
+    const float *saw = (const float *)(L + C::SCALES) + C::BN + wm * C::WM;
+    auto fence = [] { // LDS reads stay on their side (their targets are written by the loads)
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+    };
+    auto sync = [&] {
+        fence();
+        ng::wait_vm<0>();
+        __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0)
+        __builtin_amdgcn_s_barrier();
+        fence();
+    };
+
+    // the next products' fragments as they lie in LDS: of B two in turn where
+    // products take them as they are
+    constexpr int RB = SUMS == TWELL_SUMS_FP8 ? 2 : 1;
+    intx8_t rb[RB], ra[C::MI];
+    float sa[C::MI], sb = 1.f;
+    floatx4_t sb4[2];
 #pragma unroll
-    for (int s = 0; s < C::NST - 1; ++s)
-        if (kb0 + s < kb1)
-            issue(kb0 + s);
+    for (int g = 0; g <= C::WB; ++g)
+        load(g, kb0, 0);
+    sync();
+    rb[0] = frag(Bw);
+    sb4[0] = *(const floatx4_t *)(sbw + q4 * 4);
+#pragma unroll
+    for (int j = 0; j < C::MI; ++j) {
+        ra[j] = frag(Aw + j * 16 * FP8_BLK);
+        sa[j] = saw[j * 16 + l16];
+    }
+    if (BLKB)
+        sb = sbw[0];
     for (int kb = kb0; kb < kb1; ++kb) {
-        // this wave's loads of the step are in once at most the later steps' pend
-        ng::wait_vm_steps<C::WB + C::WS, C::NST - 2>(min(kb1 - 1, kb + C::NST - 2) - kb);
-        __syncthreads(); // every wave's loads are in, and the last step is consumed
-        if (kb + C::NST - 1 < kb1)
-            issue(kb + C::NST - 1);
-        const uint8_t *S = L + (kb - kb0) % C::NST * C::STAGE;
-        const uint8_t *Bs = S + wn * C::WN * FP8_BLK, *As = S + (C::BN + wm * C::WM) * FP8_BLK;
-        const float *sbs = (const float *)(S + C::SCALES) + wn * C::WN;
-        const float *sas = (const float *)(S + C::SCALES) + C::BN + wm * C::WM;
-        intx8_t fa[C::MI];
-        float sa[C::MI];
+        const int st = (kb - kb0) & 1, cur = st * C::STAGE, nxt = C::STAGE - cur;
+        Frag<SUMS> fa[C::MI], fb;
+        float s[C::MI];
 #pragma unroll
         for (int j = 0; j < C::MI; ++j) {
-            fa[j] = frag(As + j * 16 * FP8_BLK);
-            sa[j] = sas[j * 16 + l16];
+            fa[j].set(ra[j]);
+            s[j] = BLKB ? sa[j] * sb : sa[j];
         }
-        if (BLKB) {
-            const float sb = sbs[0];
+        constexpr int NP = C::NI * C::MI, LAG = 3;
+        floatx4_t v[LAG + 1];
+        floatx4_t sbv[2];
+        auto scale = [&](int t) { // product t into its accumulator
+            const int i = t / C::MI, j = t % C::MI;
 #pragma unroll
-            for (int j = 0; j < C::MI; ++j)
-                sa[j] *= sb;
-        }
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = fmaf(v[t % (LAG + 1)][e], BLKB ? s[j] : s[j] * sbv[i & 1][e],
+                                    acc[i][j][e]);
+        };
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) {
-            const intx8_t fb = frag(Bs + i * 16 * FP8_BLK);
-            floatx4_t sb4 = {1.f, 1.f, 1.f, 1.f};
-            if (!BLKB)
-                sb4 = *(const floatx4_t *)(sbs + i * 16 + q4 * 4);
-#pragma unroll
-            for (int j = 0; j < C::MI; ++j) {
-                const floatx4_t p = block_sum<SUMS>(fb, fa[j]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = fmaf(p[e], BLKB ? sa[j] : sa[j] * sb4[e], acc[i][j][e]);
+        for (int t = 0; t < NP; ++t) {
+            const int i = t / C::MI, j = t % C::MI;
+            if (j == 0) {
+                if (i == C::NI - 1)
+                    sync();
+                fb.set(rb[i % RB]);
+                sbv[i & 1] = sb4[i & 1];
+                if (i < C::NI - 1) {
+                    rb[(i + 1) % RB] = frag(Bw + cur + (i + 1) * 16 * FP8_BLK);
+                    if (!BLKB)
+                        sb4[(i + 1) & 1] =
+                            *(const floatx4_t *)((const uint8_t *)(sbw + (i + 1) * 16 + q4 * 4) + cur);
+                } else {
+                    rb[0] = frag(Bw + nxt);
+                    if (!BLKB)
+                        sb4[0] = *(const floatx4_t *)((const uint8_t *)(sbw + q4 * 4) + nxt);
+                    else
+                        sb = *(const float *)((const uint8_t *)sbw + nxt);
+                }
             }
+            v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j]);
+            if (t >= LAG)
+                scale(t - LAG);
+            if (i == C::NI - 1) {
+                ra[j] = frag(Aw + nxt + j * 16 * FP8_BLK);
+                sa[j] = *(const float *)((const uint8_t *)(saw + j * 16 + l16) + nxt);
+            }
+            if (t <= C::WB)
+                load(t, kb + 1, st ^ 1);
+            __builtin_amdgcn_sched_barrier(0);
         }
+#pragma unroll
+        for (int t = NP - LAG; t < NP; ++t)
+            scale(t);
     }
     // ---- epilogue: lane's element e of tile (i, j) is token j * 16 + l16,
     // n i * 16 + q4 * 4 + e of the wave's part
@@ -261,13 +331,13 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_mm_tile_kernel(MmArgs a)
     // bf16: the wave's rows through its own piece of LDS, so that a store
     // instruction writes whole rows of WN values
     __syncthreads(); // every wave is done with the stages
-    constexpr int RB = C::WN * 2 + 16; // padded row: 16 rows start on 16 distinct banks
-    uint8_t *buf = L + w * C::WM * RB;
+    constexpr int ORB = C::WN * 2 + 16; // padded row: 16 rows start on 16 distinct banks
+    uint8_t *buf = L + w * C::WM * ORB;
 #pragma unroll
     for (int j = 0; j < C::MI; ++j)
 #pragma unroll
         for (int i = 0; i < C::NI; ++i)
-            *(uint2 *)(buf + (j * 16 + l16) * RB + (i * 16 + q4 * 4) * 2) =
+            *(uint2 *)(buf + (j * 16 + l16) * ORB + (i * 16 + q4 * 4) * 2) =
                 make_uint2(f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]),
                            f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]));
     constexpr int LPR = C::WN / 8; // lanes of a row, eight values each
@@ -275,7 +345,7 @@ __global__ __launch_bounds__(C::NT, 1) void fp8_mm_tile_kernel(MmArgs a)
 #pragma unroll
     for (int r0 = 0; r0 < C::WM; r0 += 64 / LPR) {
         const int m = mw + r0 + rr;
-        const uint4 v = *(const uint4 *)(buf + (r0 + rr) * RB + c8 * 16);
+        const uint4 v = *(const uint4 *)(buf + (r0 + rr) * ORB + c8 * 16);
         if (m >= a.M || n >= a.N)
             continue;
         uint16_t *row = (uint16_t *)a.out + m * a.ldo;
@@ -319,16 +389,18 @@ __global__ __launch_bounds__(64 * WV) void fp8_mm_rows_kernel(MmArgs a)
     for (int e = 0; e < 4; ++e)
         nb[e] = min(n0 + q4 * 4 + e, a.N - 1) / a.rb;
     for (int kb = w; kb < a.nkb; kb += WV) {
-        const intx8_t fb = frag32(pb + (int64_t)kb * FP8_BLK);
+        Frag<SUMS> fb;
+        fb.set(frag32(pb + (int64_t)kb * FP8_BLK));
         float sb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             sb[e] = a.sb[(int64_t)kb * a.nsb + nb[e]];
 #pragma unroll
         for (int t = 0; t < TB; ++t) {
-            const intx8_t fa = frag32(pa[t] + (int64_t)kb * FP8_BLK);
+            Frag<SUMS> fa;
+            fa.set(frag32(pa[t] + (int64_t)kb * FP8_BLK));
             const float sa = a.sa[(int64_t)kb * a.nsa + am[t] / a.ra];
-            const floatx4_t p = block_sum<SUMS>(fb, fa);
+            const floatx4_t p = Frag<SUMS>::mul(fb, fa);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 acc[t][e] = fmaf(p[e], sa * sb[e], acc[t][e]);
@@ -373,8 +445,9 @@ template <int SUMS> void launch_rows(const MmArgs &a, hipStream_t s)
         fp8_mm_rows_kernel<4, SUMS><<<grid, 64 * WV, 0, s>>>(a);
 }
 
-using T256 = TileCfg<256, 256, 4, 2, 2>; // waves of 64 tokens x 128 n
-using T128 = TileCfg<128, 128, 2, 2, 2>; // waves of 64 x 64
+using T256 = TileCfg<256, 256, 4, 2>; // waves of 64 tokens x 128 n
+using T192 = TileCfg<192, 256, 4, 2>; // waves of 48 x 128
+using T128 = TileCfg<128, 128, 2, 2>; // waves of 64 x 64
 
 template <class C, int SUMS> void launch_tile(const MmArgs &a, hipStream_t s)
 {
@@ -392,8 +465,12 @@ template <int SUMS> void launch_sums(const MmArgs &a, hipStream_t s)
     const int64_t t256 = (int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256);
     if (a.M <= 64)
         launch_rows<SUMS>(a, s);
-    else if (t256 >= 128)
-        launch_tile<T256, SUMS>(a, s);
+    else if (t256 >= 128) {
+        if constexpr (SUMS == TWELL_SUMS_FP8)
+            launch_tile<T256, SUMS>(a, s);
+        else
+            launch_tile<T192, SUMS>(a, s);
+    }
     else
         launch_tile<T128, SUMS>(a, s);
 }
