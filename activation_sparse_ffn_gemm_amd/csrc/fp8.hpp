@@ -87,7 +87,8 @@ DEVI void stg16u(void *p, uint4 v)
 // 8 (l + LPR c) .. + 7 for c < C, zeros past d. Loads leave the raw bits in
 // the registers (bf16: the first four words), so that the loads of several
 // arrays are in flight together; widen() makes them floats in place.
-template <int LPR, int C> struct Row {
+// RAG: d is no multiple of eight, and one lane's last chunk is cut.
+template <int LPR, int C, bool RAG> struct Row {
     float v[C][8];
 
     DEVI void put(int c, int i, uint4 q)
@@ -104,32 +105,47 @@ template <int LPR, int C> struct Row {
     DEVI void load(const void *row, int dt, int d, int lane)
     {
         if (dt == TWELL_BF16) {
+            const uint16_t *p = (const uint16_t *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
                 uint4 q = make_uint4(0, 0, 0, 0);
-                if (j + 8 <= d)
-                    q = ldg16u((const uint16_t *)row + j);
+                if (j + 8 <= d) {
+                    q = ldg16u(p + j);
+                } else if (RAG && j < d) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = (j + 2 * i < d ? p[j + 2 * i] : 0) |
+                               (j + 2 * i + 1 < d ? (uint32_t)p[j + 2 * i + 1] << 16 : 0);
+                    q = make_uint4(w[0], w[1], w[2], w[3]);
+                }
                 put(c, 0, q);
             }
         } else {
+            const float *p = (const float *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
                 uint4 q = make_uint4(0, 0, 0, 0), r = q;
                 if (j + 8 <= d) {
-                    q = ldg16u((const float *)row + j);
-                    r = ldg16u((const float *)row + j + 4);
+                    q = ldg16u(p + j);
+                    r = ldg16u(p + j + 4);
                 }
                 put(c, 0, q);
                 put(c, 4, r);
+                if (RAG && j < d && j + 8 > d) {
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+                        if (j + i < d)
+                            v[c][i] = p[j + i];
+                }
             }
         }
     }
 
-    // Floats from the raw bits; the last d % 8 elements, which no whole chunk
-    // covers, are read here, one by one.
-    DEVI void widen(const void *row, int dt, int d, int lane)
+    // floats from the raw bits
+    DEVI void widen(int dt)
     {
         if (dt == TWELL_BF16) {
 #pragma unroll
@@ -138,66 +154,43 @@ template <int LPR, int C> struct Row {
                 elem<TWELL_BF16>::widen(q, v[c]);
             }
         }
-        if (d & 7) {
-            const int n = d >> 3, ct = n / LPR; // the chunk that ends past d
-            if (lane == n % LPR) {
-                float t[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t[i] = i >= (d & 7)       ? 0.f
-                           : dt == TWELL_BF16 ? elem<TWELL_BF16>::load1(row, 8 * n + i)
-                                              : elem<TWELL_F32>::load1(row, 8 * n + i);
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (c == ct) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[c][i] = t[i];
-                    }
-            }
-        }
     }
 
     // bf16: rounded to nearest, ties to even
     DEVI void store(void *row, int dt, int d, int lane) const
     {
         if (dt == TWELL_BF16) {
+            uint16_t *p = (uint16_t *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
-                if (j + 8 <= d)
-                    stg16u((uint16_t *)row + j,
-                           make_uint4(f32x2_to_bf16x2(v[c][0], v[c][1]),
-                                      f32x2_to_bf16x2(v[c][2], v[c][3]),
-                                      f32x2_to_bf16x2(v[c][4], v[c][5]),
-                                      f32x2_to_bf16x2(v[c][6], v[c][7])));
+                const uint4 q = make_uint4(
+                    f32x2_to_bf16x2(v[c][0], v[c][1]), f32x2_to_bf16x2(v[c][2], v[c][3]),
+                    f32x2_to_bf16x2(v[c][4], v[c][5]), f32x2_to_bf16x2(v[c][6], v[c][7]));
+                if (j + 8 <= d) {
+                    stg16u(p + j, q);
+                } else if (RAG && j < d) {
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+                        if (j + i < d)
+                            p[j + i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+                }
             }
         } else {
+            float *p = (float *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
                 if (j + 8 <= d) {
-                    stg16u((float *)row + j, bits(c, 0));
-                    stg16u((float *)row + j + 4, bits(c, 4));
+                    stg16u(p + j, bits(c, 0));
+                    stg16u(p + j + 4, bits(c, 4));
+                } else if (RAG && j < d) {
+#pragma unroll
+                    for (int i = 0; i < 7; ++i)
+                        if (j + i < d)
+                            p[j + i] = v[c][i];
                 }
-            }
-        }
-        if (d & 7) {
-            const int n = d >> 3, ct = n / LPR;
-            if (lane == n % LPR) {
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    if (c == ct) {
-#pragma unroll
-                        for (int i = 0; i < 7; ++i)
-                            if (i < (d & 7)) {
-                                if (dt == TWELL_BF16)
-                                    ((uint16_t *)row)[8 * n + i] =
-                                        (uint16_t)f32x2_to_bf16x2(v[c][i], 0.f);
-                                else
-                                    ((float *)row)[8 * n + i] = v[c][i];
-                            }
-                    }
             }
         }
     }

@@ -3,18 +3,22 @@
 //   s = max(amax(block), 2^-64) / 448,  q = e4m3(x / s)
 //
 // over blocks of 1 x 128 or 128 x 128 elements. One workgroup takes a 128 x
-// 128 tile of x into registers, 64 elements per thread (eight rows of eight
+// 128 tile of x into registers, 32 elements per thread (four rows of eight
 // consecutive columns), so the tile holds whole blocks of every kind asked
 // for: x is read once whatever is written. Row amaxes are DPP moves inside
-// the 16 lanes that share a row, column amaxes go over the thread's own rows,
+// the 16 lanes that share a row; column amaxes go over the thread's own rows,
 // the wave's other lanes and the workgroup's waves (LDS). The transpose is
-// turned in LDS as bytes. Bound by HBM: x in, q (and q_t) out.
+// turned in LDS as bytes. Bound by HBM: x in, q (and q_t) out; a thread holds
+// few elements so that several tiles are on a CU, one loading while another
+// stores (64 elements a thread took 19.1 us for 8192 x 2048 bf16 and its
+// transpose).
 #include "fp8.hpp"
 
 namespace {
 
-constexpr int NT = 256, TS = FP8_BLK;
-static_assert(TS == 128, "a tile is one block of each kind");
+constexpr int NT = 512, NW = NT / 64, TS = FP8_BLK;
+constexpr int RPT = TS * 16 / NT; // rows of a thread
+static_assert(TS == 128 && RPT == 4, "a tile is one block of each kind; four rows a thread");
 
 struct QuantArgs {
     const void *x;
@@ -22,21 +26,33 @@ struct QuantArgs {
     float *s, *st;
     int64_t ld;
     int R, C, dt, tiles_c;
-    int block; // scales of the whole tile (128 x 128) instead of its rows' / columns'
 };
 
+DEVI uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// LDS word of rows 4 rr .. 4 rr + 3 of column c of the turned tile: 32 words a
+// column, its 16-byte chunks XOR-ed with the column's eights so that the 16
+// columns and four row groups a wave writes at once lie on distinct banks
+// (the columns' upper half one column further, on the other 32 banks).
+DEVI int turn_word(int c, int rr)
+{
+    return (c + (c >> 6)) * 32 + (rr ^ (((c >> 3) & 7) << 2));
+}
+
+// ROWS: q of x, COLS: q of its transpose, BLOCK: 128 x 128 blocks.
+template <bool ROWS, bool COLS, bool BLOCK>
 __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
 {
-    __shared__ uint32_t cmax[4][TS]; // column amaxes of each wave's 32 rows
-    __shared__ uint32_t wmax[4];
-    __shared__ uint2 turn[TS][TS / 8]; // [column][eight rows], chunks swizzled
+    __shared__ uint32_t cmax[NW][TS]; // column amaxes of each wave's rows
+    __shared__ __attribute__((aligned(16))) float cs[2][TS]; // the columns' scales and 1 / scales
+    __shared__ __attribute__((aligned(16))) uint32_t turn[COLS ? (TS + 1) * 32 : 1];
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
     const int tr = blockIdx.x / a.tiles_c, tc = blockIdx.x % a.tiles_c;
     const int cc = tid & 15, rr = tid >> 4; // this thread's column chunk and row group
-    const int r0 = tr * TS + rr * 8, c0 = tc * TS + cc * 8;
-    float v[8][8];
+    const int r0 = tr * TS + rr * RPT, c0 = tc * TS + cc * 8;
+    float v[RPT][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < RPT; ++i) {
         const int r = r0 + i;
         const uint8_t *p = (const uint8_t *)row_ptr(a.x, a.dt, a.ld, r < a.R ? r : 0);
         if (r < a.R && c0 + 8 <= a.C) {
@@ -54,104 +70,109 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
                                                    : elem<TWELL_F32>::load1(p, c0 + k);
         }
     }
-    uint32_t m = 0;
-    if (a.block) {
+    float sb = 0.f, ib = 0.f;
+    if constexpr (BLOCK) {
+        uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < RPT; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t b = abs_bits(v[i][k]);
-                m = b > m ? b : m;
-            }
+            for (int k = 0; k < 8; ++k)
+                m = umax(m, abs_bits(v[i][k]));
         m = row16_umax(m);
 #pragma unroll
-        for (int o = 16; o < 64; o <<= 1) {
-            const uint32_t b = (uint32_t)__shfl_xor((int)m, o, 64);
-            m = b > m ? b : m;
-        }
+        for (int o = 16; o < 64; o <<= 1)
+            m = umax(m, (uint32_t)__shfl_xor((int)m, o, 64));
         if (lane == 0)
-            wmax[w] = m;
+            cmax[w][0] = m;
         __syncthreads();
-        m = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            m = umax(m, cmax[i][0]);
+        sb = fp8_scale(m);
+        ib = 1.f / sb;
+        if (tid == 0) {
+            // [column block][row block], and the same number for the transpose
+            if (ROWS)
+                a.s[(int64_t)tc * fp8_blocks(a.R) + tr] = sb;
+            if (COLS)
+                a.st[(int64_t)tr * fp8_blocks(a.C) + tc] = sb;
+        }
+    } else if constexpr (COLS) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < RPT; ++i)
+                m = umax(m, abs_bits(v[i][k]));
+#pragma unroll
+            for (int o = 16; o < 64; o <<= 1)
+                m = umax(m, (uint32_t)__shfl_xor((int)m, o, 64));
+            if (lane < 16)
+                cmax[w][cc * 8 + k] = m;
+        }
+        __syncthreads();
+        if (tid < TS) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                m = umax(m, cmax[i][tid]);
+            const float s = fp8_scale(m);
+            cs[0][tid] = s;
+            cs[1][tid] = 1.f / s;
+            if (tc * TS + tid < a.C)
+                a.st[(int64_t)tr * a.C + tc * TS + tid] = s;
+        }
     }
-    const float sb = a.block ? fp8_scale(m) : 0.f;
-    const float ib = a.block ? 1.f / sb : 0.f;
-    if (a.block && tid == 0) {
-        // [column block][row block], and the same number for the transpose
-        if (a.q)
-            a.s[(int64_t)tc * fp8_blocks(a.R) + tr] = sb;
-        if (a.qt)
-            a.st[(int64_t)tr * fp8_blocks(a.C) + tc] = sb;
-    }
-    if (a.q) {
+    if constexpr (ROWS) {
         const int64_t pitch = fp8_pitch(a.C);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < RPT; ++i) {
             float s = sb, inv = ib;
-            if (!a.block) {
-                uint32_t rm = 0;
+            if (!BLOCK) {
+                uint32_t m = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t b = abs_bits(v[i][k]);
-                    rm = b > rm ? b : rm;
-                }
-                s = fp8_scale(row16_umax(rm));
+                for (int k = 0; k < 8; ++k)
+                    m = umax(m, abs_bits(v[i][k]));
+                s = fp8_scale(row16_umax(m));
                 inv = 1.f / s;
             }
             const int r = r0 + i;
             if (r < a.R) {
                 *(uint2 *)(a.q + (int64_t)r * pitch + c0) = quant8(v[i], s, inv);
-                if (!a.block && cc == 0)
+                if (!BLOCK && cc == 0)
                     a.s[(int64_t)tc * a.R + r] = s;
             }
         }
     }
-    if (!a.qt)
-        return;
-    if (!a.block) {
+    if constexpr (COLS) {
+        if (!BLOCK)
+            __syncthreads(); // cs
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            uint32_t km = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t b = abs_bits(v[i][k]);
-                km = b > km ? b : km;
-            }
-#pragma unroll
-            for (int o = 16; o < 64; o <<= 1) {
-                const uint32_t b = (uint32_t)__shfl_xor((int)km, o, 64);
-                km = b > km ? b : km;
-            }
-            if (lane < 16)
-                cmax[w][cc * 8 + k] = km;
+            const float s = BLOCK ? sb : cs[0][cc * 8 + k], inv = BLOCK ? ib : cs[1][cc * 8 + k];
+            turn[turn_word(cc * 8 + k, rr)] = f32x4_to_e4m3x4(
+                div_by_scale(v[0][k], s, inv), div_by_scale(v[1][k], s, inv),
+                div_by_scale(v[2][k], s, inv), div_by_scale(v[3][k], s, inv));
         }
         __syncthreads();
-    }
+        const int64_t pitch = fp8_pitch(a.R);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int c = cc * 8 + k;
-        float s = sb, inv = ib;
-        if (!a.block) {
-            s = fp8_scale(max(max(cmax[0][c], cmax[1][c]), max(cmax[2][c], cmax[3][c])));
-            inv = 1.f / s;
-            if (rr == 0 && tc * TS + c < a.C)
-                a.st[(int64_t)tr * a.C + tc * TS + c] = s;
+        for (int i = 0; i < TS * 8 / NT; ++i) { // 16 bytes: column c, rows 16 ch ..
+            const int q = tid + i * NT, c = q >> 3, ch = q & 7;
+            if (tc * TS + c < a.C)
+                *(uint4 *)(a.qt + (int64_t)(tc * TS + c) * pitch + tr * TS + ch * 16) =
+                    *(const uint4 *)&turn[turn_word(c, 4 * ch)];
         }
-        float u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            u[i] = v[i][k];
-        turn[c][rr ^ cc] = quant8(u, s, inv);
     }
-    __syncthreads();
-    const int64_t pitch = fp8_pitch(a.R);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int c = k * 16 + (tid >> 4), ch = tid & 15;
-        if (tc * TS + c < a.C)
-            *(uint2 *)(a.qt + (int64_t)(tc * TS + c) * pitch + tr * TS + ch * 8) =
-                turn[c][ch ^ (c >> 3)];
-    }
+}
+
+template <bool ROWS, bool COLS> void launch_layout(const QuantArgs &a, bool block, hipStream_t s)
+{
+    const dim3 grid((uint32_t)(fp8_blocks(a.R) * (int64_t)a.tiles_c));
+    if (block)
+        fp8_quant_kernel<ROWS, COLS, true><<<grid, NT, 0, s>>>(a);
+    else
+        fp8_quant_kernel<ROWS, COLS, false><<<grid, NT, 0, s>>>(a);
 }
 
 } // namespace
@@ -165,10 +186,15 @@ hipError_t launch_fp8_quant(const twell_mat_t *x, const twell_fp8_t *o, const tw
         a.q = o->q, a.s = o->scale;
     if (ot)
         a.qt = ot->q, a.st = ot->scale;
-    a.block = (o ? o : ot)->block_rows == TS;
+    const bool block = (o ? o : ot)->block_rows == TS;
     a.tiles_c = fp8_blocks(a.C);
     Timer tm(timing, s);
-    fp8_quant_kernel<<<dim3((uint32_t)(fp8_blocks(a.R) * (int64_t)a.tiles_c)), NT, 0, s>>>(a);
+    if (o && ot)
+        launch_layout<true, true>(a, block, s);
+    else if (o)
+        launch_layout<true, false>(a, block, s);
+    else
+        launch_layout<false, true>(a, block, s);
     tm.mark("fp8_quant");
     return hipGetLastError();
 }

@@ -20,21 +20,41 @@
 
 namespace {
 
-constexpr int NT = 256; // threads of a workgroup
+// Lanes that share a row: every lane holds eight elements, sixteen in rows
+// past 8192. Registers stay few (32), so the chip is full of rows in flight;
+// rows of 2048 as one wave's 32 elements a lane ran at 3.3 TB/s, as four
+// waves' eight at 5.0.
+template <int LPR> DEVI int row_lane() { return (int)threadIdx.x % LPR; }
 
-// Sum over the LPR lanes that share a row: a wave, or the whole workgroup
-// (through buf, NT / 64 floats; the caller gives a buffer of its own to each
-// sum, so no barrier is needed before the write).
+// Sum over the LPR lanes that share a row, in every one of them. Past a wave
+// it goes through buf (a float for each wave of the workgroup); each sum of a
+// kernel has a buf of its own, so no barrier is needed before it is written.
 template <int LPR> DEVI float row_sum(float v, float *buf)
 {
-    v = wave_sum(v);
-    if constexpr (LPR == 64)
+    if constexpr (LPR < 64) {
+        v += dpp_mov<0xB1>(v);
+        v += dpp_mov<0x4E>(v);
+        v += dpp_mov<0x141>(v);
+        v += dpp_mov<0x140>(v);
+        if constexpr (LPR == 32)
+            v += __shfl_xor(v, 16, 64);
         return v;
-    const int w = wave_id();
-    if ((threadIdx.x & 63) == 0)
-        buf[w] = v;
-    __syncthreads();
-    return (buf[0] + buf[1]) + (buf[2] + buf[3]);
+    } else {
+        v = wave_sum(v);
+        if constexpr (LPR > 64) {
+            constexpr int W = LPR / 64; // waves of a row
+            const int w = wave_id();
+            if ((threadIdx.x & 63) == 0)
+                buf[w] = v;
+            __syncthreads();
+            const float *b = buf + w / W * W;
+            v = b[0];
+#pragma unroll
+            for (int i = 1; i < W; ++i)
+                v += b[i];
+        }
+        return v;
+    }
 }
 
 struct FwdArgs {
@@ -47,37 +67,35 @@ struct FwdArgs {
     float eps;
 };
 
-template <int LPR, int C> __global__ __launch_bounds__(NT) void rmsnorm_fwd_kernel(FwdArgs a)
+constexpr int fwd_threads(int lpr) { return lpr < 256 ? 256 : lpr; }
+
+template <int LPR, int C, bool RAG>
+__global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a)
 {
-    constexpr int RPB = NT / LPR; // rows per workgroup
-    __shared__ float buf[NT / 64];
-    const int lane = LPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t t = (int64_t)blockIdx.x * RPB + (LPR == 64 ? wave_id() : 0);
-    if (t >= a.T)
-        return; // LPR == 64 only: a whole wave, and no barrier follows
-    const int d = a.d;
-    Row<LPR, C> h;
-    {
-        const void *px = row_ptr(a.x, a.dtx, a.ldx, t);
-        h.load(px, a.dtx, d, lane);
-        if (a.res) {
-            Row<LPR, C> r;
-            const void *pr = row_ptr(a.res, a.dtr, a.ldr, t);
-            r.load(pr, a.dtr, d, lane);
-            h.widen(px, a.dtx, d, lane);
-            r.widen(pr, a.dtr, d, lane);
+    constexpr int RPB = fwd_threads(LPR) / LPR; // rows per workgroup
+    __shared__ float buf[fwd_threads(LPR) / 64];
+    const int lane = row_lane<LPR>();
+    const int64_t t = (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
+    // a workgroup's rows past T are empty: they load and store nothing
+    const int d = t < a.T ? a.d : 0;
+    Row<LPR, C, RAG> h, g;
+    h.load(row_ptr(a.x, a.dtx, a.ldx, t), a.dtx, d, lane);
+    if (a.res) {
+        Row<LPR, C, RAG> r;
+        r.load(row_ptr(a.res, a.dtr, a.ldr, t), a.dtr, d, lane);
+        g.load(a.gain, a.dtg, d, lane);
+        h.widen(a.dtx);
+        r.widen(a.dtr);
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    h.v[c][i] += r.v[c][i];
-            h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
-        } else {
-            h.widen(px, a.dtx, d, lane);
-        }
+            for (int i = 0; i < 8; ++i)
+                h.v[c][i] += r.v[c][i];
+        h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
+    } else {
+        g.load(a.gain, a.dtg, d, lane);
+        h.widen(a.dtx);
     }
-    Row<LPR, C> g;
-    g.load(a.gain, a.dtg, d, lane);
     float ss = 0.f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -85,8 +103,8 @@ template <int LPR, int C> __global__ __launch_bounds__(NT) void rmsnorm_fwd_kern
         for (int i = 0; i < 8; ++i)
             ss = fmaf(h.v[c][i], h.v[c][i], ss);
     ss = row_sum<LPR>(ss, buf);
-    const float r = 1.f / sqrtf(ss / (float)d + a.eps);
-    g.widen(a.gain, a.dtg, d, lane);
+    const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+    g.widen(a.dtg);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -96,7 +114,7 @@ template <int LPR, int C> __global__ __launch_bounds__(NT) void rmsnorm_fwd_kern
         h.store(row_ptr(a.n, a.dtn, a.ldn, t), a.dtn, d, lane);
         return;
     }
-    const int64_t pitch = fp8_pitch(d);
+    const int64_t pitch = fp8_pitch(a.d);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int j = 8 * (lane + LPR * c);
@@ -107,7 +125,7 @@ template <int LPR, int C> __global__ __launch_bounds__(NT) void rmsnorm_fwd_kern
             m = b > m ? b : m;
         }
         const float s = fp8_scale(row16_umax(m));
-        if (j < pitch) {
+        if (j < pitch && t < a.T) {
             *(uint2 *)(a.q + t * pitch + j) = quant8(h.v[c], s, 1.f / s);
             if ((lane & 15) == 0)
                 a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = s;
@@ -124,107 +142,114 @@ struct BwdArgs {
     float eps;
 };
 
-template <int LPR, int C> __global__ __launch_bounds__(NT) void rmsnorm_bwd_kernel(BwdArgs a)
+// Eight waves a workgroup (sixteen for the widest rows), so that there are
+// few partial rows for the waves in flight.
+constexpr int bwd_threads(int lpr) { return lpr < 512 ? 512 : lpr; }
+
+template <int LPR, int C, bool RAG>
+__global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a)
 {
-    constexpr int RPB = NT / LPR;
-    extern __shared__ float lds[]; // LPR == 64: d floats (the waves' dgain sums)
-    __shared__ float buf[2][2][NT / 64];
-    const int lane = LPR == 64 ? threadIdx.x & 63 : threadIdx.x;
-    const int w = LPR == 64 ? wave_id() : 0;
-    const int d = a.d;
+    constexpr int NT = bwd_threads(LPR), RPB = NT / LPR, NW = NT / 64;
+    constexpr int COLS = 8 * LPR * C;
+    __shared__ float buf[2][2][NW];
+    __shared__ float lds[RPB > 1 ? COLS : 1]; // the rows' dgain sums
+    const int lane = row_lane<LPR>();
+    const int row = (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
     float acc[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc[c][i] = 0.f;
+    Row<LPR, C, RAG> g;
+    g.load(a.gain, a.dtg, a.d, lane);
+    g.widen(a.dtg);
     int it = 0;
-    for (int64_t t = (int64_t)blockIdx.x * RPB + w; t < a.T; t += (int64_t)gridDim.x * RPB, ++it) {
-        Row<LPR, C> h, dn, g;
-        const void *ph = row_ptr(a.h, a.dth, a.ldh, t), *pd = row_ptr(a.dn, a.dtdn, a.lddn, t);
-        h.load(ph, a.dth, d, lane);
-        dn.load(pd, a.dtdn, d, lane);
-        g.load(a.gain, a.dtg, d, lane);
-        h.widen(ph, a.dth, d, lane);
-        dn.widen(pd, a.dtdn, d, lane);
-        g.widen(a.gain, a.dtg, d, lane);
+    for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < a.T; t0 += (int64_t)gridDim.x * RPB, ++it) {
+        const int64_t t = t0 + row;
+        const int d = t < a.T ? a.d : 0; // rows past T are empty
+        Row<LPR, C, RAG> h, dn, rs;
+        h.load(row_ptr(a.h, a.dth, a.ldh, t), a.dth, d, lane);
+        dn.load(row_ptr(a.dn, a.dtdn, a.lddn, t), a.dtdn, d, lane);
+        if (a.dres)
+            rs.load(row_ptr(a.dres, a.dtdres, a.lddres, t), a.dtdres, d, lane);
+        h.widen(a.dth);
+        dn.widen(a.dtdn);
         float ss = 0.f, dot = 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 ss = fmaf(h.v[c][i], h.v[c][i], ss);
-                g.v[c][i] *= dn.v[c][i];
-                dot = fmaf(g.v[c][i], h.v[c][i], dot);
+                dot = fmaf(g.v[c][i] * dn.v[c][i], h.v[c][i], dot);
             }
         // two buffers in turn: a wave may still read the last row's sums
         ss = row_sum<LPR>(ss, buf[it & 1][0]);
         dot = row_sum<LPR>(dot, buf[it & 1][1]);
-        const float r = 1.f / sqrtf(ss / (float)d + a.eps);
-        const float m = dot * r / (float)d; // mean(dg xh)
+        const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
+        const float m = dot * r / (float)a.d; // mean(dg xh)
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float xh = h.v[c][i] * r;
                 acc[c][i] = fmaf(dn.v[c][i], xh, acc[c][i]);
-                h.v[c][i] = r * fmaf(-xh, m, g.v[c][i]);
+                h.v[c][i] = r * fmaf(-xh, m, g.v[c][i] * dn.v[c][i]);
             }
         if (a.dres) {
-            const void *pr = row_ptr(a.dres, a.dtdres, a.lddres, t);
-            dn.load(pr, a.dtdres, d, lane);
-            dn.widen(pr, a.dtdres, d, lane);
+            rs.widen(a.dtdres);
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    h.v[c][i] += dn.v[c][i];
+                    h.v[c][i] += rs.v[c][i];
         }
         h.store(row_ptr(a.dh, a.dtdh, a.lddh, t), a.dtdh, d, lane);
     }
-    float *part = a.part + (int64_t)blockIdx.x * d;
-    if constexpr (LPR == 64) { // the waves' sums, added in wave order
-        for (int q = 0; q < NT / 64; ++q) {
-            if (w == q) {
+    // the rows' sums, added in row order
+    float *part = a.part + (int64_t)blockIdx.x * a.d;
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int j = 8 * (lane + LPR * c) + i;
-                        if (j < d)
-                            lds[j] = q ? lds[j] + acc[c][i] : acc[c][i];
-                    }
-            }
+    for (int q = 0; q < RPB; ++q) {
+        if (q)
             __syncthreads();
+        if (row == q) {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int j = 8 * (lane + LPR * c) + i;
+                    const float v = q ? lds[j] + acc[c][i] : acc[c][i];
+                    if (q < RPB - 1)
+                        lds[j] = v;
+                    else if (j < a.d)
+                        part[j] = v;
+                }
         }
-        for (int j = threadIdx.x; j < d; j += NT)
-            part[j] = lds[j];
-    } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j = 8 * (lane + LPR * c) + i;
-                if (j < d)
-                    part[j] = acc[c][i];
-            }
     }
 }
 
 // dgain[j] = sum of the G partial rows, in row order: 64 columns per
-// workgroup, SL slices of consecutive rows, joined in slice order.
+// workgroup, SL slices of consecutive rows, joined in slice order; a lane has
+// eight rows' loads in flight.
+constexpr int BWD_WG = 512;
 constexpr int SL = 16;
 __global__ __launch_bounds__(64 * SL) void rmsnorm_dgain_kernel(const float *part, int G, int d,
                                                               float *dgain)
 {
     __shared__ float s[SL][64];
     const int lane = threadIdx.x & 63, w = wave_id();
-    const int j = blockIdx.x * 64 + lane;
+    const int j = blockIdx.x * 64 + lane, jc = min(j, d - 1);
     const int per = (G + SL - 1) / SL, g0 = min(G, w * per), g1 = min(G, g0 + per);
     float v = 0.f;
-    if (j < d)
-        for (int g = g0; g < g1; ++g)
-            v += part[(int64_t)g * d + j];
+    for (int g = g0; g < g1; g += 8) {
+        float p[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[i] = part[(int64_t)min(g + i, g1 - 1) * d + jc];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v += g + i < g1 ? p[i] : 0.f;
+    }
     s[w][lane] = v;
     __syncthreads();
     if (w == 0 && j < d) {
@@ -234,15 +259,60 @@ __global__ __launch_bounds__(64 * SL) void rmsnorm_dgain_kernel(const float *par
     }
 }
 
-// Rows one wave each once there are enough of them to give every SIMD two
-// waves; fewer, or longer, rows take a whole workgroup.
-constexpr int WAVE_ROWS = 2048;
+// Lanes of a row of d elements: eight each, as many as it needs.
+int row_lanes(int d)
+{
+    int l = 16;
+    while (l < 1024 && 8 * l < d)
+        l *= 2;
+    return l;
+}
 
+// Workgroups (and partial rows of dgain) of the backward: two for each CU, and
+// for few rows one for every four turns of its row slots. A single one writes
+// dgain itself.
 int bwd_groups(int T, int d)
 {
-    const int rpb = T >= WAVE_ROWS && d <= 2048 ? 4 : 1;
-    const int g = (T + rpb - 1) / rpb;
-    return g < 512 ? g : 512;
+    const int lpr = row_lanes(d), rpb = bwd_threads(lpr) / lpr;
+    const int64_t g = ((int64_t)T + 4 * rpb - 1) / (4 * rpb);
+    return g < BWD_WG ? (int)g : BWD_WG;
+}
+
+template <int LPR, int C, bool RAG> void fwd_one(const FwdArgs &a, hipStream_t s)
+{
+    constexpr int NT = fwd_threads(LPR), RPB = NT / LPR;
+    rmsnorm_fwd_kernel<LPR, C, RAG><<<(a.T + RPB - 1) / RPB, NT, 0, s>>>(a);
+}
+
+template <bool RAG> void fwd_sizes(const FwdArgs &a, hipStream_t s)
+{
+    switch (row_lanes(a.d)) {
+    case 16: return fwd_one<16, 1, RAG>(a, s);
+    case 32: return fwd_one<32, 1, RAG>(a, s);
+    case 64: return fwd_one<64, 1, RAG>(a, s);
+    case 128: return fwd_one<128, 1, RAG>(a, s);
+    case 256: return fwd_one<256, 1, RAG>(a, s);
+    case 512: return fwd_one<512, 1, RAG>(a, s);
+    }
+    return a.d <= 8192 ? fwd_one<1024, 1, RAG>(a, s) : fwd_one<1024, 2, RAG>(a, s);
+}
+
+template <int LPR, int C, bool RAG> void bwd_one(const BwdArgs &a, int G, hipStream_t s)
+{
+    rmsnorm_bwd_kernel<LPR, C, RAG><<<G, bwd_threads(LPR), 0, s>>>(a);
+}
+
+template <bool RAG> void bwd_sizes(const BwdArgs &a, int G, hipStream_t s)
+{
+    switch (row_lanes(a.d)) {
+    case 16: return bwd_one<16, 1, RAG>(a, G, s);
+    case 32: return bwd_one<32, 1, RAG>(a, G, s);
+    case 64: return bwd_one<64, 1, RAG>(a, G, s);
+    case 128: return bwd_one<128, 1, RAG>(a, G, s);
+    case 256: return bwd_one<256, 1, RAG>(a, G, s);
+    case 512: return bwd_one<512, 1, RAG>(a, G, s);
+    }
+    return a.d <= 8192 ? bwd_one<1024, 1, RAG>(a, G, s) : bwd_one<1024, 2, RAG>(a, G, s);
 }
 
 } // namespace
@@ -263,26 +333,10 @@ hipError_t launch_rmsnorm_fwd(const twell_mat_t *x, const twell_mat_t *res, cons
     else
         a.n = n->data, a.ldn = n->ld, a.dtn = n->dtype;
     Timer tm(timing, s);
-    const int T = a.T, d = a.d;
-    if (T >= WAVE_ROWS && d <= 4096) {
-        const dim3 grid((T + 3) / 4);
-        if (d <= 512)
-            rmsnorm_fwd_kernel<64, 1><<<grid, NT, 0, s>>>(a);
-        else if (d <= 1024)
-            rmsnorm_fwd_kernel<64, 2><<<grid, NT, 0, s>>>(a);
-        else if (d <= 2048)
-            rmsnorm_fwd_kernel<64, 4><<<grid, NT, 0, s>>>(a);
-        else
-            rmsnorm_fwd_kernel<64, 8><<<grid, NT, 0, s>>>(a);
-    } else if (d <= 2048) {
-        rmsnorm_fwd_kernel<NT, 1><<<T, NT, 0, s>>>(a);
-    } else if (d <= 4096) {
-        rmsnorm_fwd_kernel<NT, 2><<<T, NT, 0, s>>>(a);
-    } else if (d <= 8192) {
-        rmsnorm_fwd_kernel<NT, 4><<<T, NT, 0, s>>>(a);
-    } else {
-        rmsnorm_fwd_kernel<NT, 8><<<T, NT, 0, s>>>(a);
-    }
+    if (a.d & 7)
+        fwd_sizes<true>(a, s);
+    else
+        fwd_sizes<false>(a, s);
     tm.mark("rmsnorm_fwd");
     return hipGetLastError();
 }
@@ -300,29 +354,19 @@ hipError_t launch_rmsnorm_bwd(const twell_mat_t *dn, const twell_mat_t *h, const
     if (dres)
         a.dres = dres->data, a.lddres = dres->ld, a.dtdres = dres->dtype;
     a.dh = dh->data, a.lddh = dh->ld, a.dtdh = dh->dtype;
-    a.part = (float *)ws;
+    const int G = bwd_groups(a.T, a.d);
+    a.part = G == 1 ? dgain : (float *)ws;
     Timer tm(timing, s);
-    const int T = a.T, d = a.d, G = bwd_groups(T, d);
-    if (T >= WAVE_ROWS && d <= 2048) {
-        const size_t lds = (size_t)d * 4;
-        if (d <= 512)
-            rmsnorm_bwd_kernel<64, 1><<<G, NT, lds, s>>>(a);
-        else if (d <= 1024)
-            rmsnorm_bwd_kernel<64, 2><<<G, NT, lds, s>>>(a);
+    if (a.T > 0) {
+        if (a.d & 7)
+            bwd_sizes<true>(a, G, s);
         else
-            rmsnorm_bwd_kernel<64, 4><<<G, NT, lds, s>>>(a);
-    } else if (T > 0) {
-        if (d <= 2048)
-            rmsnorm_bwd_kernel<NT, 1><<<G, NT, 0, s>>>(a);
-        else if (d <= 4096)
-            rmsnorm_bwd_kernel<NT, 2><<<G, NT, 0, s>>>(a);
-        else if (d <= 8192)
-            rmsnorm_bwd_kernel<NT, 4><<<G, NT, 0, s>>>(a);
-        else
-            rmsnorm_bwd_kernel<NT, 8><<<G, NT, 0, s>>>(a);
+            bwd_sizes<false>(a, G, s);
     }
     tm.mark("rmsnorm_bwd");
-    rmsnorm_dgain_kernel<<<(d + 63) / 64, 64 * SL, 0, s>>>(a.part, G, d, dgain);
-    tm.mark("rmsnorm_dgain");
+    if (G != 1) {
+        rmsnorm_dgain_kernel<<<(a.d + 63) / 64, 64 * SL, 0, s>>>(a.part, G, a.d, dgain);
+        tm.mark("rmsnorm_dgain");
+    }
     return hipGetLastError();
 }
