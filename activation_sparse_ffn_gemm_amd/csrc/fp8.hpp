@@ -37,32 +37,40 @@ DEVI uint32_t row16_umax(uint32_t v)
 }
 DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Scale of a block from the bits of its largest absolute value.
-DEVI float fp8_scale(uint32_t amax_bits)
+// a / b rounded to float32 as a division rounds it, from inv = 1 / b: what
+// the product a inv is off by is one fused step away (a - q b is exact in the
+// fused multiply-add). Three instructions for a division's ten; nothing may
+// overflow or be infinite.
+DEVI float div_by(float a, float b, float inv)
 {
-    const uint32_t floor_bits = __float_as_uint(FP8_AMAX_MIN);
-    return __uint_as_float(amax_bits > floor_bits ? amax_bits : floor_bits) / FP8_MAX;
+    const float q = a * inv;
+    return fmaf(fmaf(-q, b, a), inv, q);
 }
 
-// v / s rounded to float32 as a division rounds it, from inv = 1 / s: the
-// product's error is one fused step away (v - q s is exact in the fused
-// multiply-add), three instructions in place of a division's ten. s is a
-// block's scale and |v| <= 448 s up to rounding, so nothing overflows; where
-// s is infinite or NaN the results are NaN, as the quotients of the block's
-// own largest values are.
-DEVI float div_by_scale(float v, float s, float inv)
+// Scale of a block from the bits of its largest absolute value, and 1 / scale
+// (the hardware's reciprocal and one Newton step). An infinite or NaN amax is
+// the scale itself, and makes 1 / scale NaN, so the block's q are NaN.
+struct BlockScale {
+    float s, inv;
+};
+DEVI BlockScale fp8_scale(uint32_t amax_bits)
 {
-    const float q = v * inv;
-    return fmaf(fmaf(-q, s, v), inv, q);
+    const uint32_t lo = __float_as_uint(FP8_AMAX_MIN);
+    const float amax = __uint_as_float(amax_bits > lo ? amax_bits : lo);
+    BlockScale b;
+    b.s = amax_bits >= 0x7f800000u ? amax : div_by(amax, FP8_MAX, 1.f / FP8_MAX);
+    const float y = __builtin_amdgcn_rcpf(b.s);
+    b.inv = fmaf(fmaf(-b.s, y, 1.f), y, y);
+    return b;
 }
 
 // Eight values of one block -> eight bytes.
-DEVI uint2 quant8(const float *v, float s, float inv)
+DEVI uint2 quant8(const float *v, BlockScale b)
 {
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        q[i] = div_by_scale(v[i], s, inv);
+        q[i] = div_by(v[i], b.s, b.inv);
     return make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
                       f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
 }

@@ -70,7 +70,7 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
                                                    : elem<TWELL_F32>::load1(p, c0 + k);
         }
     }
-    float sb = 0.f, ib = 0.f;
+    BlockScale sb = {};
     if constexpr (BLOCK) {
         uint32_t m = 0;
 #pragma unroll
@@ -89,13 +89,12 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
         for (int i = 0; i < NW; ++i)
             m = umax(m, cmax[i][0]);
         sb = fp8_scale(m);
-        ib = 1.f / sb;
         if (tid == 0) {
             // [column block][row block], and the same number for the transpose
             if (ROWS)
-                a.s[(int64_t)tc * fp8_blocks(a.R) + tr] = sb;
+                a.s[(int64_t)tc * fp8_blocks(a.R) + tr] = sb.s;
             if (COLS)
-                a.st[(int64_t)tr * fp8_blocks(a.C) + tc] = sb;
+                a.st[(int64_t)tr * fp8_blocks(a.C) + tc] = sb.s;
         }
     } else if constexpr (COLS) {
 #pragma unroll
@@ -116,31 +115,30 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
 #pragma unroll
             for (int i = 0; i < NW; ++i)
                 m = umax(m, cmax[i][tid]);
-            const float s = fp8_scale(m);
-            cs[0][tid] = s;
-            cs[1][tid] = 1.f / s;
+            const BlockScale b = fp8_scale(m);
+            cs[0][tid] = b.s;
+            cs[1][tid] = b.inv;
             if (tc * TS + tid < a.C)
-                a.st[(int64_t)tr * a.C + tc * TS + tid] = s;
+                a.st[(int64_t)tr * a.C + tc * TS + tid] = b.s;
         }
     }
     if constexpr (ROWS) {
         const int64_t pitch = fp8_pitch(a.C);
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
-            float s = sb, inv = ib;
+            BlockScale b = sb;
             if (!BLOCK) {
                 uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     m = umax(m, abs_bits(v[i][k]));
-                s = fp8_scale(row16_umax(m));
-                inv = 1.f / s;
+                b = fp8_scale(row16_umax(m));
             }
             const int r = r0 + i;
             if (r < a.R) {
-                *(uint2 *)(a.q + (int64_t)r * pitch + c0) = quant8(v[i], s, inv);
+                *(uint2 *)(a.q + (int64_t)r * pitch + c0) = quant8(v[i], b);
                 if (!BLOCK && cc == 0)
-                    a.s[(int64_t)tc * a.R + r] = s;
+                    a.s[(int64_t)tc * a.R + r] = b.s;
             }
         }
     }
@@ -149,10 +147,11 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
             __syncthreads(); // cs
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float s = BLOCK ? sb : cs[0][cc * 8 + k], inv = BLOCK ? ib : cs[1][cc * 8 + k];
+            const float s = BLOCK ? sb.s : cs[0][cc * 8 + k];
+            const float inv = BLOCK ? sb.inv : cs[1][cc * 8 + k];
             turn[turn_word(cc * 8 + k, rr)] = f32x4_to_e4m3x4(
-                div_by_scale(v[0][k], s, inv), div_by_scale(v[1][k], s, inv),
-                div_by_scale(v[2][k], s, inv), div_by_scale(v[3][k], s, inv));
+                div_by(v[0][k], s, inv), div_by(v[1][k], s, inv),
+                div_by(v[2][k], s, inv), div_by(v[3][k], s, inv));
         }
         __syncthreads();
         const int64_t pitch = fp8_pitch(a.R);

@@ -124,11 +124,11 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
             const uint32_t b = abs_bits(h.v[c][i]);
             m = b > m ? b : m;
         }
-        const float s = fp8_scale(row16_umax(m));
+        const BlockScale b = fp8_scale(row16_umax(m));
         if (j < pitch && t < a.T) {
-            *(uint2 *)(a.q + t * pitch + j) = quant8(h.v[c], s, 1.f / s);
+            *(uint2 *)(a.q + t * pitch + j) = quant8(h.v[c], b);
             if ((lane & 15) == 0)
-                a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = s;
+                a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = b.s;
         }
     }
 }
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
     constexpr int NT = bwd_threads(LPR), RPB = NT / LPR, NW = NT / 64;
     constexpr int COLS = 8 * LPR * C;
     __shared__ float buf[2][2][NW];
-    __shared__ float lds[RPB > 1 ? COLS : 1]; // the rows' dgain sums
+    __shared__ __attribute__((aligned(16))) float lds[RPB > 1 ? RPB : 1][RPB > 1 ? COLS : 4];
     const int lane = row_lane<LPR>();
     const int row = (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
     float acc[C][8];
@@ -206,24 +206,29 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
         }
         h.store(row_ptr(a.dh, a.dtdh, a.lddh, t), a.dtdh, d, lane);
     }
-    // the rows' sums, added in row order
+    // the row slots' sums, added in slot order
     float *part = a.part + (int64_t)blockIdx.x * a.d;
 #pragma unroll
-    for (int q = 0; q < RPB; ++q) {
-        if (q)
-            __syncthreads();
-        if (row == q) {
+    for (int c = 0; c < C; ++c) {
+        const int j = 8 * (lane + LPR * c);
+        if constexpr (RPB > 1) {
+            *(floatx4_t *)&lds[row][j] = floatx4_t{acc[c][0], acc[c][1], acc[c][2], acc[c][3]};
+            *(floatx4_t *)&lds[row][j + 4] = floatx4_t{acc[c][4], acc[c][5], acc[c][6], acc[c][7]};
+        } else {
 #pragma unroll
-            for (int c = 0; c < C; ++c)
+            for (int i = 0; i < 8; ++i)
+                if (j + i < a.d)
+                    part[j + i] = acc[c][i];
+        }
+    }
+    if constexpr (RPB > 1) {
+        __syncthreads();
+        for (int j = threadIdx.x; j < a.d; j += NT) {
+            float v = lds[0][j];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = 8 * (lane + LPR * c) + i;
-                    const float v = q ? lds[j] + acc[c][i] : acc[c][i];
-                    if (q < RPB - 1)
-                        lds[j] = v;
-                    else if (j < a.d)
-                        part[j] = v;
-                }
+            for (int q = 1; q < RPB; ++q)
+                v += lds[q][j];
+            part[j] = v;
         }
     }
 }
@@ -268,14 +273,13 @@ int row_lanes(int d)
     return l;
 }
 
-// Workgroups (and partial rows of dgain) of the backward: two for each CU, and
-// for few rows one for every four turns of its row slots. A single one writes
-// dgain itself.
+// Workgroups (and partial rows of dgain) of the backward: one for rows that
+// take at most four turns (it writes dgain itself), else up to two for each CU.
 int bwd_groups(int T, int d)
 {
     const int lpr = row_lanes(d), rpb = bwd_threads(lpr) / lpr;
-    const int64_t g = ((int64_t)T + 4 * rpb - 1) / (4 * rpb);
-    return g < BWD_WG ? (int)g : BWD_WG;
+    const int64_t g = ((int64_t)T + rpb - 1) / rpb;
+    return g <= 4 ? (g > 0) : g < BWD_WG ? (int)g : BWD_WG;
 }
 
 template <int LPR, int C, bool RAG> void fwd_one(const FwdArgs &a, hipStream_t s)
