@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -137,7 +138,7 @@ def load() -> ctypes.CDLL:
     L.hybrid_fwd_workspace_bytes.restype = S
     L.hybrid_bwd_workspace_bytes.argtypes = [ctypes.c_int, I, I, I, I, I]
     L.hybrid_bwd_workspace_bytes.restype = S
-    M, Q, F = ctypes.POINTER(MatC), ctypes.POINTER(Fp8C), ctypes.c_float
+    M, Q, F = P, P, ctypes.c_float  # structures as packed bytes (_pack_mat, _pack_fp8)
     L.twell_rmsnorm_fwd.argtypes = [M, M, P, ctypes.c_int, F, M, M, Q, P, P]
     L.twell_rmsnorm_bwd.argtypes = [M, M, P, ctypes.c_int, F, M, M, P, P, S, P, P]
     L.twell_rmsnorm_bwd_workspace_bytes.argtypes = [I, I]
@@ -285,6 +286,11 @@ def _x2(x, name="x"):
 
 def _stream(device) -> c_p:
     return c_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+# the same stream's handle for a device's number, without building a Stream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 @dataclass
@@ -609,37 +615,68 @@ def empty_fp8(rows, cols, block_rows, device) -> Fp8:
                cols, block_rows)
 
 
-def _check_fp8(m, name, rows=None, cols=None):
+# These calls are short enough on the GPU for their arguments' checks to be
+# what they cost: the structures are packed as bytes (MatC and Fp8C, a third of
+# the time of building them), and the usual case of every check is one test.
+_pack_mat = struct.Struct("iiqi4xP").pack
+_pack_fp8 = struct.Struct("iii4xPP").pack
+assert struct.calcsize("iiqi4xP") == ctypes.sizeof(MatC)
+assert struct.calcsize("iii4xPP") == ctypes.sizeof(Fp8C)
+_DT = {torch.float32: TWELL_F32, torch.bfloat16: TWELL_BF16}
+
+
+def _check_fp8(m, name, rows=None, cols=None) -> bytes:
+    """m's structure, of a well-formed Fp8 [rows][cols]."""
     if not isinstance(m, Fp8):
         raise TwellError(f"{name}: expected an Fp8")
-    if m.block_rows not in (1, FP8_BLOCK):
-        raise TwellError(f"{name}.block_rows: {m.block_rows}, expected 1 or {FP8_BLOCK}")
-    if not isinstance(m.q, torch.Tensor) or m.q.dim() != 2:
+    q, s, br = m.q, m.scale, m.block_rows
+    if br not in (1, FP8_BLOCK):
+        raise TwellError(f"{name}.block_rows: {br}, expected 1 or {FP8_BLOCK}")
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise TwellError(f"{name}.q: expected a [rows][cols up to 128] tensor")
-    rows = m.q.shape[0] if rows is None else rows
-    cols = m.cols if cols is None else cols
-    if m.cols != cols:
+    if rows is None:
+        rows = q.shape[0]
+    if cols is not None and m.cols != cols:
         raise TwellError(f"{name}: {m.cols} columns, expected {cols}")
+    cols = m.cols
     nb = -(-cols // FP8_BLOCK)
-    _req(m.q, f"{name}.q", (rows, nb * FP8_BLOCK), torch.float8_e4m3fn)
-    _req(m.scale, f"{name}.scale", (nb, -(-rows // m.block_rows)), torch.float32)
+    _req(q, f"{name}.q", (rows, nb * FP8_BLOCK), torch.float8_e4m3fn)
+    _req(s, f"{name}.scale", (nb, -(-rows // br)), torch.float32)
+    return _pack_fp8(rows, cols, br, q.data_ptr(), s.data_ptr())
 
 
-def _mat(t, name, shape=None, dtype=None) -> MatC:
-    """A [rows][cols] float32 or bfloat16 tensor whose columns are
-    consecutive; its rows may be any stride apart (a slice of columns)."""
+def _mat(t, name, rows=None, cols=None, dtype=None):
+    """(structure, rows, cols) of a [rows][cols] float32 or bfloat16 tensor
+    whose columns are consecutive; its rows may be any stride apart (a slice
+    of columns)."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise TwellError(f"{name}: expected a [rows][cols] tensor")
     r, c = t.shape
-    if shape is not None and (r, c) != tuple(shape):
-        raise TwellError(f"{name}: shape {(r, c)}, expected {tuple(shape)}")
-    dt = _dt(t)
-    if dtype is not None and t.dtype != dtype:
-        raise TwellError(f"{name}: dtype {t.dtype}, expected {dtype}")
     ld, sc = t.stride()
+    tdt = t.dtype
+    dt = _DT.get(tdt)
+    if rows is not None and (r != rows or c != cols):
+        raise TwellError(f"{name}: shape {(r, c)}, expected {(rows, cols)}")
+    if dt is None:
+        raise TwellError(f"unsupported dtype {tdt}")
+    if dtype is not None and tdt != dtype:
+        raise TwellError(f"{name}: dtype {tdt}, expected {dtype}")
     if (sc != 1 and c > 1) or (r > 1 and ld < c):
         raise TwellError(f"{name}: columns must be consecutive and rows must not overlap")
-    return MatC(r, c, max(ld, c) if r <= 1 else ld, dt, t.data_ptr())
+    return _pack_mat(r, c, ld if r > 1 else c, dt, t.data_ptr()), r, c
+
+
+def _new_mat(rows, cols, dtype, device):
+    """A new contiguous tensor and its structure."""
+    t = torch.empty((rows, cols), dtype=dtype, device=device)
+    if dtype not in _DT:
+        raise TwellError(f"unsupported dtype {dtype}")
+    return t, _pack_mat(rows, cols, cols, _DT[dtype], t.data_ptr())
+
+
+def _new_fp8(rows, cols, block_rows, device):
+    m = empty_fp8(rows, cols, block_rows, device)
+    return m, _pack_fp8(rows, cols, block_rows, m.q.data_ptr(), m.scale.data_ptr())
 
 
 def _gain(gain, d):
@@ -649,40 +686,56 @@ def _gain(gain, d):
     return _dt(gain)
 
 
+def _gpu(named: dict) -> int:
+    """The number of the one GPU that every given tensor lives on."""
+    dev = -1
+    for t in named.values():
+        if t is not None:
+            i = t.get_device()
+            if i < 0 or (dev >= 0 and i != dev):
+                _on_gpu(*named.items())  # names the tensor
+            dev = i
+    return dev
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def rmsnorm_fwd(x, gain, residual=None, eps: float = 1e-6, out_dtype=torch.bfloat16, h=None,
                 out=None, timing: KernelTimer | None = None):
     """h = residual + x and its root-mean-square norm n times gain; returns
     (n, h). n is a tensor of out_dtype (float32 or bfloat16), or an Fp8 for
     float8_e4m3fn; h has residual's dtype (without a residual h is x). h and
     out, if given, are written (h may be residual or x, out may be x, in place)."""
-    mx = _mat(x, "x")
-    T, d = mx.rows, mx.cols
+    mx, T, d = _mat(x, "x")
     gdt = _gain(gain, d)
     mr = mh = mn = m8 = None
+    on = {"x": x, "gain": gain}
     if residual is not None:
-        mr = _mat(residual, "residual", (T, d))
+        mr = _mat(residual, "residual", T, d)[0]
+        on["residual"] = residual
         if h is None:
-            h = torch.empty((T, d), dtype=residual.dtype, device=x.device)
-        mh = _mat(h, "h", (T, d), residual.dtype)
+            h, mh = _new_mat(T, d, residual.dtype, x.device)
+        else:
+            mh = _mat(h, "h", T, d, residual.dtype)[0]
+            on["h"] = h
     elif h is not None:
         raise TwellError("h: written only with a residual")
     if out_dtype == torch.float8_e4m3fn:
         if out is None:
-            out = empty_fp8(T, d, 1, x.device)
+            out, m8 = _new_fp8(T, d, 1, x.device)
         else:
-            _check_fp8(out, "out", T, d)
-        m8 = out.c()
-        on = (("out.q", out.q), ("out.scale", out.scale))
+            m8 = _check_fp8(out, "out", T, d)
+            on["out.q"], on["out.scale"] = out.q, out.scale
+    elif out is None:
+        out, mn = _new_mat(T, d, out_dtype, x.device)
     else:
-        if out is None:
-            out = torch.empty((T, d), dtype=out_dtype, device=x.device)
-        mn = _mat(out, "out", (T, d), out_dtype)
-        on = (("out", out),)
-    dev = _on_gpu(("x", x), ("gain", gain), ("residual", residual), ("h", h), *on)
-    ref = ctypes.byref
-    _check(load().twell_rmsnorm_fwd(ref(mx), mr and ref(mr), _ptr(gain), gdt, eps,
-                                    mh and ref(mh), mn and ref(mn), m8 and ref(m8),
-                                    _timing(timing), _stream(dev)), "twell_rmsnorm_fwd")
+        mn = _mat(out, "out", T, d, out_dtype)[0]
+        on["out"] = out
+    dev = _gpu(on)
+    _check(load().twell_rmsnorm_fwd(mx, mr, gain.data_ptr(), gdt, eps, mh, mn, m8,
+                                    _timing(timing), _raw_stream(dev)), "twell_rmsnorm_fwd")
     return out, (x if residual is None else h)
 
 
@@ -694,25 +747,24 @@ def rmsnorm_bwd(dn, h, gain, dres=None, eps: float = 1e-6, dh_dtype=torch.float3
                 dgain=None, workspace=None, timing: KernelTimer | None = None):
     """Gradients of rmsnorm_fwd from dn: (dh, dgain). h is the stream the
     forward normed (its h), dres the gradient reaching h past the norm."""
-    md = _mat(dn, "dn")
-    T, d = md.rows, md.cols
-    mh = _mat(h, "h", (T, d))
+    md, T, d = _mat(dn, "dn")
+    mh = _mat(h, "h", T, d)[0]
     gdt = _gain(gain, d)
-    mr = None if dres is None else _mat(dres, "dres", (T, d))
+    mr = None if dres is None else _mat(dres, "dres", T, d)[0]
     if dh is None:
-        dh = torch.empty((T, d), dtype=dh_dtype, device=dn.device)
-    mo = _mat(dh, "dh", (T, d))
+        dh, mo = _new_mat(T, d, dh_dtype, dn.device)
+    else:
+        mo = _mat(dh, "dh", T, d)[0]
     if dgain is None:
         dgain = torch.empty(d, dtype=torch.float32, device=dn.device)
     _req(dgain, "dgain", (d,), torch.float32)
-    dev = _on_gpu(("dn", dn), ("h", h), ("gain", gain), ("dres", dres), ("dh", dh),
-                  ("dgain", dgain), ("workspace", workspace))
-    workspace = _ws(workspace, rmsnorm_bwd_workspace_bytes(T, d), dev)
-    nbytes = 0 if workspace is None else workspace.numel()
-    ref = ctypes.byref
-    _check(load().twell_rmsnorm_bwd(ref(md), ref(mh), _ptr(gain), gdt, eps, mr and ref(mr),
-                                    ref(mo), _ptr(dgain), _ptr(workspace), nbytes,
-                                    _timing(timing), _stream(dev)), "twell_rmsnorm_bwd")
+    _ws_form(workspace)
+    dev = _gpu({"dn": dn, "h": h, "gain": gain, "dres": dres, "dh": dh, "dgain": dgain,
+                "workspace": workspace})
+    workspace = _ws(workspace, rmsnorm_bwd_workspace_bytes(T, d), dn.device)
+    _check(load().twell_rmsnorm_bwd(md, mh, gain.data_ptr(), gdt, eps, mr, mo, dgain.data_ptr(),
+                                    _at(workspace), 0 if workspace is None else workspace.numel(),
+                                    _timing(timing), _raw_stream(dev)), "twell_rmsnorm_bwd")
     return dh, dgain
 
 
@@ -720,32 +772,27 @@ def fp8_quant(x, block_rows: int = 1, layout: str = "rows", out: Fp8 | None = No
               out_t: Fp8 | None = None, timing: KernelTimer | None = None):
     """x in 8 bits with block scales; returns (of x, of its transpose), None
     for the one that layout ("rows", "cols" or "both") leaves out."""
-    mx = _mat(x, "x")
-    R, C = mx.rows, mx.cols
+    mx, R, C = _mat(x, "x")
     if layout not in ("rows", "cols", "both"):
         raise TwellError(f"layout: {layout!r}, expected 'rows', 'cols' or 'both'")
     if block_rows not in (1, FP8_BLOCK):
         raise TwellError(f"block_rows: {block_rows}, expected 1 or {FP8_BLOCK}")
-    on = []
-    if layout == "cols":
-        if out is not None:
-            raise TwellError("out: not written with layout 'cols'")
-    elif out is None:
-        out = empty_fp8(R, C, block_rows, x.device)
-    if layout == "rows":
-        if out_t is not None:
-            raise TwellError("out_t: not written with layout 'rows'")
-    elif out_t is None:
-        out_t = empty_fp8(C, R, block_rows, x.device)
-    for name, m, shape in (("out", out, (R, C)), ("out_t", out_t, (C, R))):
-        if m is not None:
-            _check_fp8(m, name, *shape)
-            if m.block_rows != block_rows:
-                raise TwellError(f"{name}: block_rows {m.block_rows}, expected {block_rows}")
-            on += [(name + ".q", m.q), (name + ".scale", m.scale)]
-    dev = _on_gpu(("x", x), *on)
-    c, ct = (None if m is None else ctypes.byref(m.c()) for m in (out, out_t))
-    _check(load().twell_fp8_quant(ctypes.byref(mx), c, ct, _timing(timing), _stream(dev)),
+    on, m = {"x": x}, {}
+    for name, t, skip, shape in (("out", out, "cols", (R, C)), ("out_t", out_t, "rows", (C, R))):
+        if layout == skip:
+            if t is not None:
+                raise TwellError(f"{name}: not written with layout {layout!r}")
+            m[name] = None, None
+        elif t is None:
+            m[name] = _new_fp8(*shape, block_rows, x.device)
+        else:
+            m[name] = t, _check_fp8(t, name, *shape)
+            if t.block_rows != block_rows:
+                raise TwellError(f"{name}: block_rows {t.block_rows}, expected {block_rows}")
+            on[name + ".q"], on[name + ".scale"] = t.q, t.scale
+    (out, mo), (out_t, mt) = m["out"], m["out_t"]
+    dev = _gpu(on)
+    _check(load().twell_fp8_quant(mx, mo, mt, _timing(timing), _raw_stream(dev)),
            "twell_fp8_quant")
     return out, out_t
 
@@ -760,20 +807,22 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=torch.bfloat16, fast_sums: bo
     bfloat16. Products are added in float32, or, with fast_sums, by the 8-bit
     matrix instruction at up to twice the rate (errors of about 2^-16 of the
     sum of the terms' sizes: right for a bfloat16 result, short for float32)."""
-    _check_fp8(a, "a")
-    _check_fp8(b, "b")
-    M, N, K = a.rows, b.rows, a.cols
+    ma, mb = _check_fp8(a, "a"), _check_fp8(b, "b")
+    M, N, K = a.q.shape[0], b.q.shape[0], a.cols
     if b.cols != K:
         raise TwellError(f"b: {b.cols} columns, a has {K}")
+    on = {"a.q": a.q, "a.scale": a.scale, "b.q": b.q, "b.scale": b.scale}
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a.q.device)
-    mo = _mat(out, "out", (M, N), out_dtype)
-    dev = _on_gpu(("a.q", a.q), ("a.scale", a.scale), ("b.q", b.q), ("b.scale", b.scale),
-                  ("out", out), ("workspace", workspace))
-    workspace = _ws(workspace, fp8_matmul_workspace_bytes(M, N, K), dev)
-    nbytes = 0 if workspace is None else workspace.numel()
-    ref = ctypes.byref
-    _check(load().twell_fp8_matmul(ref(a.c()), ref(b.c()), ref(mo),
-                                   SUMS_FP8 if fast_sums else SUMS_F32, _ptr(workspace), nbytes,
-                                   _timing(timing), _stream(dev)), "twell_fp8_matmul")
+        out, mo = _new_mat(M, N, out_dtype, a.q.device)
+    else:
+        mo = _mat(out, "out", M, N, out_dtype)[0]
+        on["out"] = out
+    if workspace is not None:
+        _ws_form(workspace)
+        on["workspace"] = workspace
+    dev = _gpu(on)
+    workspace = _ws(workspace, fp8_matmul_workspace_bytes(M, N, K), out.device)
+    _check(load().twell_fp8_matmul(ma, mb, mo, SUMS_FP8 if fast_sums else SUMS_F32,
+                                   _at(workspace), 0 if workspace is None else workspace.numel(),
+                                   _timing(timing), _raw_stream(dev)), "twell_fp8_matmul")
     return out

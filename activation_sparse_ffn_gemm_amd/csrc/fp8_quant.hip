@@ -41,7 +41,7 @@ DEVI int turn_word(int c, int rr)
 
 // ROWS: q of x, COLS: q of its transpose, BLOCK: 128 x 128 blocks.
 template <bool ROWS, bool COLS, bool BLOCK>
-__global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
+__global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
 {
     __shared__ uint32_t cmax[NW][TS]; // column amaxes of each wave's rows
     __shared__ __attribute__((aligned(16))) float cs[2][TS]; // the columns' scales and 1 / scales
