@@ -18,6 +18,8 @@
 // its second: a lane's four results then belong to one token and four
 // consecutive n. Which k a lane's 32 bytes are does not matter as long as
 // both operands agree, so each lane takes 32 consecutive bytes of its row.
+#include <cmath>
+
 #include "fp8.hpp"
 #include "ntgemm.hpp"
 
@@ -37,11 +39,6 @@ struct MmArgs {
     int parts, per; // parts, blocks of k in each
 };
 
-DEVI intx8_t frag32(const uint8_t *p)
-{
-    const uint4 a = ldg16(p), b = ldg16(p + 16);
-    return intx8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
 DEVI floatx4_t mfma_e4m3(intx8_t a, intx8_t b)
 {
     const floatx4_t zero = {0.f, 0.f, 0.f, 0.f};
@@ -87,7 +84,7 @@ template <> struct Frag<TWELL_SUMS_F32> {
 // ---------------------------------------------------------------- large products
 // One workgroup computes BM tokens x BN n. A block of 128 k is one step: its
 // 128-byte rows of both operands, and their scales, go straight from global
-// memory to LDS, two steps resident, each row's 16-byte chunks XOR-swizzled so
+// memory to LDS, NST steps resident, each row's 16-byte chunks XOR-swizzled so
 // that the 16 rows a fragment read touches lie on distinct banks. A wave owns
 // WN x WM of the tile: NI fragments of B rows by MI of A rows, 32 bytes a lane.
 //
@@ -97,27 +94,30 @@ template <> struct Frag<TWELL_SUMS_F32> {
 // - A fragment of B is read one row of products before its own.
 // - A product's four results are scaled into the accumulators three products
 //   later, when they have left the matrix unit.
-// - The next step's loads go out one by one beside the step's first products,
-//   into the stage that the step before has left.
+// - The loads of step + NST - 1 go out one by one beside the step's first
+//   products, into the stage that the step before has left.
 // - The step's one barrier stands before its last row of products. By then
 //   every read of its stage is done and the next stage's loads are in, so the
 //   next step's first fragments are read beside that last row.
-template <int BM_, int BN_, int WGM_, int WGN_> struct TileCfg {
-    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
+template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
     static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
     static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 16, NI = WN / 16;
     static constexpr int ROWS = BM + BN;                 // B rows first, then A rows
     static constexpr int WBB = BN / 8 / NWV, WBA = BM / 8 / NWV; // 1 KB loads (eight rows) a wave
     static constexpr int WB = WBB + WBA;
-    static constexpr int NSC = ROWS / 64;                // 64-scale loads: waves 0 .. NSC - 1
+    static constexpr int NSC = ROWS / 64;                // 64-scale loads: wave w load w % NSC
+    static constexpr int SYNC = (NI - 1) * MI;           // product at which a step's barrier is
+    static constexpr int LPS = (WB + 1 + SYNC - 1) / SYNC; // loads beside a product before it
     static constexpr int SCALES = ROWS * FP8_BLK;        // byte offset of a stage's scales
     static constexpr int STAGE = SCALES + ROWS * 4;
     static constexpr int OUTB = WM * (WN * 2 + 16) * NWV; // the epilogue's bf16 rows
-    static constexpr int LDS = 2 * STAGE > OUTB ? 2 * STAGE : OUTB;
+    static constexpr int LDS = NST * STAGE > OUTB ? NST * STAGE : OUTB;
     static_assert(BN % (8 * NWV) == 0 && BM % (8 * NWV) == 0 && BN % 64 == 0 && BM % 64 == 0 &&
                       NSC <= NWV, "whole loads");
     static_assert(WN <= FP8_BLK && FP8_BLK % WN == 0, "a wave's n share one 128-row scale block");
     static_assert(NI % 2 == 0, "two fragments of B in turn");
+    static_assert(NST >= 2 && (NST - 2) * (WB + 1) < 64, "loads in flight must fit vmcnt");
 };
 
 #pragma clang diagnostic push
@@ -143,9 +143,24 @@ DEVI void dma4(const float *base, uint32_t off, uint32_t lds, int kb, int kb1)
 }
 #pragma clang diagnostic pop
 
+// Waits until at most N of this wave's loads are in flight, or, where fewer
+// than `full` steps are left (fewer are in flight than N allows for), until
+// none is.
+template <int N> DEVI void wait_oldest(int left, int full)
+{
+    if constexpr (N == 0)
+        ng::wait_vm<0>();
+    else
+        asm volatile("s_cmp_lt_i32 %0, %1\n\ts_cbranch_scc1 .Lall%=\n\ts_waitcnt vmcnt(%2)\n\t"
+                     "s_branch .Ldone%=\n.Lall%=:\n\ts_waitcnt vmcnt(0)\n.Ldone%=:"
+                     :
+                     : "s"(left), "s"(full), "n"(N)
+                     : "scc");
+}
+
 // BLKB: B's scale block is 128 rows, so a wave's n share one scale per step.
 template <class C, int SUMS, bool BLKB>
-__global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
+__global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t L[C::LDS];
     // XCD-aware order: XCD k takes the k-th contiguous run of a grouped tile
@@ -178,14 +193,14 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
         const int last = g < C::WBB ? a.N - 1 - n0 : a.M - 1 - m0;
         off[g] = (uint32_t)min(r, last) * (uint32_t)a.pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
     }
-    const bool sisb = w * 64 < C::BN;
+    const int ws = w % C::NSC;
+    const bool sisb = ws * 64 < C::BN;
     const float *ssrc = sisb ? a.sb : a.sa;
     const int ns = sisb ? a.nsb : a.nsa;
-    const int srow = sisb ? min(n0 + w * 64 + lane, a.N - 1)
-                          : min(m0 + w * 64 - C::BN + lane, a.M - 1);
+    const int srow = sisb ? min(n0 + ws * 64 + lane, a.N - 1)
+                          : min(m0 + ws * 64 - C::BN + lane, a.M - 1);
     const uint32_t soff = (uint32_t)(srow / (sisb ? a.rb : a.ra)) * 4u;
     // load g of this wave (g == WB: its scales) for step kb into stage st
-    const int sb1 = __builtin_amdgcn_readfirstlane(w < C::NSC ? kb1 : INT_MIN);
     auto load = [&](int g, int kb, int st) {
         const uint32_t dst = lds0 + (uint32_t)st * C::STAGE;
         if (g < C::WBB)
@@ -194,7 +209,7 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
             dma16(srca + (int64_t)kb * FP8_BLK, off[g],
                   dst + C::BN * FP8_BLK + (w * C::WBA + g - C::WBB) * 1024, kb, kb1);
         else
-            dma4(ssrc + (int64_t)kb * ns, soff, dst + C::SCALES + w * 256, kb, sb1);
+            dma4(ssrc + (int64_t)kb * ns, soff, dst + C::SCALES + ws * 256, kb, kb1);
     };
 
     floatx4_t acc[C::NI][C::MI];
@@ -217,9 +232,11 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
     };
-    auto sync = [&] {
+    // the loads of the oldest step in flight are in, and every wave is here;
+    // left: steps from that one to the end
+    auto sync = [&](int left) {
         fence();
-        ng::wait_vm<0>();
+        wait_oldest<(C::NST - 2) * (C::WB + 1)>(left, C::NST - 1);
         __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0)
         __builtin_amdgcn_s_barrier();
         fence();
@@ -232,9 +249,11 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
     float sa[C::MI], sb = 1.f;
     floatx4_t sb4[2];
 #pragma unroll
-    for (int g = 0; g <= C::WB; ++g)
-        load(g, kb0, 0);
-    sync();
+    for (int k = 0; k < C::NST - 1; ++k)
+#pragma unroll
+        for (int g = 0; g <= C::WB; ++g)
+            load(g, kb0 + k, k);
+    sync(kb1 - kb0);
     rb[0] = frag(Bw);
     sb4[0] = *(const floatx4_t *)(sbw + q4 * 4);
 #pragma unroll
@@ -244,8 +263,11 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
     }
     if (BLKB)
         sb = sbw[0];
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const int st = (kb - kb0) & 1, cur = st * C::STAGE, nxt = C::STAGE - cur;
+    for (int kb = kb0, st = 0; kb < kb1; ++kb) {
+        const int free = st == 0 ? C::NST - 1 : st - 1; // the last step's stage
+        const int cur = st * C::STAGE;
+        st = st == C::NST - 1 ? 0 : st + 1;
+        const int nxt = st * C::STAGE;
         Frag<SUMS> fa[C::MI], fb;
         float s[C::MI];
 #pragma unroll
@@ -268,7 +290,7 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
             const int i = t / C::MI, j = t % C::MI;
             if (j == 0) {
                 if (i == C::NI - 1)
-                    sync();
+                    sync(kb1 - kb - 1);
                 fb.set(rb[i % RB]);
                 sbv[i & 1] = sb4[i & 1];
                 if (i < C::NI - 1) {
@@ -291,8 +313,9 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
                 ra[j] = frag(Aw + nxt + j * 16 * FP8_BLK);
                 sa[j] = *(const float *)((const uint8_t *)(saw + j * 16 + l16) + nxt);
             }
-            if (t <= C::WB)
-                load(t, kb + 1, st ^ 1);
+#pragma unroll
+            for (int g = t * C::LPS; g < (t + 1) * C::LPS && g <= C::WB; ++g)
+                load(g, kb + C::NST - 1, free);
             __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
@@ -361,93 +384,183 @@ __global__ __launch_bounds__(C::NT, 2) void fp8_mm_tile_kernel(MmArgs a)
     }
 }
 
-// ---------------------------------------------------------------- few tokens
-constexpr int WV = 8; // waves of a workgroup: each takes every eighth block of k
-
-// TB tiles of 16 tokens by 16 n per workgroup.
-template <int TB, int SUMS>
-__global__ __launch_bounds__(64 * WV) void fp8_mm_rows_kernel(MmArgs a)
+// out = the sum of the parts, in order; four n a thread.
+__global__ __launch_bounds__(256) void fp8_mm_join_kernel(MmArgs a)
 {
-    __shared__ floatx4_t part[WV][TB][64];
-    const int lane = threadIdx.x & 63, w = wave_id();
-    const int l16 = lane & 15, q4 = lane >> 4;
-    const int tiles_n = (a.N + 15) / 16;
-    const int n0 = (int)(blockIdx.x % tiles_n) * 16;
-    const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * (16 * TB);
-    const uint8_t *pb = a.qb + (int64_t)min(n0 + l16, a.N - 1) * a.pitch + q4 * 32;
-    const uint8_t *pa[TB];
-    int am[TB];
-    floatx4_t acc[TB];
+    const int64_t n4 = (a.N + 3) / 4, q = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (q >= n4 * a.M)
+        return;
+    const int64_t m = q / n4;
+    const int n = (int)(q % n4) * 4;
+    const float *p = a.part + m * a.N + n;
+    const int64_t stride = (int64_t)a.M * a.N;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if (n + 4 <= a.N) {
+        for (int i = 0; i < a.parts; ++i) {
+            const uint4 u = ldg16u(p + i * stride);
+            v[0] += __uint_as_float(u.x), v[1] += __uint_as_float(u.y);
+            v[2] += __uint_as_float(u.z), v[3] += __uint_as_float(u.w);
+        }
+    } else {
+        for (int i = 0; i < a.parts; ++i)
 #pragma unroll
-    for (int t = 0; t < TB; ++t) {
-        am[t] = (int)min(m0 + t * 16 + l16, (int64_t)a.M - 1);
-        pa[t] = a.qa + (int64_t)am[t] * a.pitch + q4 * 32;
-        acc[t] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+            for (int e = 0; e < 3; ++e)
+                if (n + e < a.N)
+                    v[e] += p[i * stride + e];
     }
-    int nb[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        nb[e] = min(n0 + q4 * 4 + e, a.N - 1) / a.rb;
-    for (int kb = w; kb < a.nkb; kb += WV) {
-        Frag<SUMS> fb;
-        fb.set(frag32(pb + (int64_t)kb * FP8_BLK));
-        float sb[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            sb[e] = a.sb[(int64_t)kb * a.nsb + nb[e]];
-#pragma unroll
-        for (int t = 0; t < TB; ++t) {
-            Frag<SUMS> fa;
-            fa.set(frag32(pa[t] + (int64_t)kb * FP8_BLK));
-            const float sa = a.sa[(int64_t)kb * a.nsa + am[t] / a.ra];
-            const floatx4_t p = Frag<SUMS>::mul(fb, fa);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[t][e] = fmaf(p[e], sa * sb[e], acc[t][e]);
-        }
-    }
-#pragma unroll
-    for (int t = 0; t < TB; ++t)
-        part[w][t][lane] = acc[t];
-    __syncthreads();
-    // wave w joins tile w's partial sums, in wave order
-    if (w >= TB)
-        return;
-    floatx4_t o = part[0][w][lane];
-#pragma unroll
-    for (int q = 1; q < WV; ++q)
-        o += part[q][w][lane];
-    const int64_t m = m0 + w * 16 + l16;
-    if (m >= a.M)
-        return;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int n = n0 + q4 * 4 + e;
-        if (n < a.N) {
+        if (n + e < a.N) {
             if (a.dto == TWELL_BF16)
-                ((uint16_t *)a.out)[m * a.ldo + n] = (uint16_t)f32x2_to_bf16x2(o[e], 0.f);
+                ((uint16_t *)a.out)[m * a.ldo + n + e] = (uint16_t)f32x2_to_bf16x2(v[e], 0.f);
             else
-                ((float *)a.out)[m * a.ldo + n] = o[e];
+                ((float *)a.out)[m * a.ldo + n + e] = v[e];
+        }
+}
+
+// ---------------------------------------------------------------- few tokens
+// A workgroup computes 16 NB n for 16 TB tokens, its WV waves taking every
+// WV-th block of k; their sums meet in LDS. A wave's rows of a block go to its
+// own piece of LDS, two blocks in turn, as whole 128-byte lines (eight adjacent
+// lanes a row): loaded straight into the fragments' registers, where adjacent
+// lanes are different rows, every lane is a request of its own, and 16 tokens
+// by 2304 n over 6144 took 8.1 us in place of 4.6. No barrier: a wave waits for
+// its own loads. The scales are staged SCB blocks of k at a time.
+template <int TB, int NB, int WV, int SCB, int SUMS>
+__global__ __launch_bounds__(64 * WV) void fp8_mm_rows_kernel(MmArgs a)
+{
+    constexpr int NF = NB + TB, STG = NF * 2048; // fragments of a block, B's first
+    constexpr int BUF = WV * 2 * STG;
+    static_assert(BUF >= WV * NB * TB * 1024, "the sums reuse the blocks' space");
+    __shared__ __attribute__((aligned(16))) uint8_t L[BUF];
+    __shared__ float ssa[SCB][16 * TB];
+    __shared__ __attribute__((aligned(16))) float ssb[SCB][16 * NB];
+    const int lane = threadIdx.x & 63, w = wave_id();
+    const int l16 = lane & 15, q4 = lane >> 4;
+    const int tiles_n = (a.N + 16 * NB - 1) / (16 * NB);
+    const int n0 = (int)(blockIdx.x % tiles_n) * (16 * NB);
+    const int m0 = (int)(blockIdx.x / tiles_n) * (16 * TB);
+    // load i of a block: eight rows of fragment i / 2, lane l the chunk of row
+    // l / 8 that the swizzle puts at byte 16 l. Rows past an operand read its
+    // last row; their outputs are dropped.
+    const uint8_t *srcb = a.qb + (int64_t)n0 * a.pitch, *srca = a.qa + (int64_t)m0 * a.pitch;
+    uint32_t off[2 * NF];
+#pragma unroll
+    for (int i = 0; i < 2 * NF; ++i) {
+        const int r = (i < 2 * NB ? i : i - 2 * NB) * 8 + lane / 8;
+        const int last = i < 2 * NB ? a.N - 1 - n0 : a.M - 1 - m0;
+        off[i] = (uint32_t)min(r, last) * (uint32_t)a.pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+    }
+    uint8_t *Lw = L + w * 2 * STG;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(ng::lds_u8 *)Lw;
+    auto fetch = [&](int kb, int st) {
+#pragma unroll
+        for (int i = 0; i < 2 * NF; ++i)
+            dma16((i < 2 * NB ? srcb : srca) + (int64_t)kb * FP8_BLK, off[i],
+                  lds0 + (uint32_t)(st * STG + i * 1024), kb, a.nkb);
+    };
+    floatx4_t acc[NB][TB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            acc[i][t] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    const int f0 = l16 * FP8_BLK + ((q4 ^ ((l16 >> 1) & 7)) << 4), f1 = f0 ^ 64;
+    auto frag = [&](const uint8_t *p) {
+        const uint4 u = *(const uint4 *)(p + f0), v = *(const uint4 *)(p + f1);
+        return intx8_t{(int)u.x, (int)u.y, (int)u.z, (int)u.w,
+                       (int)v.x, (int)v.y, (int)v.z, (int)v.w};
+    };
+    fetch(w, 0);
+    int st = 0;
+    for (int k0 = 0; k0 < a.nkb; k0 += SCB) {
+        const int nk = min(SCB, a.nkb - k0);
+        if (k0)
+            __syncthreads(); // the last scales are used
+        for (int q = threadIdx.x; q < nk * 16 * TB; q += 64 * WV)
+            ssa[q / (16 * TB)][q % (16 * TB)] =
+                a.sa[(int64_t)(k0 + q / (16 * TB)) * a.nsa +
+                     min(m0 + q % (16 * TB), a.M - 1) / a.ra];
+        for (int q = threadIdx.x; q < nk * 16 * NB; q += 64 * WV)
+            ssb[q / (16 * NB)][q % (16 * NB)] =
+                a.sb[(int64_t)(k0 + q / (16 * NB)) * a.nsb +
+                     min(n0 + q % (16 * NB), a.N - 1) / a.rb];
+        __syncthreads();
+        static_assert(SCB % WV == 0, "a wave's blocks go on into the next scales");
+        for (int kc = w; kc < nk; kc += WV, st ^= 1) {
+            // the other piece was read a block ago; its loads, then this one's wait
+            fetch(k0 + kc + WV, st ^ 1);
+            if (k0 + kc + WV < a.nkb)
+                ng::wait_vm<2 * NF>();
+            else
+                ng::wait_vm<0>();
+            asm volatile("" ::: "memory");
+            const uint8_t *S = Lw + st * STG;
+            Frag<SUMS> fb[NB];
+            floatx4_t sb[NB];
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                fb[i].set(frag(S + i * 2048));
+                sb[i] = *(const floatx4_t *)&ssb[kc][i * 16 + q4 * 4];
+            }
+#pragma unroll
+            for (int t = 0; t < TB; ++t) {
+                Frag<SUMS> fa;
+                fa.set(frag(S + (NB + t) * 2048));
+                const float sa = ssa[kc][t * 16 + l16];
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    const floatx4_t p = Frag<SUMS>::mul(fb[i], fa);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[i][t][e] = fmaf(p[e], sa * sb[i][e], acc[i][t][e]);
+                }
+            }
+            // the reads are done before the piece is loaded again
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            asm volatile("" ::: "memory");
+        }
+    }
+    __syncthreads();
+    floatx4_t(*part)[NB * TB][64] = (floatx4_t(*)[NB * TB][64])L;
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            part[w][i * TB + t][lane] = acc[i][t];
+    __syncthreads();
+    // tile q's partial sums are joined by wave q % WV, in wave order
+    for (int q = w; q < NB * TB; q += WV) {
+        floatx4_t o = part[0][q][lane];
+#pragma unroll
+        for (int u = 1; u < WV; ++u)
+            o += part[u][q][lane];
+        const int m = m0 + q % TB * 16 + l16;
+        if (m >= a.M)
+            continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int n = n0 + q / TB * 16 + q4 * 4 + e;
+            if (n < a.N) {
+                if (a.dto == TWELL_BF16)
+                    ((uint16_t *)a.out)[m * a.ldo + n] = (uint16_t)f32x2_to_bf16x2(o[e], 0.f);
+                else
+                    ((float *)a.out)[m * a.ldo + n] = o[e];
+            }
         }
     }
 }
 
-template <int SUMS> void launch_rows(const MmArgs &a, hipStream_t s)
+template <int TB, int NB, int WV, int SCB, int SUMS> void rows_one(const MmArgs &a, hipStream_t s)
 {
-    const int64_t tn = (a.N + 15) / 16;
-    const int tb = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-    const dim3 grid((uint32_t)(tn * ((a.M + 16 * tb - 1) / (16 * tb))));
-    if (tb == 1)
-        fp8_mm_rows_kernel<1, SUMS><<<grid, 64 * WV, 0, s>>>(a);
-    else if (tb == 2)
-        fp8_mm_rows_kernel<2, SUMS><<<grid, 64 * WV, 0, s>>>(a);
-    else
-        fp8_mm_rows_kernel<4, SUMS><<<grid, 64 * WV, 0, s>>>(a);
+    const int64_t tn = (a.N + 16 * NB - 1) / (16 * NB);
+    const dim3 grid((uint32_t)(tn * ((a.M + 16 * TB - 1) / (16 * TB))));
+    fp8_mm_rows_kernel<TB, NB, WV, SCB, SUMS><<<grid, 64 * WV, 0, s>>>(a);
 }
-
-using T256 = TileCfg<256, 256, 4, 2>; // waves of 64 tokens x 128 n
-using T192 = TileCfg<192, 256, 4, 2>; // waves of 48 x 128
-using T128 = TileCfg<128, 128, 2, 2>; // waves of 64 x 64
+using T256 = TileCfg<256, 256, 4, 2, 2>; // waves of 64 tokens x 128 n
+using T192 = TileCfg<192, 256, 4, 2, 2>; // waves of 48 x 128
+using T128 = TileCfg<128, 128, 2, 4, 3>; // waves of 64 x 32
+using T64 = TileCfg<64, 128, 2, 4, 3>;   // waves of 32 x 32
 
 template <class C, int SUMS> void launch_tile(const MmArgs &a, hipStream_t s)
 {
@@ -460,24 +573,85 @@ template <class C, int SUMS> void launch_tile(const MmArgs &a, hipStream_t s)
         fp8_mm_tile_kernel<C, SUMS, false><<<grid, C::NT, 0, s>>>(a);
 }
 
-template <int SUMS> void launch_sums(const MmArgs &a, hipStream_t s)
+// Which kernel takes a product, and in how many parts of the contraction: the
+// least of the times that these measured figures give (us; they order the
+// kernels, no more). A tile kernel runs a tile per CU at a time, a step of 128 k
+// at `step` and `tile` for its beginning and end; full sums cost what widening
+// and the bfloat16 instruction do. Parts add a second launch and the partial
+// sums' way through memory. A rows kernel's wave takes 0.15 for each fragment
+// of a block of k (its loads' issue), unless all the workgroups' reads together
+// pass what the L2s serve (12 MB a us).
+enum Kernel { ROWS_1_1, ROWS_1_2, ROWS_2_2, ROWS_2_2_8, TILE_64, TILE_128, TILE_BIG };
+struct Plan {
+    Kernel k;
+    int parts, per; // parts of the contraction, blocks of k in each
+};
+
+Plan plan(int M, int N, int nkb, int sums)
 {
-    const int64_t t256 = (int64_t)((a.N + 255) / 256) * ((a.M + 255) / 256);
-    if (a.M <= 64)
-        launch_rows<SUMS>(a, s);
-    else if (t256 >= 128) {
-        if constexpr (SUMS == TWELL_SUMS_FP8)
-            launch_tile<T256, SUMS>(a, s);
-        else
-            launch_tile<T192, SUMS>(a, s);
+    const bool full = sums == TWELL_SUMS_F32;
+    Plan best = {TILE_BIG, 1, nkb};
+    double least = 1e300;
+    auto up = [](double a, double b) { return ceil(a / b); };
+    auto offer = [&](Kernel k, int parts, double t) {
+        if (t < least)
+            least = t, best = {k, parts, (nkb + parts - 1) / parts};
+    };
+    const struct {
+        Kernel k;
+        int tb, nb, wv, occ; // occ: workgroups that a CU runs in the time of one
+    } rows[] = {{ROWS_1_1, 1, 1, 8, 1}, {ROWS_1_2, 1, 2, 8, 1}, {ROWS_2_2, 2, 2, 4, 2},
+                {ROWS_2_2_8, 2, 2, 8, 1}};
+    for (const auto &r : rows) {
+        const double wg = up(M, 16 * r.tb) * up(N, 16 * r.nb);
+        const double lat = up(wg, 256 * r.occ) * (up(nkb, r.wv) * 0.15 * (r.tb + r.nb) + 0.8);
+        const double mem = wg * 16 * (r.tb + r.nb) * nkb * FP8_BLK / 12e6;
+        offer(r.k, 1, 2.0 + (lat > mem ? lat : mem));
     }
+    const struct {
+        Kernel k;
+        int bm, bn;
+        double step, tile;
+    } tiles[] = {{TILE_64, 64, 128, full ? 0.62 : 0.37, 1.5},
+                 {TILE_128, 128, 128, full ? 1.3 : 0.5, 2.5},
+                 {TILE_BIG, full ? 192 : 256, 256, full ? 2.3 : 1.52, 5.5}};
+    for (const auto &c : tiles)
+        for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
+            const double wg = up(M, c.bm) * up(N, c.bn) * parts;
+            const double join = parts == 1 ? 0. : 3.0 + (double)parts * M * N * 8 / 4e6;
+            offer(c.k, parts, 2.6 + up(wg, 256) * (up(nkb, parts) * c.step + c.tile) + join);
+        }
+    best.parts = best.per ? (nkb + best.per - 1) / best.per : 1;
+    return best;
+}
+
+template <int SUMS> void launch_sums(const MmArgs &a, Kernel k, hipStream_t s)
+{
+    switch (k) {
+    case ROWS_1_1: return rows_one<1, 1, 8, 64, SUMS>(a, s);
+    case ROWS_1_2: return rows_one<1, 2, 8, 64, SUMS>(a, s);
+    case ROWS_2_2: return rows_one<2, 2, 4, 64, SUMS>(a, s);
+    case ROWS_2_2_8: return rows_one<2, 2, 8, 32, SUMS>(a, s);
+    case TILE_64: return launch_tile<T64, SUMS>(a, s);
+    case TILE_128: return launch_tile<T128, SUMS>(a, s);
+    case TILE_BIG: break;
+    }
+    // full sums hold the widened fragments too: 256 x 256 would not fit the registers
+    if constexpr (SUMS == TWELL_SUMS_FP8)
+        launch_tile<T256, SUMS>(a, s);
     else
-        launch_tile<T128, SUMS>(a, s);
+        launch_tile<T192, SUMS>(a, s);
 }
 
 } // namespace
 
-size_t fp8_mm_workspace(int M, int N, int K) { return 0; }
+size_t fp8_mm_workspace(int M, int N, int K)
+{
+    const int nkb = fp8_blocks(K);
+    const int a = plan(M, N, nkb, TWELL_SUMS_FP8).parts, b = plan(M, N, nkb, TWELL_SUMS_F32).parts;
+    const int parts = a > b ? a : b;
+    return parts > 1 ? (size_t)parts * M * N * 4 : 0;
+}
 
 hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out,
                          int sums, void *ws, twell_timing_t *timing, hipStream_t s)
@@ -490,11 +664,17 @@ hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell
     a.ra = A->block_rows, a.rb = B->block_rows;
     a.nsa = (a.M + a.ra - 1) / a.ra, a.nsb = (a.N + a.rb - 1) / a.rb;
     Timer tm(timing, s);
-    a.parts = 1, a.per = a.nkb;
+    const Plan p = plan(a.M, a.N, a.nkb, sums);
+    a.parts = p.parts, a.per = p.per, a.part = (float *)ws;
     if (sums == TWELL_SUMS_FP8)
-        launch_sums<TWELL_SUMS_FP8>(a, s);
+        launch_sums<TWELL_SUMS_FP8>(a, p.k, s);
     else
-        launch_sums<TWELL_SUMS_F32>(a, s);
+        launch_sums<TWELL_SUMS_F32>(a, p.k, s);
     tm.mark("fp8_mm");
+    if (a.parts > 1) {
+        const int64_t q = (int64_t)((a.N + 3) / 4) * a.M;
+        fp8_mm_join_kernel<<<(uint32_t)((q + 255) / 256), 256, 0, s>>>(a);
+        tm.mark("fp8_mm_join");
+    }
     return hipGetLastError();
 }
