@@ -247,7 +247,7 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
     constexpr int RB = SUMS == TWELL_SUMS_FP8 ? 2 : 1;
     intx8_t rb[RB], ra[C::MI];
     float sa[C::MI], sb = 1.f;
-    floatx4_t sb4[2];
+    floatx4_t sb4[2]; // B's scales of this and the next row of products
 #pragma unroll
     for (int k = 0; k < C::NST - 1; ++k)
 #pragma unroll
@@ -275,14 +275,14 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
             fa[j].set(ra[j]);
             s[j] = BLKB ? sa[j] * sb : sa[j];
         }
-        constexpr int NP = C::NI * C::MI, LAG = 3;
+        constexpr int NP = C::NI * C::MI;
+        constexpr int LAG = SUMS == TWELL_SUMS_FP8 && C::MI > 2 ? 3 : 2;
         floatx4_t v[LAG + 1];
-        floatx4_t sbv[2];
         auto scale = [&](int t) { // product t into its accumulator
             const int i = t / C::MI, j = t % C::MI;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(v[t % (LAG + 1)][e], BLKB ? s[j] : s[j] * sbv[i & 1][e],
+                acc[i][j][e] = fmaf(v[t % (LAG + 1)][e], BLKB ? s[j] : s[j] * sb4[i & 1][e],
                                     acc[i][j][e]);
         };
 #pragma unroll
@@ -292,23 +292,21 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
                 if (i == C::NI - 1)
                     sync(kb1 - kb - 1);
                 fb.set(rb[i % RB]);
-                sbv[i & 1] = sb4[i & 1];
                 if (i < C::NI - 1) {
                     rb[(i + 1) % RB] = frag(Bw + cur + (i + 1) * 16 * FP8_BLK);
-                    if (!BLKB)
-                        sb4[(i + 1) & 1] =
-                            *(const floatx4_t *)((const uint8_t *)(sbw + (i + 1) * 16 + q4 * 4) + cur);
                 } else {
                     rb[0] = frag(Bw + nxt);
-                    if (!BLKB)
-                        sb4[0] = *(const floatx4_t *)((const uint8_t *)(sbw + q4 * 4) + nxt);
-                    else
+                    if (BLKB)
                         sb = *(const float *)((const uint8_t *)sbw + nxt);
                 }
             }
             v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j]);
             if (t >= LAG)
                 scale(t - LAG);
+            static_assert(LAG <= C::MI, "the last row's scales are used by then");
+            if (!BLKB && j == LAG - 1) // the row before is scaled: its place is free
+                sb4[(i + 1) & 1] = *(const floatx4_t *)((const uint8_t *)(
+                    sbw + (i < C::NI - 1 ? (i + 1) * 16 : 0) + q4 * 4) + (i < C::NI - 1 ? cur : nxt));
             if (i == C::NI - 1) {
                 ra[j] = frag(Aw + nxt + j * 16 * FP8_BLK);
                 sa[j] = *(const float *)((const uint8_t *)(saw + j * 16 + l16) + nxt);
@@ -562,15 +560,12 @@ using T192 = TileCfg<192, 256, 4, 2, 2>; // waves of 48 x 128
 using T128 = TileCfg<128, 128, 2, 4, 3>; // waves of 64 x 32
 using T64 = TileCfg<64, 128, 2, 4, 3>;   // waves of 32 x 32
 
-template <class C, int SUMS> void launch_tile(const MmArgs &a, hipStream_t s)
+template <class C, int SUMS, bool BLKB> void launch_tile(const MmArgs &a, hipStream_t s)
 {
     const int64_t total = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.M + C::BM - 1) / C::BM) *
                           a.parts;
     const dim3 grid((uint32_t)((total + NXCD - 1) / NXCD * NXCD));
-    if (a.rb == FP8_BLK)
-        fp8_mm_tile_kernel<C, SUMS, true><<<grid, C::NT, 0, s>>>(a);
-    else
-        fp8_mm_tile_kernel<C, SUMS, false><<<grid, C::NT, 0, s>>>(a);
+    fp8_mm_tile_kernel<C, SUMS, BLKB><<<grid, C::NT, 0, s>>>(a);
 }
 
 // Which kernel takes a product, and in how many parts of the contraction: the
@@ -581,16 +576,16 @@ template <class C, int SUMS> void launch_tile(const MmArgs &a, hipStream_t s)
 // sums' way through memory. A rows kernel's wave takes 0.15 for each fragment
 // of a block of k (its loads' issue), unless all the workgroups' reads together
 // pass what the L2s serve (12 MB a us).
-enum Kernel { ROWS_1_1, ROWS_1_2, ROWS_2_2, ROWS_2_2_8, TILE_64, TILE_128, TILE_BIG };
+enum Kernel { ROWS_1_1, ROWS_1_2, ROWS_2_2, ROWS_2_2_8, TILE_64, TILE_128, TILE_192, TILE_256 };
 struct Plan {
     Kernel k;
     int parts, per; // parts of the contraction, blocks of k in each
 };
 
-Plan plan(int M, int N, int nkb, int sums)
+Plan plan(int M, int N, int nkb, int sums, int rb)
 {
-    const bool full = sums == TWELL_SUMS_F32;
-    Plan best = {TILE_BIG, 1, nkb};
+    const bool full = sums == TWELL_SUMS_F32, blkb = rb == FP8_BLK;
+    Plan best = {TILE_64, 1, nkb};
     double least = 1e300;
     auto up = [](double a, double b) { return ceil(a / b); };
     auto offer = [&](Kernel k, int parts, double t) {
@@ -614,33 +609,42 @@ Plan plan(int M, int N, int nkb, int sums)
         double step, tile;
     } tiles[] = {{TILE_64, 64, 128, full ? 0.62 : 0.37, 1.5},
                  {TILE_128, 128, 128, full ? 1.3 : 0.5, 2.5},
-                 {TILE_BIG, full ? 192 : 256, 256, full ? 2.3 : 1.52, 5.5}};
-    for (const auto &c : tiles)
+                 {TILE_192, 192, 256, blkb ? 2.2 : 2.4, 5.5},
+                 {TILE_256, 256, 256, full ? 3.2 : 1.52, 5.5}};
+    for (const auto &c : tiles) {
+        // full sums hold their operands widened: with a scale for each row of B
+        // as well, 256 x 256 does not fit the registers (4.0 a step, 192 x 256
+        // 2.4). Fast sums have no use for 192 x 256.
+        if (c.k == (!full ? TILE_192 : blkb ? -1 : TILE_256))
+            continue;
         for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
             const double wg = up(M, c.bm) * up(N, c.bn) * parts;
             const double join = parts == 1 ? 0. : 3.0 + (double)parts * M * N * 8 / 4e6;
             offer(c.k, parts, 2.6 + up(wg, 256) * (up(nkb, parts) * c.step + c.tile) + join);
         }
+    }
     best.parts = best.per ? (nkb + best.per - 1) / best.per : 1;
     return best;
 }
 
-template <int SUMS> void launch_sums(const MmArgs &a, Kernel k, hipStream_t s)
+template <int SUMS, bool BLKB> void launch_sums(const MmArgs &a, Kernel k, hipStream_t s)
 {
     switch (k) {
     case ROWS_1_1: return rows_one<1, 1, 8, 64, SUMS>(a, s);
     case ROWS_1_2: return rows_one<1, 2, 8, 64, SUMS>(a, s);
     case ROWS_2_2: return rows_one<2, 2, 4, 64, SUMS>(a, s);
     case ROWS_2_2_8: return rows_one<2, 2, 8, 32, SUMS>(a, s);
-    case TILE_64: return launch_tile<T64, SUMS>(a, s);
-    case TILE_128: return launch_tile<T128, SUMS>(a, s);
-    case TILE_BIG: break;
+    case TILE_64: return launch_tile<T64, SUMS, BLKB>(a, s);
+    case TILE_128: return launch_tile<T128, SUMS, BLKB>(a, s);
+    case TILE_192:
+        if constexpr (SUMS == TWELL_SUMS_F32)
+            launch_tile<T192, SUMS, BLKB>(a, s);
+        return;
+    case TILE_256:
+        if constexpr (SUMS == TWELL_SUMS_FP8 || BLKB)
+            launch_tile<T256, SUMS, BLKB>(a, s);
+        return;
     }
-    // full sums hold the widened fragments too: 256 x 256 would not fit the registers
-    if constexpr (SUMS == TWELL_SUMS_FP8)
-        launch_tile<T256, SUMS>(a, s);
-    else
-        launch_tile<T192, SUMS>(a, s);
 }
 
 } // namespace
@@ -648,8 +652,12 @@ template <int SUMS> void launch_sums(const MmArgs &a, Kernel k, hipStream_t s)
 size_t fp8_mm_workspace(int M, int N, int K)
 {
     const int nkb = fp8_blocks(K);
-    const int a = plan(M, N, nkb, TWELL_SUMS_FP8).parts, b = plan(M, N, nkb, TWELL_SUMS_F32).parts;
-    const int parts = a > b ? a : b;
+    int parts = 1; // the most that any call of these sizes takes
+    for (int sums : {TWELL_SUMS_F32, TWELL_SUMS_FP8})
+        for (int rb : {1, FP8_BLK}) {
+            const int p = plan(M, N, nkb, sums, rb).parts;
+            parts = p > parts ? p : parts;
+        }
     return parts > 1 ? (size_t)parts * M * N * 4 : 0;
 }
 
@@ -664,13 +672,19 @@ hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell
     a.ra = A->block_rows, a.rb = B->block_rows;
     a.nsa = (a.M + a.ra - 1) / a.ra, a.nsb = (a.N + a.rb - 1) / a.rb;
     Timer tm(timing, s);
-    const Plan p = plan(a.M, a.N, a.nkb, sums);
+    const Plan p = plan(a.M, a.N, a.nkb, sums, a.rb);
     a.parts = p.parts, a.per = p.per, a.part = (float *)ws;
+    const bool blkb = a.rb == FP8_BLK;
     if (sums == TWELL_SUMS_FP8)
-        launch_sums<TWELL_SUMS_FP8>(a, p.k, s);
+        blkb ? launch_sums<TWELL_SUMS_FP8, true>(a, p.k, s)
+             : launch_sums<TWELL_SUMS_FP8, false>(a, p.k, s);
     else
-        launch_sums<TWELL_SUMS_F32>(a, p.k, s);
-    tm.mark("fp8_mm");
+        blkb ? launch_sums<TWELL_SUMS_F32, true>(a, p.k, s)
+             : launch_sums<TWELL_SUMS_F32, false>(a, p.k, s);
+    static const char *const names[] = {"fp8_mm_rows_1x1", "fp8_mm_rows_1x2", "fp8_mm_rows_2x2",
+                                        "fp8_mm_rows_2x2_8", "fp8_mm_tile64", "fp8_mm_tile128",
+                                        "fp8_mm_tile192", "fp8_mm_tile256"};
+    tm.mark(names[p.k]);
     if (a.parts > 1) {
         const int64_t q = (int64_t)((a.N + 3) / 4) * a.M;
         fp8_mm_join_kernel<<<(uint32_t)((q + 255) / 256), 256, 0, s>>>(a);

@@ -110,6 +110,9 @@ def test_quant_offsets_past_32_bits():
 
 
 # ---------------------------------------------------------------- product
+LARGE = [(2049, 4097, 1160), (2000, 5801, 392), (3001, 2305, 2312)]  # the large tiles, ragged
+
+
 def _fp8(rows, cols, block_rows, seed, integers=False):
     """A matrix on the CPU: (q, scale), zeros past cols."""
     g = torch.Generator().manual_seed(seed)
@@ -156,6 +159,38 @@ def test_product_integers(M, N, K, ra, rb):
     assert torch.equal(got.cpu().double(), want)
     assert torch.equal(fast, got) and torch.equal(fast_half, half)
     assert torch.equal(half.cpu(), want.float().to(BF))
+
+
+def test_every_kernel_on_integers():
+    """Sizes that between them take every kernel, whole and split
+    contractions, each result exact."""
+    names = set()
+    timer = tw.KernelTimer()
+    for M, N, K in ((1, 300, 700), (1, 4100, 300), (4100, 16, 300), (4100, 20, 1000),
+                    (4100, 100, 700), (2049, 1000, 700), (2000, 4100, 700), (2000, 6000, 700),
+                    (1, 16, 70000), (520, 20, 40000), (130, 6000, 8192)):
+        for rb in (128, 1):
+            a, b = _fp8(M, K, 1, 1, True), _fp8(N, K, rb, 2, True)
+            # float32 is exact here too: |sum| < 70000 * 16, in quarters
+            da, db = ref.dequant(*a, 1).float().to(DEV), ref.dequant(*b, rb).float().to(DEV)
+            want = da @ db.t()
+            A, B = _up(a, K, 1), _up(b, K, rb)
+            for fast in (False, True):
+                print("[case] fp8_matmul kernels", M, N, K, rb, fast, flush=True)
+                need = tw.fp8_matmul_workspace_bytes(M, N, K)
+                ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN
+                got = tw.fp8_matmul(A, B, out_dtype=F32, fast_sums=fast, workspace=ws)
+                half = tw.fp8_matmul(A, B, fast_sums=fast, timing=timer)
+                torch.cuda.synchronize()
+                names |= {(n, fast, rb) for n, _ in timer.collect()}
+                assert torch.equal(got, want)
+                assert torch.equal(half, want.to(BF))
+    seen = {n for n, _, _ in names}
+    assert seen == {"fp8_mm_rows_1x1", "fp8_mm_rows_1x2", "fp8_mm_rows_2x2", "fp8_mm_rows_2x2_8",
+                    "fp8_mm_tile64", "fp8_mm_tile128", "fp8_mm_tile192", "fp8_mm_tile256",
+                    "fp8_mm_join"}, seen
+    for fast, rb in ((True, 1), (True, 128), (False, 128)):
+        assert ("fp8_mm_tile256", fast, rb) in names, (fast, rb)
 
 
 @pytest.mark.parametrize("out", [F32, BF], ids=["f32", "bf16"])
@@ -320,3 +355,19 @@ def test_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs(), want))
+
+
+@pytest.mark.parametrize("rb", [128, 1])
+@pytest.mark.parametrize("M,N,K", LARGE)
+def test_product_large(M, N, K, rb):
+    print("[case] fp8_matmul large", M, N, K, rb, flush=True)
+    a, b = _fp8(M, K, 1, 3), _fp8(N, K, rb, 4)
+    da, db = ref.dequant(*a, 1).to(DEV), ref.dequant(*b, rb).to(DEV)
+    want, mag = da @ db.t(), da.abs() @ db.abs().t()
+    A, B = _up(a, K, 1), _up(b, K, rb)
+    k = 128 + 2 + -(-K // 128) + 64
+    for out in (F32, BF):
+        for fast in (False, True):
+            got = tw.fp8_matmul(A, B, out_dtype=out, fast_sums=fast)
+            tol = (k * ref.U32 + (ref.FAST if fast else 0)) * mag + ref.ustore(out) * want.abs()
+            ref.assert_within(got, want, tol, f"product {out} {fast}")
