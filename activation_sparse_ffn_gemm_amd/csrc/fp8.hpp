@@ -37,19 +37,10 @@ DEVI uint32_t row16_umax(uint32_t v)
 }
 DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// a / b rounded to float32 as a division rounds it, from inv = 1 / b: what
-// the product a inv is off by is one fused step away (a - q b is exact in the
-// fused multiply-add). Three instructions for a division's ten; nothing may
-// overflow or be infinite.
-DEVI float div_by(float a, float b, float inv)
-{
-    const float q = a * inv;
-    return fmaf(fmaf(-q, b, a), inv, q);
-}
-
-// Scale of a block from the bits of its largest absolute value, and 1 / scale
-// (the hardware's reciprocal and one Newton step). An infinite or NaN amax is
-// the scale itself, and makes 1 / scale NaN, so the block's q are NaN.
+// Scale of a block from the bits of its largest absolute value, and about
+// 1 / scale. The scale is amax / 448 rounded once: the product's error is one
+// fused step away (amax - q 448 is exact in the fused multiply-add). An
+// infinite or NaN amax is the scale itself, and makes 1 / scale NaN.
 struct BlockScale {
     float s, inv;
 };
@@ -57,20 +48,62 @@ DEVI BlockScale fp8_scale(uint32_t amax_bits)
 {
     const uint32_t lo = __float_as_uint(FP8_AMAX_MIN);
     const float amax = __uint_as_float(amax_bits > lo ? amax_bits : lo);
+    const float q = amax * (1.f / FP8_MAX);
     BlockScale b;
-    b.s = amax_bits >= 0x7f800000u ? amax : div_by(amax, FP8_MAX, 1.f / FP8_MAX);
+    b.s = amax_bits >= 0x7f800000u ? amax : fmaf(fmaf(-q, FP8_MAX, amax), 1.f / FP8_MAX, q);
     const float y = __builtin_amdgcn_rcpf(b.s);
-    b.inv = fmaf(fmaf(-b.s, y, 1.f), y, y);
+    b.inv = fmaf(fmaf(-b.s, y, 1.f), y, y); // NaN for an infinite scale
     return b;
 }
 
-// Eight values of one block -> eight bytes.
+// A float whose e4m3 rounding is that of v / s. Ties between e4m3 values, and
+// the values, have their low 19 bits clear; t is the float of that kind
+// nearest to the quotient, and v - t s, whose sign the fused multiply-add gives
+// exactly, says on which side of t the quotient lies. t moved by DELTA to that
+// side rounds like it: DELTA is more than half a unit of the largest quotients
+// and less than the distance of any other such t from a tie. (Rounding the
+// float quotient instead rounds twice: of bfloat16 values over a bfloat16
+// amax, one in 250 lies that near to a tie.)
+DEVI float e4m3_quotient(float v, BlockScale b)
+{
+    constexpr float DELTA = 0x1.8p-16f;
+    const float t = __uint_as_float((__float_as_uint(v * b.inv) + 0x40000u) & 0xfff80000u);
+    const float rest = fmaf(-t, b.s, v) * 0x1p100f;
+    return t + __builtin_amdgcn_fmed3f(rest, -DELTA, DELTA);
+}
+DEVI uint32_t quant4(const float *v, BlockScale b)
+{
+    return f32x4_to_e4m3x4(e4m3_quotient(v[0], b), e4m3_quotient(v[1], b),
+                           e4m3_quotient(v[2], b), e4m3_quotient(v[3], b));
+}
 DEVI uint2 quant8(const float *v, BlockScale b)
 {
+    return make_uint2(quant4(v, b), quant4(v + 4, b));
+}
+
+// Eight quotients in 64 bits, each to its nearest e4m3 value. Where a float32
+// of one lies on a tie (its low 19 bits clear: seldom) and the quotient does
+// not, the float is moved to the odd one of the two around the quotient, which
+// is no tie and has the same neighbours.
+DEVI uint2 quant8(const double *y)
+{
+    constexpr uint32_t TIE_BITS = 0x7ffff;
     float q[8];
+    uint32_t low = TIE_BITS;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q[i] = div_by(v[i], b.s, b.inv);
+    for (int i = 0; i < 8; ++i) {
+        q[i] = (float)y[i];
+        const uint32_t t = __float_as_uint(q[i]) & TIE_BITS;
+        low = t < low ? t : low;
+    }
+    if (low == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double r = (double)q[i];
+            if (y[i] != r)
+                q[i] = __uint_as_float((__float_as_uint(q[i]) - (fabs(y[i]) < fabs(r))) | 1u);
+        }
+    }
     return make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
                       f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
 }

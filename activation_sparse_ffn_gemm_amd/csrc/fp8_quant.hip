@@ -8,7 +8,8 @@
 // for: x is read once whatever is written. Row amaxes are DPP moves inside
 // the 16 lanes that share a row; column amaxes go over the thread's own rows,
 // the wave's other lanes and the workgroup's waves (LDS). The transpose is
-// turned in LDS as bytes. Bound by HBM: x in, q (and q_t) out; a thread holds
+// turned in LDS as bytes. bf16 stays two to a word until it is quantised, and
+// its maxima are taken two at a time. Bound by HBM: x in, q (and q_t) out; a thread holds
 // few elements so that several tiles are on a CU, one loading while another
 // stores (64 elements a thread took 19.1 us for 8192 x 2048 bf16 and its
 // transpose).
@@ -25,7 +26,7 @@ struct QuantArgs {
     uint8_t *q, *qt;
     float *s, *st;
     int64_t ld;
-    int R, C, dt, tiles_c;
+    int R, C, tiles_c;
 };
 
 DEVI uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
@@ -39,36 +40,82 @@ DEVI int turn_word(int c, int rr)
     return (c + (c >> 6)) * 32 + (rr ^ (((c >> 3) & 7) << 2));
 }
 
+// Eight consecutive elements of a row in 32-bit words, as they are stored, and
+// the running maximum of absolute values: as integers these order like the
+// floats (infinity above all, NaN above infinity). bf16 goes two to a word.
+template <int DT> struct Eight;
+template <> struct Eight<TWELL_BF16> {
+    static constexpr int W = 4;
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    uint32_t w[W];
+    DEVI void load(const void *row, int c, int C)
+    {
+        const uint16_t *p = (const uint16_t *)row + c;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (c + 8 <= C)
+            q = ldg16u(p);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        if (c < C && c + 8 > C) {
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (c + k < C)
+                    w[k / 2] |= (uint32_t)p[k] << (16 * (k & 1));
+        }
+    }
+    DEVI float operator[](int k) const { return k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]); }
+    DEVI uint32_t abs(int k) const { return w[k] & 0x7fff7fffu; }
+    // word by word, and over a word's elements (the bits of a float)
+    DEVI static uint32_t max2(uint32_t a, uint32_t b)
+    {
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, a),
+                                                                      __builtin_bit_cast(u16x2_t, b)));
+    }
+    DEVI static uint32_t top(uint32_t a) { return umax(a << 16, a & 0xffff0000u); }
+    DEVI static uint32_t elem_bits(uint32_t word, int k) { return k & 1 ? word & 0xffff0000u : word << 16; }
+};
+template <> struct Eight<TWELL_F32> {
+    static constexpr int W = 8;
+    uint32_t w[W];
+    DEVI void load(const void *row, int c, int C)
+    {
+        const float *p = (const float *)row + c;
+        uint4 q = make_uint4(0, 0, 0, 0), r = q;
+        if (c + 8 <= C)
+            q = ldg16u(p), r = ldg16u(p + 4);
+        w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+        w[4] = r.x, w[5] = r.y, w[6] = r.z, w[7] = r.w;
+        if (c < C && c + 8 > C) {
+#pragma unroll
+            for (int k = 0; k < 7; ++k)
+                if (c + k < C)
+                    w[k] = __float_as_uint(p[k]);
+        }
+    }
+    DEVI float operator[](int k) const { return __uint_as_float(w[k]); }
+    DEVI uint32_t abs(int k) const { return w[k] & 0x7fffffffu; }
+    DEVI static uint32_t max2(uint32_t a, uint32_t b) { return umax(a, b); }
+    DEVI static uint32_t top(uint32_t a) { return a; }
+    DEVI static uint32_t elem_bits(uint32_t word, int) { return word; }
+};
+
 // ROWS: q of x, COLS: q of its transpose, BLOCK: 128 x 128 blocks.
-template <bool ROWS, bool COLS, bool BLOCK>
-__global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
+template <int DT, bool ROWS, bool COLS, bool BLOCK>
+__global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
 {
-    __shared__ uint32_t cmax[NW][TS]; // column amaxes of each wave's rows
+    using E = Eight<DT>;
+    constexpr int W = E::W, EPW = 8 / W; // words of a thread's row, elements of a word
+    __shared__ uint32_t cmax[NW][TS / EPW]; // column amaxes of each wave's rows
     __shared__ __attribute__((aligned(16))) float cs[2][TS]; // the columns' scales and 1 / scales
     __shared__ __attribute__((aligned(16))) uint32_t turn[COLS ? (TS + 1) * 32 : 1];
     const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
     const int tr = blockIdx.x / a.tiles_c, tc = blockIdx.x % a.tiles_c;
     const int cc = tid & 15, rr = tid >> 4; // this thread's column chunk and row group
     const int r0 = tr * TS + rr * RPT, c0 = tc * TS + cc * 8;
-    float v[RPT][8];
+    E v[RPT];
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
+    for (int i = 0; i < RPT; ++i) { // rows past x are empty
         const int r = r0 + i;
-        const uint8_t *p = (const uint8_t *)row_ptr(a.x, a.dt, a.ld, r < a.R ? r : 0);
-        if (r < a.R && c0 + 8 <= a.C) {
-            if (a.dt == TWELL_BF16) {
-                elem<TWELL_BF16>::widen(ldg16u(p + 2 * (int64_t)c0), v[i]);
-            } else {
-                elem<TWELL_F32>::widen(ldg16u(p + 4 * (int64_t)c0), v[i]);
-                elem<TWELL_F32>::widen(ldg16u(p + 4 * (int64_t)c0 + 16), v[i] + 4);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[i][k] = r >= a.R || c0 + k >= a.C ? 0.f
-                          : a.dt == TWELL_BF16     ? elem<TWELL_BF16>::load1(p, c0 + k)
-                                                   : elem<TWELL_F32>::load1(p, c0 + k);
-        }
+        v[i].load(row_ptr(a.x, DT, a.ld, r < a.R ? r : 0), c0, r < a.R ? a.C : 0);
     }
     BlockScale sb = {};
     if constexpr (BLOCK) {
@@ -76,9 +123,9 @@ __global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                m = umax(m, abs_bits(v[i][k]));
-        m = row16_umax(m);
+            for (int k = 0; k < W; ++k)
+                m = E::max2(m, v[i].abs(k));
+        m = row16_umax(E::top(m));
 #pragma unroll
         for (int o = 16; o < 64; o <<= 1)
             m = umax(m, (uint32_t)__shfl_xor((int)m, o, 64));
@@ -98,24 +145,24 @@ __global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
         }
     } else if constexpr (COLS) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < W; ++k) {
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < RPT; ++i)
-                m = umax(m, abs_bits(v[i][k]));
+                m = E::max2(m, v[i].abs(k));
 #pragma unroll
             for (int o = 16; o < 64; o <<= 1)
-                m = umax(m, (uint32_t)__shfl_xor((int)m, o, 64));
+                m = E::max2(m, (uint32_t)__shfl_xor((int)m, o, 64));
             if (lane < 16)
-                cmax[w][cc * 8 + k] = m;
+                cmax[w][cc * W + k] = m;
         }
         __syncthreads();
         if (tid < TS) {
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < NW; ++i)
-                m = umax(m, cmax[i][tid]);
-            const BlockScale b = fp8_scale(m);
+                m = E::max2(m, cmax[i][tid / EPW]);
+            const BlockScale b = fp8_scale(E::elem_bits(m, tid % EPW));
             cs[0][tid] = b.s;
             cs[1][tid] = b.inv;
             if (tc * TS + tid < a.C)
@@ -130,13 +177,17 @@ __global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
             if (!BLOCK) {
                 uint32_t m = 0;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    m = umax(m, abs_bits(v[i][k]));
-                b = fp8_scale(row16_umax(m));
+                for (int k = 0; k < W; ++k)
+                    m = E::max2(m, v[i].abs(k));
+                b = fp8_scale(row16_umax(E::top(m)));
             }
+            float u[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                u[k] = v[i][k];
             const int r = r0 + i;
             if (r < a.R) {
-                *(uint2 *)(a.q + (int64_t)r * pitch + c0) = quant8(v[i], b);
+                *(uint2 *)(a.q + (int64_t)r * pitch + c0) = quant8(u, b);
                 if (!BLOCK && cc == 0)
                     a.s[(int64_t)tc * a.R + r] = b.s;
             }
@@ -147,11 +198,11 @@ __global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
             __syncthreads(); // cs
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float s = BLOCK ? sb.s : cs[0][cc * 8 + k];
-            const float inv = BLOCK ? sb.inv : cs[1][cc * 8 + k];
-            turn[turn_word(cc * 8 + k, rr)] = f32x4_to_e4m3x4(
-                div_by(v[0][k], s, inv), div_by(v[1][k], s, inv),
-                div_by(v[2][k], s, inv), div_by(v[3][k], s, inv));
+            BlockScale b = sb;
+            if (!BLOCK)
+                b = BlockScale{cs[0][cc * 8 + k], cs[1][cc * 8 + k]};
+            const float u[RPT] = {v[0][k], v[1][k], v[2][k], v[3][k]};
+            turn[turn_word(cc * 8 + k, rr)] = quant4(u, b);
         }
         __syncthreads();
         const int64_t pitch = fp8_pitch(a.R);
@@ -165,13 +216,25 @@ __global__ __launch_bounds__(NT, 6) void fp8_quant_kernel(QuantArgs a)
     }
 }
 
-template <bool ROWS, bool COLS> void launch_layout(const QuantArgs &a, bool block, hipStream_t s)
+template <int DT, bool ROWS, bool COLS>
+void launch_layout(const QuantArgs &a, bool block, hipStream_t s)
 {
     const dim3 grid((uint32_t)(fp8_blocks(a.R) * (int64_t)a.tiles_c));
     if (block)
-        fp8_quant_kernel<ROWS, COLS, true><<<grid, NT, 0, s>>>(a);
+        fp8_quant_kernel<DT, ROWS, COLS, true><<<grid, NT, 0, s>>>(a);
     else
-        fp8_quant_kernel<ROWS, COLS, false><<<grid, NT, 0, s>>>(a);
+        fp8_quant_kernel<DT, ROWS, COLS, false><<<grid, NT, 0, s>>>(a);
+}
+
+template <int DT>
+void launch_type(const QuantArgs &a, bool rows, bool cols, bool block, hipStream_t s)
+{
+    if (rows && cols)
+        launch_layout<DT, true, true>(a, block, s);
+    else if (rows)
+        launch_layout<DT, true, false>(a, block, s);
+    else
+        launch_layout<DT, false, true>(a, block, s);
 }
 
 } // namespace
@@ -180,7 +243,7 @@ hipError_t launch_fp8_quant(const twell_mat_t *x, const twell_fp8_t *o, const tw
                             twell_timing_t *timing, hipStream_t s)
 {
     QuantArgs a = {};
-    a.x = x->data, a.ld = x->ld, a.dt = x->dtype, a.R = x->rows, a.C = x->cols;
+    a.x = x->data, a.ld = x->ld, a.R = x->rows, a.C = x->cols;
     if (o)
         a.q = o->q, a.s = o->scale;
     if (ot)
@@ -188,12 +251,10 @@ hipError_t launch_fp8_quant(const twell_mat_t *x, const twell_fp8_t *o, const tw
     const bool block = (o ? o : ot)->block_rows == TS;
     a.tiles_c = fp8_blocks(a.C);
     Timer tm(timing, s);
-    if (o && ot)
-        launch_layout<true, true>(a, block, s);
-    else if (o)
-        launch_layout<true, false>(a, block, s);
+    if (x->dtype == TWELL_BF16)
+        launch_type<TWELL_BF16>(a, o, ot, block, s);
     else
-        launch_layout<false, true>(a, block, s);
+        launch_type<TWELL_F32>(a, o, ot, block, s);
     tm.mark("fp8_quant");
     return hipGetLastError();
 }

@@ -3,9 +3,14 @@
 // Forward, per row: h = residual + x (float32), r = 1 / sqrt(mean(h^2) + eps),
 // n = h r gain. Everything is one pass: a row stays in registers between the
 // sum of squares and the output, in float32; h and n are each rounded once,
-// when they are stored (the norm is of the unrounded h). 8-bit output: the
-// lanes of a 16-lane group hold 128 consecutive columns (eight each), so a
-// block's amax is four DPP moves away and q is written from registers.
+// when they are stored (the norm is of the unrounded h).
+//
+// 8-bit output: the lanes of a 16-lane group hold 128 consecutive columns
+// (eight each), so a block's amax is four DPP moves away and q is written from
+// registers. The row is taken in 64 bits there, so that q is the e4m3 value
+// nearest to n / scale: in 32 bits the roundings of h, h r, h r gain, the scale
+// and the quotient put one value in a million on the wrong side of a tie
+// between two e4m3 values, a sixteenth off. The arithmetic hides behind memory.
 //
 // Backward, per row, with xh = h r and dg = dn gain:
 //   dh = r (dg - xh mean(dg xh)) + dres,   dgain = sum over rows of dn xh.
@@ -26,10 +31,49 @@ namespace {
 // waves' eight at 5.0.
 template <int LPR> DEVI int row_lane() { return (int)threadIdx.x % LPR; }
 
+template <int CTRL> DEVI double dpp_mov(double v)
+{
+    const int2 q = __builtin_bit_cast(int2, v);
+    return __builtin_bit_cast(double,
+                              make_int2(__builtin_amdgcn_mov_dpp(q.x, CTRL, 0xF, 0xF, false),
+                                        __builtin_amdgcn_mov_dpp(q.y, CTRL, 0xF, 0xF, false)));
+}
+// Maximum over each group of 16 lanes (values that are not negative).
+DEVI double row16_max(double v)
+{
+    v = fmax(v, dpp_mov<0xB1>(v));
+    v = fmax(v, dpp_mov<0x4E>(v));
+    v = fmax(v, dpp_mov<0x141>(v));
+    return fmax(v, dpp_mov<0x140>(v));
+}
+// 1 / v and 1 / sqrt(v), from the hardware's estimates by a Newton step: within
+// 2^-40 or so, where the e4m3 quotient needs 2^-30. 1 / sqrt(infinity) is 0 and
+// 1 / sqrt(0) infinity, as the estimate says.
+DEVI double rcp64(double v)
+{
+    const double y = __builtin_amdgcn_rcp(v);
+    return fma(fma(-v, y, 1.), y, y);
+}
+DEVI double rsqrt64(double v)
+{
+    const double y = __builtin_amdgcn_rsq(v);
+    const double z = fma(0.5 * y, fma(-v * y, y, 1.), y);
+    return v > 0. && v < __builtin_inf() ? z : y;
+}
+
 // Sum over the LPR lanes that share a row, in every one of them. Past a wave
 // it goes through buf (a float for each wave of the workgroup); each sum of a
 // kernel has a buf of its own, so no barrier is needed before it is written.
-template <int LPR> DEVI float row_sum(float v, float *buf)
+DEVI double wave_sum(double v)
+{
+    v += dpp_mov<0xB1>(v);
+    v += dpp_mov<0x4E>(v);
+    v += dpp_mov<0x141>(v);
+    v += dpp_mov<0x140>(v);
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+template <int LPR, class F> DEVI F row_sum(F v, F *buf)
 {
     if constexpr (LPR < 64) {
         v += dpp_mov<0xB1>(v);
@@ -47,7 +91,7 @@ template <int LPR> DEVI float row_sum(float v, float *buf)
             if ((threadIdx.x & 63) == 0)
                 buf[w] = v;
             __syncthreads();
-            const float *b = buf + w / W * W;
+            const F *b = buf + w / W * W;
             v = b[0];
 #pragma unroll
             for (int i = 1; i < W; ++i)
@@ -65,6 +109,7 @@ struct FwdArgs {
     int64_t ldx, ldr, ldh, ldn;
     int T, d, dtx, dtr, dtg, dtn;
     float eps;
+    double inv_d; // 1 / d
 };
 
 constexpr int fwd_threads(int lpr) { return lpr < 256 ? 256 : lpr; }
@@ -110,25 +155,75 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             h.v[c][i] = h.v[c][i] * r * g.v[c][i];
-    if (!a.q) {
-        h.store(row_ptr(a.n, a.dtn, a.ldn, t), a.dtn, d, lane);
-        return;
+    h.store(row_ptr(a.n, a.dtn, a.ldn, t), a.dtn, d, lane);
+}
+
+// The same with n in 8 bits.
+template <int LPR, int C, bool RAG>
+__global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs a)
+{
+    constexpr int RPB = fwd_threads(LPR) / LPR;
+    __shared__ double buf[fwd_threads(LPR) / 64];
+    const int lane = row_lane<LPR>();
+    const int64_t t = (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
+    const int d = t < a.T ? a.d : 0;
+    double p[C][8]; // h, then h gain
+    double ss = 0.;
+    Row<LPR, C, RAG> h, g;
+    h.load(row_ptr(a.x, a.dtx, a.ldx, t), a.dtx, d, lane);
+    if (a.res) {
+        Row<LPR, C, RAG> r;
+        r.load(row_ptr(a.res, a.dtr, a.ldr, t), a.dtr, d, lane);
+        g.load(a.gain, a.dtg, d, lane);
+        h.widen(a.dtx);
+        r.widen(a.dtr);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[c][i] = (double)h.v[c][i] + (double)r.v[c][i];
+                h.v[c][i] += r.v[c][i];
+            }
+        h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
+    } else {
+        g.load(a.gain, a.dtg, d, lane);
+        h.widen(a.dtx);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                p[c][i] = (double)h.v[c][i];
     }
+    g.widen(a.dtg);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            ss = fma(p[c][i], p[c][i], ss);
+            p[c][i] *= (double)g.v[c][i];
+        }
+    ss = row_sum<LPR>(ss, buf);
+    const double r = rsqrt64(ss * a.inv_d + (double)a.eps);
     const int64_t pitch = fp8_pitch(a.d);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int j = 8 * (lane + LPR * c);
-        uint32_t m = 0;
+        double m = 0.;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t b = abs_bits(h.v[c][i]);
-            m = b > m ? b : m;
-        }
-        const BlockScale b = fp8_scale(row16_umax(m));
+        for (int i = 0; i < 8; ++i)
+            m = fmax(m, fabs(p[c][i]));
+        // scale = max(amax, 2^-64) / 448; a NaN stays
+        m = row16_max(m) * r;
+        m = m <= (double)FP8_AMAX_MIN ? (double)FP8_AMAX_MIN : m;
+        const float s = (float)(m * (1. / FP8_MAX));
+        const double k = r * rcp64((double)s); // y = p k = n / scale
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[c][i] *= k;
         if (j < pitch && t < a.T) {
-            *(uint2 *)(a.q + t * pitch + j) = quant8(h.v[c], b);
+            *(uint2 *)(a.q + t * pitch + j) = quant8(p[c]);
             if ((lane & 15) == 0)
-                a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = b.s;
+                a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = s;
         }
     }
 }
@@ -285,7 +380,11 @@ int bwd_groups(int T, int d)
 template <int LPR, int C, bool RAG> void fwd_one(const FwdArgs &a, hipStream_t s)
 {
     constexpr int NT = fwd_threads(LPR), RPB = NT / LPR;
-    rmsnorm_fwd_kernel<LPR, C, RAG><<<(a.T + RPB - 1) / RPB, NT, 0, s>>>(a);
+    const dim3 grid((a.T + RPB - 1) / RPB);
+    if (a.q)
+        rmsnorm_fwd8_kernel<LPR, C, RAG><<<grid, NT, 0, s>>>(a);
+    else
+        rmsnorm_fwd_kernel<LPR, C, RAG><<<grid, NT, 0, s>>>(a);
 }
 
 template <bool RAG> void fwd_sizes(const FwdArgs &a, hipStream_t s)
@@ -327,7 +426,7 @@ hipError_t launch_rmsnorm_fwd(const twell_mat_t *x, const twell_mat_t *res, cons
 {
     FwdArgs a = {};
     a.x = x->data, a.ldx = x->ld, a.dtx = x->dtype, a.T = x->rows, a.d = x->cols;
-    a.gain = gain, a.dtg = dtg, a.eps = eps;
+    a.gain = gain, a.dtg = dtg, a.eps = eps, a.inv_d = 1. / x->cols;
     if (res) {
         a.res = res->data, a.ldr = res->ld, a.dtr = res->dtype;
         a.h = h->data, a.ldh = h->ld;

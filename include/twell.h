@@ -335,10 +335,9 @@ typedef struct {
  *          past `cols` hold zeros (twell_rmsnorm_fwd and twell_fp8_quant
  *          write them, twell_fp8_matmul reads them)
  *   scale  [ceil(cols / 128)][ceil(rows / block_rows)] float32
- * The library writes scale = max(amax, 2^-64) / 448 over the block, and
- * q = x / scale rounded to 32 bits and then to the nearest e4m3 value, ties
- * to even. A NaN or infinity in a block makes its scale that, and the values
- * the block stands for NaN.
+ * The library writes scale = max(amax, 2^-64) / 448 over the block, rounded to
+ * float32, and for q the e4m3 value nearest to x / scale, ties to even. A NaN
+ * or infinity in a block makes the values that it stands for NaN.
  */
 typedef struct {
     int32_t rows, cols, block_rows;

@@ -52,9 +52,16 @@ def rmsnorm_bwd(dn, h, gain, eps, dres=None):
     return dh, (dn * xh).sum(0), mag, (dn * xh).abs().sum(0)
 
 
+def to_e4m3(y):
+    """float64 to the nearest e4m3 value, ties to even (|y| <= 448)."""
+    step = 2 * half_step(y)
+    return (torch.round(y / step) * step).float().to(torch.float8_e4m3fn)
+
+
 def quant(x, block_rows):
     """(q, scale) as the layout defines them, bit for bit: the scale is the
-    32-bit quotient amax / 448, q the nearest e4m3 of the 32-bit quotient."""
+    32-bit quotient amax / 448, q the e4m3 value nearest to x / scale (in 64
+    bits no quotient of two floats is rounded onto or across a tie)."""
     x = x.float()
     R, C = x.shape
     rb, cb = -(-R // block_rows), -(-C // 128)
@@ -62,7 +69,7 @@ def quant(x, block_rows):
     p[:R, :C] = x
     b = p.view(rb, block_rows, cb, 128)
     s = b.abs().amax(dim=(1, 3)).clamp(min=AMAX_MIN) / E4M3_MAX
-    q = (b / s[:, None, :, None]).to(torch.float8_e4m3fn).view(rb * block_rows, cb * 128)[:R]
+    q = to_e4m3(b.double() / s.double()[:, None, :, None]).view(rb * block_rows, cb * 128)[:R]
     return q, s.t().contiguous()
 
 
