@@ -145,43 +145,48 @@ template <int LPR, int C, bool RAG> struct Row {
 
     DEVI void load(const void *row, int dt, int d, int lane)
     {
+        uint4 q[C], r[C]; // r: the second half of a float32 chunk
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            q[c] = r[c] = make_uint4(0, 0, 0, 0);
         if (dt == TWELL_BF16) {
             const uint16_t *p = (const uint16_t *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
-                uint4 q = make_uint4(0, 0, 0, 0);
                 if (j + 8 <= d) {
-                    q = ldg16u(p + j);
+                    q[c] = ldg16u(p + j);
                 } else if (RAG && j < d) {
                     uint32_t w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         w[i] = (j + 2 * i < d ? p[j + 2 * i] : 0) |
                                (j + 2 * i + 1 < d ? (uint32_t)p[j + 2 * i + 1] << 16 : 0);
-                    q = make_uint4(w[0], w[1], w[2], w[3]);
+                    q[c] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                put(c, 0, q);
             }
         } else {
-            const float *p = (const float *)row;
+            const uint32_t *p = (const uint32_t *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
-                uint4 q = make_uint4(0, 0, 0, 0), r = q;
                 if (j + 8 <= d) {
-                    q = ldg16u(p + j);
-                    r = ldg16u(p + j + 4);
-                }
-                put(c, 0, q);
-                put(c, 4, r);
-                if (RAG && j < d && j + 8 > d) {
+                    q[c] = ldg16u(p + j);
+                    r[c] = ldg16u(p + j + 4);
+                } else if (RAG && j < d) {
+                    uint32_t w[8];
 #pragma unroll
-                    for (int i = 0; i < 7; ++i)
-                        if (j + i < d)
-                            v[c][i] = p[j + i];
+                    for (int i = 0; i < 8; ++i)
+                        w[i] = j + i < d ? p[j + i] : 0;
+                    q[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                    r[c] = make_uint4(w[4], w[5], w[6], w[7]);
                 }
             }
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            put(c, 0, q[c]);
+            put(c, 4, r[c]);
         }
     }
 
@@ -192,7 +197,10 @@ template <int LPR, int C, bool RAG> struct Row {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const uint4 q = bits(c, 0);
-                elem<TWELL_BF16>::widen(q, v[c]);
+                v[c][0] = bf16_lo(q.x), v[c][1] = bf16_hi(q.x);
+                v[c][2] = bf16_lo(q.y), v[c][3] = bf16_hi(q.y);
+                v[c][4] = bf16_lo(q.z), v[c][5] = bf16_hi(q.z);
+                v[c][6] = bf16_lo(q.w), v[c][7] = bf16_hi(q.w);
             }
         }
     }
