@@ -610,8 +610,8 @@ class Fp8:
 
 def empty_fp8(rows, cols, block_rows, device) -> Fp8:
     nb = -(-cols // FP8_BLOCK)
-    return Fp8(torch.empty((rows, nb * FP8_BLOCK), dtype=torch.float8_e4m3fn, device=device),
-               torch.empty((nb, -(-rows // block_rows)), dtype=torch.float32, device=device),
+    return Fp8(torch.empty(rows, nb * FP8_BLOCK, dtype=_E4, device=device),
+               torch.empty(nb, -(-rows // block_rows), dtype=_F32, device=device),
                cols, block_rows)
 
 
@@ -622,27 +622,32 @@ _pack_mat = struct.Struct("iiqi4xP").pack
 _pack_fp8 = struct.Struct("iii4xPP").pack
 assert struct.calcsize("iiqi4xP") == ctypes.sizeof(MatC)
 assert struct.calcsize("iii4xPP") == ctypes.sizeof(Fp8C)
+_F32, _E4 = torch.float32, torch.float8_e4m3fn
 _DT = {torch.float32: TWELL_F32, torch.bfloat16: TWELL_BF16}
 
 
-def _check_fp8(m, name, rows=None, cols=None) -> bytes:
-    """m's structure, of a well-formed Fp8 [rows][cols]."""
+def _check_fp8(m, name, rows=None, cols=None):
+    """(structure, rows) of a well-formed Fp8 [rows][cols]."""
     if not isinstance(m, Fp8):
         raise TwellError(f"{name}: expected an Fp8")
-    q, s, br = m.q, m.scale, m.block_rows
+    q, s, br, mc = m.q, m.scale, m.block_rows, m.cols
     if br not in (1, FP8_BLOCK):
         raise TwellError(f"{name}.block_rows: {br}, expected 1 or {FP8_BLOCK}")
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise TwellError(f"{name}.q: expected a [rows][cols up to 128] tensor")
-    if rows is None:
-        rows = q.shape[0]
-    if cols is not None and m.cols != cols:
-        raise TwellError(f"{name}: {m.cols} columns, expected {cols}")
-    cols = m.cols
-    nb = -(-cols // FP8_BLOCK)
-    _req(q, f"{name}.q", (rows, nb * FP8_BLOCK), torch.float8_e4m3fn)
-    _req(s, f"{name}.scale", (nb, -(-rows // br)), torch.float32)
-    return _pack_fp8(rows, cols, br, q.data_ptr(), s.data_ptr())
+    r, pitch = q.shape
+    nb = -(-mc // FP8_BLOCK)
+    sshape = (nb, r if br == 1 else -(-r // FP8_BLOCK))
+    if not (isinstance(s, torch.Tensor) and pitch == nb * FP8_BLOCK and s.shape == sshape
+            and q.dtype == _E4 and s.dtype == _F32 and q.is_contiguous() and s.is_contiguous()
+            and (cols is None or (mc == cols and r == rows))):
+        if cols is not None and mc != cols:
+            raise TwellError(f"{name}: {mc} columns, expected {cols}")
+        if rows is None:
+            rows = r
+        _req(q, f"{name}.q", (rows, nb * FP8_BLOCK), _E4)
+        _req(s, f"{name}.scale", sshape, _F32)
+    return _pack_fp8(r, mc, br, q.data_ptr(), s.data_ptr()), r
 
 
 def _mat(t, name, rows=None, cols=None, dtype=None):
@@ -668,10 +673,11 @@ def _mat(t, name, rows=None, cols=None, dtype=None):
 
 def _new_mat(rows, cols, dtype, device):
     """A new contiguous tensor and its structure."""
-    t = torch.empty((rows, cols), dtype=dtype, device=device)
-    if dtype not in _DT:
+    dt = _DT.get(dtype)
+    if dt is None:
         raise TwellError(f"unsupported dtype {dtype}")
-    return t, _pack_mat(rows, cols, cols, _DT[dtype], t.data_ptr())
+    t = torch.empty(rows, cols, dtype=dtype, device=device)
+    return t, _pack_mat(rows, cols, cols, dt, t.data_ptr())
 
 
 def _new_fp8(rows, cols, block_rows, device):
@@ -726,7 +732,7 @@ def rmsnorm_fwd(x, gain, residual=None, eps: float = 1e-6, out_dtype=torch.bfloa
         if out is None:
             out, m8 = _new_fp8(T, d, 1, x.device)
         else:
-            m8 = _check_fp8(out, "out", T, d)
+            m8 = _check_fp8(out, "out", T, d)[0]
             on["out.q"], on["out.scale"] = out.q, out.scale
     elif out is None:
         out, mn = _new_mat(T, d, out_dtype, x.device)
@@ -786,7 +792,7 @@ def fp8_quant(x, block_rows: int = 1, layout: str = "rows", out: Fp8 | None = No
         elif t is None:
             m[name] = _new_fp8(*shape, block_rows, x.device)
         else:
-            m[name] = t, _check_fp8(t, name, *shape)
+            m[name] = t, _check_fp8(t, name, *shape)[0]
             if t.block_rows != block_rows:
                 raise TwellError(f"{name}: block_rows {t.block_rows}, expected {block_rows}")
             on[name + ".q"], on[name + ".scale"] = t.q, t.scale
@@ -807,8 +813,8 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=torch.bfloat16, fast_sums: bo
     bfloat16. Products are added in float32, or, with fast_sums, by the 8-bit
     matrix instruction at up to twice the rate (errors of about 2^-16 of the
     sum of the terms' sizes: right for a bfloat16 result, short for float32)."""
-    ma, mb = _check_fp8(a, "a"), _check_fp8(b, "b")
-    M, N, K = a.q.shape[0], b.q.shape[0], a.cols
+    (ma, M), (mb, N) = _check_fp8(a, "a"), _check_fp8(b, "b")
+    K = a.cols
     if b.cols != K:
         raise TwellError(f"b: {b.cols} columns, a has {K}")
     on = {"a.q": a.q, "a.scale": a.scale, "b.q": b.q, "b.scale": b.scale}
