@@ -763,8 +763,10 @@ def rmsnorm_bwd(dn, h, gain, dres=None, eps: float = 1e-6, dh_dtype=torch.float3
         mo = _mat(dh, "dh", T, d)[0]
     if dgain is None:
         dgain = torch.empty(d, dtype=torch.float32, device=dn.device)
-    _req(dgain, "dgain", (d,), torch.float32)
-    _ws_form(workspace)
+    else:
+        _req(dgain, "dgain", (d,), torch.float32)
+    if workspace is not None:
+        _ws_form(workspace)
     dev = _gpu({"dn": dn, "h": h, "gain": gain, "dres": dres, "dh": dh, "dgain": dgain,
                 "workspace": workspace})
     workspace = _ws(workspace, rmsnorm_bwd_workspace_bytes(T, d), dn.device)
