@@ -19,6 +19,7 @@
 // consecutive n. Which k a lane's 32 bytes are does not matter as long as
 // both operands agree, so each lane takes 32 consecutive bytes of its row.
 #include <cmath>
+#include <type_traits>
 
 #include "fp8.hpp"
 #include "ntgemm.hpp"
@@ -99,6 +100,13 @@ template <> struct Frag<TWELL_SUMS_F32> {
 // - The step's one barrier stands before its last row of products. By then
 //   every read of its stage is done and the next stage's loads are in, so the
 //   next step's first fragments are read beside that last row.
+//
+// Of the two large tiles a CU holds one workgroup, so there is nobody to work
+// while it begins and ends. There the workgroups stay and take further tiles:
+// the next tile's first loads go out before this one's results are stored, and
+// the stores drain beside its first steps (8192 x 5632 over 2048: 93 -> 88 us).
+// Stores write whole 128-byte lines, through LDS: float32 results stored from
+// the accumulators, 64 bytes of a row at a time, took 173 us there, so 165.
 template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
     static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
@@ -111,13 +119,18 @@ template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
     static constexpr int LPS = (WB + 1 + SYNC - 1) / SYNC; // loads beside a product before it
     static constexpr int SCALES = ROWS * FP8_BLK;        // byte offset of a stage's scales
     static constexpr int STAGE = SCALES + ROWS * 4;
-    static constexpr int OUTB = WM * (WN * 2 + 16) * NWV; // the epilogue's bf16 rows
-    static constexpr int LDS = NST * STAGE > OUTB ? NST * STAGE : OUTB;
+    // the epilogue's rows, 16 tokens a wave at a time: WE n in bf16, 32 in
+    // float32, padded so that 16 rows start on 16 distinct banks
+    static constexpr int WE = WN < 64 ? WN : 64, OROW = 128 + 16, OUTB = 16 * OROW * NWV;
+    static constexpr bool STAY = NST == 2; // workgroups go on to further tiles
+    static constexpr int LDS = NST * STAGE + (STAY ? OUTB : 0);
     static_assert(BN % (8 * NWV) == 0 && BM % (8 * NWV) == 0 && BN % 64 == 0 && BM % 64 == 0 &&
                       NSC <= NWV, "whole loads");
-    static_assert(WN <= FP8_BLK && FP8_BLK % WN == 0, "a wave's n share one 128-row scale block");
+    static_assert(WN % 32 == 0 && WN <= FP8_BLK && FP8_BLK % WN == 0,
+                  "a wave's n share one 128-row scale block");
     static_assert(NI % 2 == 0, "two fragments of B in turn");
     static_assert(NST >= 2 && (NST - 2) * (WB + 1) < 64, "loads in flight must fit vmcnt");
+    static_assert(OUTB <= NST * STAGE && LDS <= 160 * 1024, "LDS");
 };
 
 #pragma clang diagnostic push
@@ -158,6 +171,14 @@ template <int N> DEVI void wait_oldest(int left, int full)
                      : "scc");
 }
 
+// v, as if it were new here: what is formed of it is not kept in registers
+// through the loop over the tiles, where there are none to spare.
+DEVI int here(int v)
+{
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // BLKB: B's scale block is 128 rows, so a wave's n share one scale per step.
 template <class C, int SUMS, bool BLKB>
 __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a)
@@ -169,37 +190,45 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
     const int n_nt = (a.N + C::BN - 1) / C::BN, n_mt = (a.M + C::BM - 1) / C::BM;
     const int64_t total = (int64_t)n_nt * n_mt * a.parts;
     const int64_t per = (total + NXCD - 1) / NXCD;
-    const int64_t q0 = (blockIdx.x % NXCD) * per + blockIdx.x / NXCD;
-    if (blockIdx.x / NXCD >= per || q0 >= total)
+    const int64_t run0 = blockIdx.x % NXCD * per;
+    const int64_t run1 = run0 + per < total ? run0 + per : total;
+    int64_t q0 = run0 + blockIdx.x / NXCD;
+    if (q0 >= run1)
         return;
-    const int part = (int)(q0 / ((int64_t)n_nt * n_mt));
-    const int q = (int)(q0 % ((int64_t)n_nt * n_mt));
-    const int64_t gsz = (int64_t)GM * n_nt;
-    const int grp = (int)(q / gsz), grows = min(GM, n_mt - grp * GM), gr = (int)(q % gsz);
-    const int m0 = (grp * GM + gr % grows) * C::BM, n0 = gr / grows * C::BN;
     const int lane = threadIdx.x & 63, w = wave_id();
     const int wm = w / C::WGN, wn = w % C::WGN, l16 = lane & 15, q4 = lane >> 4;
-    const int kb0 = part * a.per, kb1 = min(a.nkb, kb0 + a.per);
-
-    // this wave's loads: eight rows of one operand each, lane l byte 16 l of
-    // the 1 KB, i.e. the chunk that the swizzle puts there. Rows past an
-    // operand read its last row (their outputs are dropped).
     const uint32_t lds0 = (uint32_t)(uintptr_t)(ng::lds_u8 *)L;
-    const uint8_t *srcb = a.qb + (int64_t)n0 * a.pitch, *srca = a.qa + (int64_t)m0 * a.pitch;
-    uint32_t off[C::WB];
-#pragma unroll
-    for (int g = 0; g < C::WB; ++g) {
-        const int r = (g < C::WBB ? w * C::WBB + g : w * C::WBA + g - C::WBB) * 8 + lane / 8;
-        const int last = g < C::WBB ? a.N - 1 - n0 : a.M - 1 - m0;
-        off[g] = (uint32_t)min(r, last) * (uint32_t)a.pitch + (((lane & 7) ^ ((r >> 1) & 7)) << 4);
-    }
     const int ws = w % C::NSC;
     const bool sisb = ws * 64 < C::BN;
     const float *ssrc = sisb ? a.sb : a.sa;
     const int ns = sisb ? a.nsb : a.nsa;
-    const int srow = sisb ? min(n0 + ws * 64 + lane, a.N - 1)
-                          : min(m0 + ws * 64 - C::BN + lane, a.M - 1);
-    const uint32_t soff = (uint32_t)(srow / (sisb ? a.rb : a.ra)) * 4u;
+
+    // The tile and this wave's loads of it: eight rows of one operand each,
+    // lane l byte 16 l of the 1 KB, i.e. the chunk that the swizzle puts
+    // there. Rows past an operand read its last row (their outputs are dropped).
+    int m0, n0, part, kb0, kb1;
+    const uint8_t *srcb, *srca;
+    uint32_t off[C::WB], soff;
+    auto place = [&] {
+        const int lane = here((int)threadIdx.x) & 63;
+        part = (int)(q0 / ((int64_t)n_nt * n_mt));
+        const int q = (int)(q0 % ((int64_t)n_nt * n_mt));
+        const int64_t gsz = (int64_t)GM * n_nt;
+        const int grp = (int)(q / gsz), grows = min(GM, n_mt - grp * GM), gr = (int)(q % gsz);
+        m0 = (grp * GM + gr % grows) * C::BM, n0 = gr / grows * C::BN;
+        kb0 = part * a.per, kb1 = min(a.nkb, kb0 + a.per);
+        srcb = a.qb + (int64_t)n0 * a.pitch, srca = a.qa + (int64_t)m0 * a.pitch;
+#pragma unroll
+        for (int g = 0; g < C::WB; ++g) {
+            const int r = (g < C::WBB ? w * C::WBB + g : w * C::WBA + g - C::WBB) * 8 + lane / 8;
+            const int last = g < C::WBB ? a.N - 1 - n0 : a.M - 1 - m0;
+            off[g] = (uint32_t)min(r, last) * (uint32_t)a.pitch +
+                     (((lane & 7) ^ ((r >> 1) & 7)) << 4);
+        }
+        const int srow = sisb ? min(n0 + ws * 64 + lane, a.N - 1)
+                              : min(m0 + ws * 64 - C::BN + lane, a.M - 1);
+        soff = (uint32_t)(srow / (sisb ? a.rb : a.ra)) * 4u;
+    };
     // load g of this wave (g == WB: its scales) for step kb into stage st
     auto load = [&](int g, int kb, int st) {
         const uint32_t dst = lds0 + (uint32_t)st * C::STAGE;
@@ -211,13 +240,14 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
         else
             dma4(ssrc + (int64_t)kb * ns, soff, dst + C::SCALES + ws * 256, kb, kb1);
     };
+    auto first_loads = [&] {
+#pragma unroll
+        for (int k = 0; k < C::NST - 1; ++k)
+#pragma unroll
+            for (int g = 0; g <= C::WB; ++g)
+                load(g, kb0 + k, k);
+    };
 
-    floatx4_t acc[C::NI][C::MI];
-#pragma unroll
-    for (int i = 0; i < C::NI; ++i)
-#pragma unroll
-        for (int j = 0; j < C::MI; ++j)
-            acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
     // byte of this lane's two chunks (q4 and q4 + 4) in a 16-row fragment
     const int f0 = l16 * FP8_BLK + ((q4 ^ ((l16 >> 1) & 7)) << 4), f1 = f0 ^ 64;
     auto frag = [&](const uint8_t *p) {
@@ -248,137 +278,158 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
     intx8_t rb[RB], ra[C::MI];
     float sa[C::MI], sb = 1.f;
     floatx4_t sb4[2]; // B's scales of this and the next row of products
-#pragma unroll
-    for (int k = 0; k < C::NST - 1; ++k)
-#pragma unroll
-        for (int g = 0; g <= C::WB; ++g)
-            load(g, kb0 + k, k);
+    place();
+    first_loads();
     sync(kb1 - kb0);
-    rb[0] = frag(Bw);
-    sb4[0] = *(const floatx4_t *)(sbw + q4 * 4);
-#pragma unroll
-    for (int j = 0; j < C::MI; ++j) {
-        ra[j] = frag(Aw + j * 16 * FP8_BLK);
-        sa[j] = saw[j * 16 + l16];
-    }
-    if (BLKB)
-        sb = sbw[0];
-    for (int kb = kb0, st = 0; kb < kb1; ++kb) {
-        const int free = st == 0 ? C::NST - 1 : st - 1; // the last step's stage
-        const int cur = st * C::STAGE;
-        st = st == C::NST - 1 ? 0 : st + 1;
-        const int nxt = st * C::STAGE;
-        Frag<SUMS> fa[C::MI], fb;
-        float s[C::MI];
-#pragma unroll
-        for (int j = 0; j < C::MI; ++j) {
-            fa[j].set(ra[j]);
-            s[j] = BLKB ? sa[j] * sb : sa[j];
-        }
-        constexpr int NP = C::NI * C::MI;
-        constexpr int LAG = SUMS == TWELL_SUMS_FP8 && C::MI > 2 ? 3 : 2;
-        floatx4_t v[LAG + 1];
-        auto scale = [&](int t) { // product t into its accumulator
-            const int i = t / C::MI, j = t % C::MI;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                acc[i][j][e] = fmaf(v[t % (LAG + 1)][e], BLKB ? s[j] : s[j] * sb4[i & 1][e],
-                                    acc[i][j][e]);
-        };
-#pragma unroll
-        for (int t = 0; t < NP; ++t) {
-            const int i = t / C::MI, j = t % C::MI;
-            if (j == 0) {
-                if (i == C::NI - 1)
-                    sync(kb1 - kb - 1);
-                fb.set(rb[i % RB]);
-                if (i < C::NI - 1) {
-                    rb[(i + 1) % RB] = frag(Bw + cur + (i + 1) * 16 * FP8_BLK);
-                } else {
-                    rb[0] = frag(Bw + nxt);
-                    if (BLKB)
-                        sb = *(const float *)((const uint8_t *)sbw + nxt);
-                }
-            }
-            v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j]);
-            if (t >= LAG)
-                scale(t - LAG);
-            static_assert(LAG <= C::MI, "the last row's scales are used by then");
-            if (!BLKB && j == LAG - 1) // the row before is scaled: its place is free
-                sb4[(i + 1) & 1] = *(const floatx4_t *)((const uint8_t *)(
-                    sbw + (i < C::NI - 1 ? (i + 1) * 16 : 0) + q4 * 4) + (i < C::NI - 1 ? cur : nxt));
-            if (i == C::NI - 1) {
-                ra[j] = frag(Aw + nxt + j * 16 * FP8_BLK);
-                sa[j] = *(const float *)((const uint8_t *)(saw + j * 16 + l16) + nxt);
-            }
-#pragma unroll
-            for (int g = t * C::LPS; g < (t + 1) * C::LPS && g <= C::WB; ++g)
-                load(g, kb + C::NST - 1, free);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int t = NP - LAG; t < NP; ++t)
-            scale(t);
-    }
-    // ---- epilogue: lane's element e of tile (i, j) is token j * 16 + l16,
-    // n i * 16 + q4 * 4 + e of the wave's part
-    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN;
-    if (a.parts > 1 || a.dto == TWELL_F32) {
-        float *out = a.parts > 1 ? a.part + (int64_t)part * a.M * a.N : (float *)a.out;
-        const int64_t ld = a.parts > 1 ? a.N : a.ldo;
-#pragma unroll
-        for (int j = 0; j < C::MI; ++j) {
-            const int m = mw + j * 16 + l16;
-            if (m >= a.M)
-                continue;
-            float *row = out + m * ld;
-#pragma unroll
-            for (int i = 0; i < C::NI; ++i) {
-                const int n = nw + i * 16 + q4 * 4;
-                const floatx4_t v = acc[i][j];
-                if (n + 4 <= a.N) {
-                    stg16u(row + n, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                               __float_as_uint(v[2]), __float_as_uint(v[3])));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (n + e < a.N)
-                            row[n + e] = v[e];
-                }
-            }
-        }
-        return;
-    }
-    // bf16: the wave's rows through its own piece of LDS, so that a store
-    // instruction writes whole rows of WN values
-    __syncthreads(); // every wave is done with the stages
-    constexpr int ORB = C::WN * 2 + 16; // padded row: 16 rows start on 16 distinct banks
-    uint8_t *buf = L + w * C::WM * ORB;
-#pragma unroll
-    for (int j = 0; j < C::MI; ++j)
+    for (;;) { // tiles
+        floatx4_t acc[C::NI][C::MI];
 #pragma unroll
         for (int i = 0; i < C::NI; ++i)
-            *(uint2 *)(buf + (j * 16 + l16) * ORB + (i * 16 + q4 * 4) * 2) =
-                make_uint2(f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]),
-                           f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]));
-    constexpr int LPR = C::WN / 8; // lanes of a row, eight values each
-    const int c8 = lane % LPR, rr = lane / LPR, n = nw + c8 * 8;
 #pragma unroll
-    for (int r0 = 0; r0 < C::WM; r0 += 64 / LPR) {
-        const int m = mw + r0 + rr;
-        const uint4 v = *(const uint4 *)(buf + (r0 + rr) * ORB + c8 * 16);
-        if (m >= a.M || n >= a.N)
-            continue;
-        uint16_t *row = (uint16_t *)a.out + m * a.ldo;
-        if (n + 8 <= a.N) {
-            stg16u(row + n, v);
-        } else {
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+            for (int j = 0; j < C::MI; ++j)
+                acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+        rb[0] = frag(Bw);
+        sb4[0] = *(const floatx4_t *)(sbw + q4 * 4);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n + e < a.N)
-                    row[n + e] = (uint16_t)(u[e / 2] >> (16 * (e & 1)));
+        for (int j = 0; j < C::MI; ++j) {
+            ra[j] = frag(Aw + j * 16 * FP8_BLK);
+            sa[j] = saw[j * 16 + l16];
         }
+        if (BLKB)
+            sb = sbw[0];
+        for (int kb = kb0, st = 0; kb < kb1; ++kb) {
+            const int free = st == 0 ? C::NST - 1 : st - 1; // the last step's stage
+            const int cur = st * C::STAGE;
+            st = st == C::NST - 1 ? 0 : st + 1;
+            const int nxt = st * C::STAGE;
+            Frag<SUMS> fa[C::MI], fb;
+            float s[C::MI];
+#pragma unroll
+            for (int j = 0; j < C::MI; ++j) {
+                fa[j].set(ra[j]);
+                s[j] = BLKB ? sa[j] * sb : sa[j];
+            }
+            constexpr int NP = C::NI * C::MI;
+            constexpr int LAG = SUMS == TWELL_SUMS_FP8 && C::MI > 2 ? 3 : 2;
+            floatx4_t v[LAG + 1];
+            auto scale = [&](int t) { // product t into its accumulator
+                const int i = t / C::MI, j = t % C::MI;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = fmaf(v[t % (LAG + 1)][e], BLKB ? s[j] : s[j] * sb4[i & 1][e],
+                                        acc[i][j][e]);
+            };
+#pragma unroll
+            for (int t = 0; t < NP; ++t) {
+                const int i = t / C::MI, j = t % C::MI;
+                if (j == 0) {
+                    if (i == C::NI - 1)
+                        sync(kb1 - kb - 1);
+                    fb.set(rb[i % RB]);
+                    if (i < C::NI - 1) {
+                        rb[(i + 1) % RB] = frag(Bw + cur + (i + 1) * 16 * FP8_BLK);
+                    } else {
+                        rb[0] = frag(Bw + nxt);
+                        if (BLKB)
+                            sb = *(const float *)((const uint8_t *)sbw + nxt);
+                    }
+                }
+                v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j]);
+                if (t >= LAG)
+                    scale(t - LAG);
+                static_assert(LAG <= C::MI, "the last row's scales are used by then");
+                if (!BLKB && j == LAG - 1) // the row before is scaled: its place is free
+                    sb4[(i + 1) & 1] = *(const floatx4_t *)((const uint8_t *)(
+                        sbw + (i < C::NI - 1 ? (i + 1) * 16 : 0) + q4 * 4) + (i < C::NI - 1 ? cur : nxt));
+                if (i == C::NI - 1) {
+                    ra[j] = frag(Aw + nxt + j * 16 * FP8_BLK);
+                    sa[j] = *(const float *)((const uint8_t *)(saw + j * 16 + l16) + nxt);
+                }
+#pragma unroll
+                for (int g = t * C::LPS; g < (t + 1) * C::LPS && g <= C::WB; ++g)
+                    load(g, kb + C::NST - 1, free);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int t = NP - LAG; t < NP; ++t)
+                scale(t);
+        }
+        // ---- the next tile's first loads, into stages that every wave has left
+        // (what it read of them beside its last products is not used)
+        const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN, pt = part;
+        const bool whole = m0 + C::BM <= a.M && n0 + C::BN <= a.N;
+        // A whole tile's S stores all follow those loads, so the loads are in when
+        // at most S of this wave's accesses are on their way (they end in order).
+        auto arrive = [&](auto S) {
+            fence();
+            if (whole)
+                ng::wait_vm<decltype(S)::value>();
+            else
+                ng::wait_vm<0>();
+            __builtin_amdgcn_s_barrier();
+            fence();
+        };
+        q0 += gridDim.x / NXCD;
+        const bool more = C::STAY && q0 < run1;
+        if (more) {
+            place();
+            first_loads();
+        } else if (!C::STAY) {
+            __syncthreads(); // the rows below lie in the stages
+        }
+        fence(); // no store before the loads
+        // ---- epilogue: lane's element e of tile (i, j) is token j * 16 + l16,
+        // n i * 16 + q4 * 4 + e of the wave's part. The values pass through the
+        // wave's own piece of LDS, 16 tokens x WE n at a time, so that a store
+        // instruction writes whole runs of WE values.
+        auto store = [&](auto type, void *out, int64_t ld) {
+            using T = decltype(type);
+            constexpr int ES = sizeof(T), WE = ES == 4 ? 32 : C::WE;
+            constexpr int VPL = 16 / ES, LPR = WE / VPL; // values a lane, lanes of a run
+            const int lane = here((int)threadIdx.x) & 63, l16 = lane & 15, q4 = lane >> 4;
+            const int c8 = lane % LPR, rr = lane / LPR;
+            uint8_t *buf = L + (C::STAY ? C::NST * C::STAGE : 0) + w * 16 * C::OROW;
+#pragma unroll
+            for (int j = 0; j < C::MI; ++j)
+#pragma unroll
+                for (int h = 0; h < C::WN / WE; ++h) {
+#pragma unroll
+                    for (int i = 0; i < WE / 16; ++i) {
+                        const floatx4_t v = acc[h * (WE / 16) + i][j];
+                        uint8_t *p = buf + l16 * C::OROW + (i * 16 + q4 * 4) * ES;
+                        if constexpr (ES == 4)
+                            *(floatx4_t *)p = v;
+                        else
+                            *(uint2 *)p = make_uint2(f32x2_to_bf16x2(v[0], v[1]),
+                                                     f32x2_to_bf16x2(v[2], v[3]));
+                    }
+                    const int n = nw + h * WE + c8 * VPL;
+#pragma unroll
+                    for (int r0 = 0; r0 < 16; r0 += 64 / LPR) {
+                        const int m = mw + j * 16 + r0 + rr;
+                        const uint4 v = *(const uint4 *)(buf + (r0 + rr) * C::OROW + c8 * 16);
+                        T *row = (T *)out + m * ld;
+                        if (whole || (m < a.M && n + VPL <= a.N)) {
+                            stg16u(row + n, v);
+                        } else if (m < a.M) {
+                            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int e = 0; e < VPL; ++e)
+                                if (n + e < a.N)
+                                    row[n + e] = (T)(u[e * ES / 4] >> (8 * ES * e % 32));
+                        }
+                    }
+                }
+            if (more)
+                arrive(std::integral_constant<int, C::MI * (C::WN / WE) * (16 * LPR / 64)>());
+        };
+        if (a.parts > 1 || a.dto == TWELL_F32)
+            store(uint32_t(), a.parts > 1 ? a.part + (int64_t)pt * a.M * a.N : (float *)a.out,
+                  a.parts > 1 ? a.N : a.ldo);
+        else
+            store(uint16_t(), a.out, a.ldo);
+        if (!more)
+            return;
     }
 }
 
@@ -564,7 +615,10 @@ template <class C, int SUMS, bool BLKB> void launch_tile(const MmArgs &a, hipStr
 {
     const int64_t total = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.M + C::BM - 1) / C::BM) *
                           a.parts;
-    const dim3 grid((uint32_t)((total + NXCD - 1) / NXCD * NXCD));
+    int64_t wgs = (total + NXCD - 1) / NXCD * NXCD;
+    if (C::STAY && wgs > 256)
+        wgs = 256; // one for each CU
+    const dim3 grid((uint32_t)wgs);
     fp8_mm_tile_kernel<C, SUMS, BLKB><<<grid, C::NT, 0, s>>>(a);
 }
 
@@ -608,14 +662,14 @@ Plan plan(int M, int N, int nkb, int sums, int rb)
         int bm, bn;
         double step, tile;
     } tiles[] = {{TILE_64, 64, 128, full ? 0.62 : 0.37, 1.5},
-                 {TILE_128, 128, 128, full ? 1.3 : 0.5, 2.5},
-                 {TILE_192, 192, 256, blkb ? 2.2 : 2.4, 5.5},
-                 {TILE_256, 256, 256, full ? 3.2 : 1.52, 5.5}};
+                 {TILE_128, 128, 128, full ? 1.3 : 0.5, full ? 1.8 : 2.5},
+                 {TILE_192, 192, 256, !full ? 1.35 : blkb ? 2.2 : 2.4, full ? 5.0 : 4.2},
+                 {TILE_256, 256, 256, full ? 3.2 : 1.52, full ? 5.0 : 4.2}};
     for (const auto &c : tiles) {
         // full sums hold their operands widened: with a scale for each row of B
         // as well, 256 x 256 does not fit the registers (4.0 a step, 192 x 256
-        // 2.4). Fast sums have no use for 192 x 256.
-        if (c.k == (!full ? TILE_192 : blkb ? -1 : TILE_256))
+        // 2.4)
+        if (c.k == TILE_256 && full && !blkb)
             continue;
         for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
             const double wg = up(M, c.bm) * up(N, c.bn) * parts;
@@ -637,9 +691,7 @@ template <int SUMS, bool BLKB> void launch_sums(const MmArgs &a, Kernel k, hipSt
     case TILE_64: return launch_tile<T64, SUMS, BLKB>(a, s);
     case TILE_128: return launch_tile<T128, SUMS, BLKB>(a, s);
     case TILE_192:
-        if constexpr (SUMS == TWELL_SUMS_F32)
-            launch_tile<T192, SUMS, BLKB>(a, s);
-        return;
+        return launch_tile<T192, SUMS, BLKB>(a, s);
     case TILE_256:
         if constexpr (SUMS == TWELL_SUMS_FP8 || BLKB)
             launch_tile<T256, SUMS, BLKB>(a, s);
