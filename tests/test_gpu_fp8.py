@@ -371,3 +371,23 @@ def test_product_large(M, N, K, rb):
             got = tw.fp8_matmul(A, B, out_dtype=out, fast_sums=fast)
             tol = (k * ref.U32 + (ref.FAST if fast else 0)) * mag + ref.ustore(out) * want.abs()
             ref.assert_within(got, want, tol, f"product {out} {fast}")
+
+
+@pytest.mark.parametrize("rb", [128, 1])
+@pytest.mark.parametrize("M,N,K,shift", [(4173, 4226, 64, 0), (4173, 4226, 300, 3),
+                                         (8192, 5632, 128, 0), (2500, 16390, 1025, 1),
+                                         (24577, 513, 640, 5)])
+def test_product_of_many_tiles(M, N, K, shift, rb):
+    """More large tiles than the chip has CUs, so that workgroups go on to
+    further ones, whole and cut; sums that are exact in float32, results in a
+    slice of a wider matrix that keeps what is around them."""
+    print("[case] fp8_matmul many tiles", M, N, K, shift, rb, flush=True)
+    a, b = _fp8(M, K, 1, 5, True), _fp8(N, K, rb, 6, True)
+    want = ref.dequant(*a, 1).to(DEV) @ ref.dequant(*b, rb).to(DEV).t()
+    A, B = _up(a, K, 1), _up(b, K, rb)
+    for out in (F32, BF):
+        for fast in (False, True):
+            wide = torch.full((M, N + 2 * shift), 7.0, dtype=out, device=DEV)
+            got = tw.fp8_matmul(A, B, out=wide[:, shift:shift + N], out_dtype=out, fast_sums=fast)
+            assert torch.equal(got, want.to(F32).to(out)), (out, fast)
+            assert bool((wide[:, :shift] == 7).all()) and bool((wide[:, shift + N:] == 7).all())
