@@ -37,10 +37,11 @@ DEVI uint32_t row16_umax(uint32_t v)
 }
 DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// Scale of a block from the bits of its largest absolute value, and about
-// 1 / scale. The scale is amax / 448 rounded once: the product's error is one
-// fused step away (amax - q 448 is exact in the fused multiply-add). An
-// infinite or NaN amax is the scale itself, and makes 1 / scale NaN.
+// Scale of a block from the bits of its largest absolute value, and a little
+// over 1 / scale (2^-22 to 2^-20 of it). The scale is amax / 448 rounded once:
+// the product's error is one fused step away (amax - q 448 is exact in the
+// fused multiply-add). An infinite or NaN amax is the scale itself, and makes
+// 1 / scale NaN.
 struct BlockScale {
     float s, inv;
 };
@@ -52,24 +53,27 @@ DEVI BlockScale fp8_scale(uint32_t amax_bits)
     BlockScale b;
     b.s = amax_bits >= 0x7f800000u ? amax : fmaf(fmaf(-q, FP8_MAX, amax), 1.f / FP8_MAX, q);
     const float y = __builtin_amdgcn_rcpf(b.s);
-    b.inv = fmaf(fmaf(-b.s, y, 1.f), y, y); // NaN for an infinite scale
+    b.inv = fmaf(fmaf(-b.s, y, 1.f + 0x1p-21f), y, y); // NaN for an infinite scale
     return b;
 }
 
-// A float whose e4m3 rounding is that of v / s. Ties between e4m3 values, and
-// the values, have their low 19 bits clear; t is the float of that kind
-// nearest to the quotient, and v - t s, whose sign the fused multiply-add gives
-// exactly, says on which side of t the quotient lies. t moved by DELTA to that
-// side rounds like it: DELTA is more than half a unit of the largest quotients
-// and less than the distance of any other such t from a tie. (Rounding the
-// float quotient instead rounds twice: of bfloat16 values over a bfloat16
-// amax, one in 250 lies that near to a tie.)
+// A float whose e4m3 rounding is that of v / s. The e4m3 values and the ties
+// between them are points of a grid, of floats whose low 19 bits are clear. v
+// inv is a little past the quotient, so its grid point t is the quotient's
+// own, or the next one where the quotient lies just before that; v - t s, whose
+// sign the fused multiply-add gives exactly, says which, or that the quotient
+// is t. t moved by DELTA to that side is in the quotient's open interval of
+// the grid and rounds like it: DELTA is more than half a unit of the largest
+// quotients and less than the grid's step wherever a tie is near. Where a
+// quotient matters (2^-10 and more) a remainder is 0 or at least 2^-110.
+// (Rounding the float quotient instead rounds twice: of bfloat16 values over a
+// bfloat16 amax, one in 250 lies that near to a tie.)
 DEVI float e4m3_quotient(float v, BlockScale b)
 {
-    constexpr float DELTA = 0x1.8p-16f;
-    const float t = __uint_as_float((__float_as_uint(v * b.inv) + 0x40000u) & 0xfff80000u);
-    const float rest = fmaf(-t, b.s, v) * 0x1p100f;
-    return t + __builtin_amdgcn_fmed3f(rest, -DELTA, DELTA);
+    constexpr float DELTA = 0x1.8p-16f, SMALL = 0x1p-120f;
+    const float t = __uint_as_float(__float_as_uint(v * b.inv) & 0xfff80000u);
+    const float rest = __builtin_amdgcn_fmed3f(fmaf(-t, b.s, v), -SMALL, SMALL);
+    return fmaf(rest, DELTA / SMALL, t);
 }
 DEVI uint32_t quant4(const float *v, BlockScale b)
 {

@@ -13,6 +13,8 @@
 // few elements so that several tiles are on a CU, one loading while another
 // stores (64 elements a thread took 19.1 us for 8192 x 2048 bf16 and its
 // transpose).
+#include <type_traits>
+
 #include "fp8.hpp"
 
 namespace {
@@ -38,6 +40,24 @@ DEVI uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 DEVI int turn_word(int c, int rr)
 {
     return (c + (c >> 6)) * 32 + (rr ^ (((c >> 3) & 7) << 2));
+}
+
+// The value of lane I of each four.
+template <int I> DEVI float quad_lane(float v)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), I * 0x55,
+                                                              0xF, 0xF, false));
+}
+
+// Bytes of four rows by four columns (a row a word, first column lowest) turned:
+// a column a word.
+DEVI void turn4(uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3, uint32_t *c)
+{
+    // perm(a, b, sel): byte n is byte sel_n of b (0-3) and a (4-7)
+    const uint32_t a = __builtin_amdgcn_perm(r1, r0, 0x05010400), b = __builtin_amdgcn_perm(r1, r0, 0x07030602);
+    const uint32_t d = __builtin_amdgcn_perm(r3, r2, 0x05010400), e = __builtin_amdgcn_perm(r3, r2, 0x07030602);
+    c[0] = __builtin_amdgcn_perm(d, a, 0x05040100), c[1] = __builtin_amdgcn_perm(d, a, 0x07060302);
+    c[2] = __builtin_amdgcn_perm(e, b, 0x05040100), c[3] = __builtin_amdgcn_perm(e, b, 0x07060302);
 }
 
 // Eight consecutive elements of a row in 32-bit words, as they are stored, and
@@ -169,40 +189,61 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
                 a.st[(int64_t)tr * a.C + tc * TS + tid] = b.s;
         }
     }
-    if constexpr (ROWS) {
-        const int64_t pitch = fp8_pitch(a.C);
+    uint2 q[RPT]; // this thread's rows in 8 bits
+    if constexpr (ROWS || BLOCK) {
+        BlockScale b = sb;
+        if constexpr (!BLOCK) { // each of four lanes makes one row's scale
+            uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < RPT; ++i) {
-            BlockScale b = sb;
-            if (!BLOCK) {
-                uint32_t m = 0;
+            for (int i = 0; i < RPT; ++i) {
+                uint32_t t = 0;
 #pragma unroll
                 for (int k = 0; k < W; ++k)
-                    m = E::max2(m, v[i].abs(k));
-                b = fp8_scale(row16_umax(E::top(m)));
+                    t = E::max2(t, v[i].abs(k));
+                t = row16_umax(E::top(t));
+                m = (cc & 3) == i ? t : m;
             }
+            b = fp8_scale(m);
+            if (cc < RPT && r0 + cc < a.R)
+                a.s[(int64_t)tc * a.R + r0 + cc] = b.s;
+        }
+        auto row = [&](auto I) {
+            constexpr int i = decltype(I)::value;
+            const BlockScale br = BLOCK ? b : BlockScale{quad_lane<i>(b.s), quad_lane<i>(b.inv)};
             float u[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 u[k] = v[i][k];
-            const int r = r0 + i;
-            if (r < a.R) {
-                *(uint2 *)(a.q + (int64_t)r * pitch + c0) = quant8(u, b);
-                if (!BLOCK && cc == 0)
-                    a.s[(int64_t)tc * a.R + r] = b.s;
-            }
-        }
+            q[i] = quant8(u, br);
+        };
+        row(std::integral_constant<int, 0>());
+        row(std::integral_constant<int, 1>());
+        row(std::integral_constant<int, 2>());
+        row(std::integral_constant<int, 3>());
+    }
+    if constexpr (ROWS) {
+        const int64_t pitch = fp8_pitch(a.C);
+#pragma unroll
+        for (int i = 0; i < RPT; ++i)
+            if (r0 + i < a.R)
+                *(uint2 *)(a.q + (int64_t)(r0 + i) * pitch + c0) = q[i];
     }
     if constexpr (COLS) {
-        if (!BLOCK)
+        if constexpr (BLOCK) { // one scale: the rows' bytes, turned
+            uint32_t c[8];
+            turn4(q[0].x, q[1].x, q[2].x, q[3].x, c);
+            turn4(q[0].y, q[1].y, q[2].y, q[3].y, c + 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                turn[turn_word(cc * 8 + k, rr)] = c[k];
+        } else {
             __syncthreads(); // cs
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            BlockScale b = sb;
-            if (!BLOCK)
-                b = BlockScale{cs[0][cc * 8 + k], cs[1][cc * 8 + k]};
-            const float u[RPT] = {v[0][k], v[1][k], v[2][k], v[3][k]};
-            turn[turn_word(cc * 8 + k, rr)] = quant4(u, b);
+            for (int k = 0; k < 8; ++k) {
+                const BlockScale b = {cs[0][cc * 8 + k], cs[1][cc * 8 + k]};
+                const float u[RPT] = {v[0][k], v[1][k], v[2][k], v[3][k]};
+                turn[turn_word(cc * 8 + k, rr)] = quant4(u, b);
+            }
         }
         __syncthreads();
         const int64_t pitch = fp8_pitch(a.R);
