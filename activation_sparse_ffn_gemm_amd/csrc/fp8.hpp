@@ -132,8 +132,12 @@ DEVI void stg16u(void *p, uint4 v)
 // 8 (l + LPR c) .. + 7 for c < C, zeros past d. Loads leave the raw bits in
 // the registers (bf16: the first four words), so that the loads of several
 // arrays are in flight together; widen() makes them floats in place.
-// RAG: d is no multiple of eight, and one lane's last chunk is cut.
-template <int LPR, int C, bool RAG> struct Row {
+// FULL: every lane has its elements, and loads are not tested (a row that is
+// not there is the caller's to avoid); EIGHTS: some lanes may have none;
+// RAGGED: d is no multiple of eight, and one lane's last chunk is cut.
+enum RowKind { FULL, EIGHTS, RAGGED };
+template <int LPR, int C, RowKind KIND> struct Row {
+    static constexpr bool RAG = KIND == RAGGED;
     float v[C][8];
 
     DEVI void put(int c, int i, uint4 q)
@@ -152,13 +156,14 @@ template <int LPR, int C, bool RAG> struct Row {
         uint4 q[C], r[C]; // r: the second half of a float32 chunk
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            q[c] = r[c] = make_uint4(0, 0, 0, 0);
+            if (KIND != FULL)
+                q[c] = r[c] = make_uint4(0, 0, 0, 0);
         if (dt == TWELL_BF16) {
             const uint16_t *p = (const uint16_t *)row;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
-                if (j + 8 <= d) {
+                if (KIND == FULL || j + 8 <= d) {
                     q[c] = ldg16u(p + j);
                 } else if (RAG && j < d) {
                     uint32_t w[4];
@@ -174,7 +179,7 @@ template <int LPR, int C, bool RAG> struct Row {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const int j = 8 * (lane + LPR * c);
-                if (j + 8 <= d) {
+                if (KIND == FULL || j + 8 <= d) {
                     q[c] = ldg16u(p + j);
                     r[c] = ldg16u(p + j + 4);
                 } else if (RAG && j < d) {
@@ -190,7 +195,8 @@ template <int LPR, int C, bool RAG> struct Row {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             put(c, 0, q[c]);
-            put(c, 4, r[c]);
+            if (KIND != FULL || dt != TWELL_BF16)
+                put(c, 4, r[c]);
         }
     }
 

@@ -10,7 +10,9 @@
 // registers. The row is taken in 64 bits there, so that q is the e4m3 value
 // nearest to n / scale: in 32 bits the roundings of h, h r, h r gain, the scale
 // and the quotient put one value in a million on the wrong side of a tie
-// between two e4m3 values, a sixteenth off. The arithmetic hides behind memory.
+// between two e4m3 values, a sixteenth off. Beside a residual's memory traffic
+// the arithmetic is hidden (8192 x 2048: 31.4 us, bf16 out 31.2); of a bf16 x
+// alone, 50 MB, it is the bound (16.9 us).
 //
 // Backward, per row, with xh = h r and dg = dn gain:
 //   dh = r (dg - xh mean(dg xh)) + dres,   dgain = sum over rows of dn xh.
@@ -20,7 +22,10 @@
 // partial row of float32, and a second kernel adds the partial rows in
 // workgroup order: results repeat bit for bit (no atomics).
 //
-// Both are bound by HBM: each array is read or written once.
+// Both are bound by HBM: each array is read or written once (8192 x 2048,
+// float32 x or dn, bf16 stream: forward 5.4 TB/s, backward 4.8). What is left
+// to save beside the traffic is instructions: rows that fill their lanes are
+// kernels of their own, without zeroed registers and tests (36 -> 31 us).
 #include "fp8.hpp"
 
 namespace {
@@ -64,7 +69,7 @@ DEVI double rsqrt64(double v)
 // Sum over the LPR lanes that share a row, in every one of them. Past a wave
 // it goes through buf (a float for each wave of the workgroup); each sum of a
 // kernel has a buf of its own, so no barrier is needed before it is written.
-DEVI double wave_sum(double v)
+DEVI double wave_sum64(double v)
 {
     v += dpp_mov<0xB1>(v);
     v += dpp_mov<0x4E>(v);
@@ -84,7 +89,10 @@ template <int LPR, class F> DEVI F row_sum(F v, F *buf)
             v += __shfl_xor(v, 16, 64);
         return v;
     } else {
-        v = wave_sum(v);
+        if constexpr (sizeof(F) == 8)
+            v = wave_sum64(v);
+        else
+            v = wave_sum(v);
         if constexpr (LPR > 64) {
             constexpr int W = LPR / 64; // waves of a row
             const int w = wave_id();
@@ -114,21 +122,22 @@ struct FwdArgs {
 
 constexpr int fwd_threads(int lpr) { return lpr < 256 ? 256 : lpr; }
 
-template <int LPR, int C, bool RAG>
+template <int LPR, int C, RowKind KIND>
 __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a)
 {
     constexpr int RPB = fwd_threads(LPR) / LPR; // rows per workgroup
     __shared__ float buf[fwd_threads(LPR) / 64];
     const int lane = row_lane<LPR>();
     const int64_t t = (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
-    // a workgroup's rows past T are empty: they load and store nothing
+    // a workgroup's rows past T store nothing; they read the last row
     const int d = t < a.T ? a.d : 0;
-    Row<LPR, C, RAG> h, g;
-    h.load(row_ptr(a.x, a.dtx, a.ldx, t), a.dtx, d, lane);
+    const int64_t tl = t < a.T ? t : a.T - 1;
+    Row<LPR, C, KIND> h, g;
+    h.load(row_ptr(a.x, a.dtx, a.ldx, tl), a.dtx, a.d, lane);
     if (a.res) {
-        Row<LPR, C, RAG> r;
-        r.load(row_ptr(a.res, a.dtr, a.ldr, t), a.dtr, d, lane);
-        g.load(a.gain, a.dtg, d, lane);
+        Row<LPR, C, KIND> r;
+        r.load(row_ptr(a.res, a.dtr, a.ldr, tl), a.dtr, a.d, lane);
+        g.load(a.gain, a.dtg, a.d, lane);
         h.widen(a.dtx);
         r.widen(a.dtr);
 #pragma unroll
@@ -138,7 +147,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
                 h.v[c][i] += r.v[c][i];
         h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
     } else {
-        g.load(a.gain, a.dtg, d, lane);
+        g.load(a.gain, a.dtg, a.d, lane);
         h.widen(a.dtx);
     }
     float ss = 0.f;
@@ -159,7 +168,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
 }
 
 // The same with n in 8 bits.
-template <int LPR, int C, bool RAG>
+template <int LPR, int C, RowKind KIND>
 __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs a)
 {
     constexpr int RPB = fwd_threads(LPR) / LPR;
@@ -167,14 +176,15 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
     const int lane = row_lane<LPR>();
     const int64_t t = (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
     const int d = t < a.T ? a.d : 0;
+    const int64_t tl = t < a.T ? t : a.T - 1;
     double p[C][8]; // h, then h gain
     double ss = 0.;
-    Row<LPR, C, RAG> h, g;
-    h.load(row_ptr(a.x, a.dtx, a.ldx, t), a.dtx, d, lane);
+    Row<LPR, C, KIND> h, g;
+    h.load(row_ptr(a.x, a.dtx, a.ldx, tl), a.dtx, a.d, lane);
     if (a.res) {
-        Row<LPR, C, RAG> r;
-        r.load(row_ptr(a.res, a.dtr, a.ldr, t), a.dtr, d, lane);
-        g.load(a.gain, a.dtg, d, lane);
+        Row<LPR, C, KIND> r;
+        r.load(row_ptr(a.res, a.dtr, a.ldr, tl), a.dtr, a.d, lane);
+        g.load(a.gain, a.dtg, a.d, lane);
         h.widen(a.dtx);
         r.widen(a.dtr);
 #pragma unroll
@@ -186,7 +196,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
             }
         h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
     } else {
-        g.load(a.gain, a.dtg, d, lane);
+        g.load(a.gain, a.dtg, a.d, lane);
         h.widen(a.dtx);
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -250,7 +260,7 @@ struct BwdArgs {
 // few partial rows for the waves in flight.
 constexpr int bwd_threads(int lpr) { return lpr < 512 ? 512 : lpr; }
 
-template <int LPR, int C, bool RAG>
+template <int LPR, int C, RowKind KIND>
 __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a)
 {
     constexpr int NT = bwd_threads(LPR), RPB = NT / LPR, NW = NT / 64;
@@ -265,18 +275,21 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             acc[c][i] = 0.f;
-    Row<LPR, C, RAG> g;
+    Row<LPR, C, KIND> g;
     g.load(a.gain, a.dtg, a.d, lane);
     g.widen(a.dtg);
     int it = 0;
     for (int64_t t0 = (int64_t)blockIdx.x * RPB; t0 < a.T; t0 += (int64_t)gridDim.x * RPB, ++it) {
         const int64_t t = t0 + row;
-        const int d = t < a.T ? a.d : 0; // rows past T are empty
-        Row<LPR, C, RAG> h, dn, rs;
-        h.load(row_ptr(a.h, a.dth, a.ldh, t), a.dth, d, lane);
-        dn.load(row_ptr(a.dn, a.dtdn, a.lddn, t), a.dtdn, d, lane);
+        // rows past T store nothing and add nothing; they read the last row
+        const bool in = RPB == 1 || t < a.T;
+        const int d = in ? a.d : 0;
+        const int64_t tl = in ? t : a.T - 1;
+        Row<LPR, C, KIND> h, dn, rs;
+        h.load(row_ptr(a.h, a.dth, a.ldh, tl), a.dth, a.d, lane);
+        dn.load(row_ptr(a.dn, a.dtdn, a.lddn, tl), a.dtdn, a.d, lane);
         if (a.dres)
-            rs.load(row_ptr(a.dres, a.dtdres, a.lddres, t), a.dtdres, d, lane);
+            rs.load(row_ptr(a.dres, a.dtdres, a.lddres, tl), a.dtdres, a.d, lane);
         h.widen(a.dth);
         dn.widen(a.dtdn);
         float ss = 0.f, dot = 0.f;
@@ -297,7 +310,7 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float xh = h.v[c][i] * r;
-                acc[c][i] = fmaf(dn.v[c][i], xh, acc[c][i]);
+                acc[c][i] = in ? fmaf(dn.v[c][i], xh, acc[c][i]) : acc[c][i];
                 h.v[c][i] = r * fmaf(-xh, m, g.v[c][i] * dn.v[c][i]);
             }
         if (a.dres) {
@@ -380,6 +393,12 @@ int row_lanes(int d)
     return l;
 }
 
+RowKind row_kind(int d)
+{
+    const int l = row_lanes(d);
+    return d & 7 ? RAGGED : d == 8 * l || d == 16 * l ? FULL : EIGHTS;
+}
+
 // Workgroups (and partial rows of dgain) of the backward: one for rows that
 // take at most four turns (it writes dgain itself), else up to sixteen waves'
 // worth for each CU (at 8192 x 2048: 48 us; half of them 52, twice 53).
@@ -391,45 +410,45 @@ int bwd_groups(int T, int d)
     return g <= 4 ? (g > 0) : g < most ? (int)g : most;
 }
 
-template <int LPR, int C, bool RAG> void fwd_one(const FwdArgs &a, hipStream_t s)
+template <int LPR, int C, RowKind KIND> void fwd_one(const FwdArgs &a, hipStream_t s)
 {
     constexpr int NT = fwd_threads(LPR), RPB = NT / LPR;
     const dim3 grid((a.T + RPB - 1) / RPB);
     if (a.q)
-        rmsnorm_fwd8_kernel<LPR, C, RAG><<<grid, NT, 0, s>>>(a);
+        rmsnorm_fwd8_kernel<LPR, C, KIND><<<grid, NT, 0, s>>>(a);
     else
-        rmsnorm_fwd_kernel<LPR, C, RAG><<<grid, NT, 0, s>>>(a);
+        rmsnorm_fwd_kernel<LPR, C, KIND><<<grid, NT, 0, s>>>(a);
 }
 
-template <bool RAG> void fwd_sizes(const FwdArgs &a, hipStream_t s)
+template <RowKind KIND> void fwd_sizes(const FwdArgs &a, hipStream_t s)
 {
     switch (row_lanes(a.d)) {
-    case 16: return fwd_one<16, 1, RAG>(a, s);
-    case 32: return fwd_one<32, 1, RAG>(a, s);
-    case 64: return fwd_one<64, 1, RAG>(a, s);
-    case 128: return fwd_one<128, 1, RAG>(a, s);
-    case 256: return fwd_one<256, 1, RAG>(a, s);
-    case 512: return fwd_one<512, 1, RAG>(a, s);
+    case 16: return fwd_one<16, 1, KIND>(a, s);
+    case 32: return fwd_one<32, 1, KIND>(a, s);
+    case 64: return fwd_one<64, 1, KIND>(a, s);
+    case 128: return fwd_one<128, 1, KIND>(a, s);
+    case 256: return fwd_one<256, 1, KIND>(a, s);
+    case 512: return fwd_one<512, 1, KIND>(a, s);
     }
-    return a.d <= 8192 ? fwd_one<1024, 1, RAG>(a, s) : fwd_one<1024, 2, RAG>(a, s);
+    return a.d <= 8192 ? fwd_one<1024, 1, KIND>(a, s) : fwd_one<1024, 2, KIND>(a, s);
 }
 
-template <int LPR, int C, bool RAG> void bwd_one(const BwdArgs &a, int G, hipStream_t s)
+template <int LPR, int C, RowKind KIND> void bwd_one(const BwdArgs &a, int G, hipStream_t s)
 {
-    rmsnorm_bwd_kernel<LPR, C, RAG><<<G, bwd_threads(LPR), 0, s>>>(a);
+    rmsnorm_bwd_kernel<LPR, C, KIND><<<G, bwd_threads(LPR), 0, s>>>(a);
 }
 
-template <bool RAG> void bwd_sizes(const BwdArgs &a, int G, hipStream_t s)
+template <RowKind KIND> void bwd_sizes(const BwdArgs &a, int G, hipStream_t s)
 {
     switch (row_lanes(a.d)) {
-    case 16: return bwd_one<16, 1, RAG>(a, G, s);
-    case 32: return bwd_one<32, 1, RAG>(a, G, s);
-    case 64: return bwd_one<64, 1, RAG>(a, G, s);
-    case 128: return bwd_one<128, 1, RAG>(a, G, s);
-    case 256: return bwd_one<256, 1, RAG>(a, G, s);
-    case 512: return bwd_one<512, 1, RAG>(a, G, s);
+    case 16: return bwd_one<16, 1, KIND>(a, G, s);
+    case 32: return bwd_one<32, 1, KIND>(a, G, s);
+    case 64: return bwd_one<64, 1, KIND>(a, G, s);
+    case 128: return bwd_one<128, 1, KIND>(a, G, s);
+    case 256: return bwd_one<256, 1, KIND>(a, G, s);
+    case 512: return bwd_one<512, 1, KIND>(a, G, s);
     }
-    return a.d <= 8192 ? bwd_one<1024, 1, RAG>(a, G, s) : bwd_one<1024, 2, RAG>(a, G, s);
+    return a.d <= 8192 ? bwd_one<1024, 1, KIND>(a, G, s) : bwd_one<1024, 2, KIND>(a, G, s);
 }
 
 } // namespace
@@ -450,10 +469,11 @@ hipError_t launch_rmsnorm_fwd(const twell_mat_t *x, const twell_mat_t *res, cons
     else
         a.n = n->data, a.ldn = n->ld, a.dtn = n->dtype;
     Timer tm(timing, s);
-    if (a.d & 7)
-        fwd_sizes<true>(a, s);
-    else
-        fwd_sizes<false>(a, s);
+    switch (row_kind(a.d)) {
+    case FULL: fwd_sizes<FULL>(a, s); break;
+    case EIGHTS: fwd_sizes<EIGHTS>(a, s); break;
+    case RAGGED: fwd_sizes<RAGGED>(a, s); break;
+    }
     tm.mark("rmsnorm_fwd");
     return hipGetLastError();
 }
@@ -475,10 +495,11 @@ hipError_t launch_rmsnorm_bwd(const twell_mat_t *dn, const twell_mat_t *h, const
     a.part = G == 1 ? dgain : (float *)ws;
     Timer tm(timing, s);
     if (a.T > 0) {
-        if (a.d & 7)
-            bwd_sizes<true>(a, G, s);
-        else
-            bwd_sizes<false>(a, G, s);
+        switch (row_kind(a.d)) {
+        case FULL: bwd_sizes<FULL>(a, G, s); break;
+        case EIGHTS: bwd_sizes<EIGHTS>(a, G, s); break;
+        case RAGGED: bwd_sizes<RAGGED>(a, G, s); break;
+        }
     }
     tm.mark("rmsnorm_bwd");
     if (G != 1) {
