@@ -410,7 +410,7 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
                         const uint4 v = *(const uint4 *)(buf + (r0 + rr) * C::OROW + c8 * 16);
                         T *row = (T *)out + m * ld;
                         if (whole || (m < a.M && n + VPL <= a.N)) {
-                            stg16u(row + n, v);
+                            stg16u_nt(row + n, v);
                         } else if (m < a.M) {
                             const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -226,7 +226,7 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
 #pragma unroll
         for (int i = 0; i < RPT; ++i)
             if (r0 + i < a.R)
-                *(uint2 *)(a.q + (int64_t)(r0 + i) * pitch + c0) = q[i];
+                stg8_nt(a.q + (int64_t)(r0 + i) * pitch + c0, q[i]);
     }
     if constexpr (COLS) {
         if constexpr (BLOCK) { // one scale: the rows' bytes, turned
@@ -251,8 +251,8 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
         for (int i = 0; i < TS * 8 / NT; ++i) { // 16 bytes: column c, rows 16 ch ..
             const int q = tid + i * NT, c = q >> 3, ch = q & 7;
             if (tc * TS + c < a.C)
-                *(uint4 *)(a.qt + (int64_t)(tc * TS + c) * pitch + tr * TS + ch * 16) =
-                    *(const uint4 *)&turn[turn_word(c, 4 * ch)];
+                stg16u_nt(a.qt + (int64_t)(tc * TS + c) * pitch + tr * TS + ch * 16,
+                          *(const uint4 *)&turn[turn_word(c, 4 * ch)]);
         }
     }
 }

@@ -11,7 +11,7 @@
 // nearest to n / scale: in 32 bits the roundings of h, h r, h r gain, the scale
 // and the quotient put one value in a million on the wrong side of a tie
 // between two e4m3 values, a sixteenth off. Beside a residual's memory traffic
-// the arithmetic is hidden (8192 x 2048: 31.4 us, bf16 out 31.2); of a bf16 x
+// the arithmetic is hidden (8192 x 2048: 29.0 us, bf16 out 29.6); of a bf16 x
 // alone, 50 MB, it is the bound (16.9 us).
 //
 // Backward, per row, with xh = h r and dg = dn gain:
@@ -23,7 +23,7 @@
 // workgroup order: results repeat bit for bit (no atomics).
 //
 // Both are bound by HBM: each array is read or written once (8192 x 2048,
-// float32 x or dn, bf16 stream: forward 5.4 TB/s, backward 4.8). What is left
+// float32 x or dn, bf16 stream: forward 5.2 to 5.7 TB/s, backward 4.8). What is left
 // to save beside the traffic is instructions: rows that fill their lanes are
 // kernels of their own, without zeroed registers and tests (36 -> 31 us).
 #include "fp8.hpp"
@@ -145,7 +145,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 h.v[c][i] += r.v[c][i];
-        h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
+        h.template store<true>(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
     } else {
         g.load(a.gain, a.dtg, a.d, lane);
         h.widen(a.dtx);
@@ -164,7 +164,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             h.v[c][i] = h.v[c][i] * r * g.v[c][i];
-    h.store(row_ptr(a.n, a.dtn, a.ldn, t), a.dtn, d, lane);
+    h.template store<true>(row_ptr(a.n, a.dtn, a.ldn, t), a.dtn, d, lane);
 }
 
 // The same with n in 8 bits.
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
                 p[c][i] = (double)h.v[c][i] + (double)r.v[c][i];
                 h.v[c][i] += r.v[c][i];
             }
-        h.store(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
+        h.template store<true>(row_ptr(a.h, a.dtr, a.ldh, t), a.dtr, d, lane);
     } else {
         g.load(a.gain, a.dtg, a.d, lane);
         h.widen(a.dtx);
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
         for (int i = 0; i < 8; ++i)
             p[c][i] *= k;
         if (j < pitch && t < a.T) {
-            *(uint2 *)(a.q + t * pitch + j) = quant8(p[c]);
+            stg8_nt(a.q + t * pitch + j, quant8(p[c]));
             if ((lane & 15) == 0)
                 a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = s;
         }
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
                 for (int i = 0; i < 8; ++i)
                     h.v[c][i] += rs.v[c][i];
         }
-        h.store(row_ptr(a.dh, a.dtdh, a.lddh, t), a.dtdh, d, lane);
+        h.template store<false>(row_ptr(a.dh, a.dtdh, a.lddh, t), a.dtdh, d, lane);
     }
     // the row slots' sums, added by halves
     float *part = a.part + (int64_t)blockIdx.x * a.d;
