@@ -132,9 +132,9 @@ DEVI void stg16u(void *p, uint4 v)
 // stay in L2, whose lines would otherwise be evicted one by one behind the
 // loads. Measured on buffers in turn, with it and without: product of 8192 x
 // 5632 over 2048 90.5 and 100.7 us, quantisation of 8192 x 2048 both ways 14.0
-// and 15.6, norm of 8192 x 2048 29.0 and 31.3 (of 2000 x 8192 to 8 bits 35.8
-// and 32.3); a product that reads them next takes the same time. The norm's
-// backward loses as often as it gains and keeps the ordinary store.
+// and 15.6, norm of 8192 x 2048 29.0 and 31.3; a product that reads them next
+// takes the same time. The norm's backward loses as often as it gains and keeps
+// the ordinary store; loads of this kind are slower (norm 30.4).
 typedef uint32_t u32x4u_t __attribute__((ext_vector_type(4), aligned(2), may_alias));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2), may_alias));
 DEVI void stg16u_nt(void *p, uint4 v)
@@ -214,7 +214,7 @@ template <int LPR, int C, RowKind KIND> struct Row {
         for (int c = 0; c < C; ++c) {
             put(c, 0, q[c]);
             if (KIND != FULL || dt != TWELL_BF16)
-                put(c, 4, r[c]);
+                put(c, 4, r[c]); // (FULL has none for bf16)
         }
     }
 

@@ -393,10 +393,13 @@ int row_lanes(int d)
     return l;
 }
 
+// Rows that fill their lanes leave out the tests; not those of sixteen waves:
+// without tests the compiler holds more loads at once, and past 64 registers a
+// CU has one such row instead of two (2000 x 8192 to 8 bits: 36 and 31 us).
 RowKind row_kind(int d)
 {
     const int l = row_lanes(d);
-    return d & 7 ? RAGGED : d == 8 * l || d == 16 * l ? FULL : EIGHTS;
+    return d & 7 ? RAGGED : d == 8 * l && l < 1024 ? FULL : EIGHTS;
 }
 
 // Workgroups (and partial rows of dgain) of the backward: one for rows that
@@ -430,7 +433,8 @@ template <RowKind KIND> void fwd_sizes(const FwdArgs &a, hipStream_t s)
     case 256: return fwd_one<256, 1, KIND>(a, s);
     case 512: return fwd_one<512, 1, KIND>(a, s);
     }
-    return a.d <= 8192 ? fwd_one<1024, 1, KIND>(a, s) : fwd_one<1024, 2, KIND>(a, s);
+    if constexpr (KIND != FULL)
+        a.d <= 8192 ? fwd_one<1024, 1, KIND>(a, s) : fwd_one<1024, 2, KIND>(a, s);
 }
 
 template <int LPR, int C, RowKind KIND> void bwd_one(const BwdArgs &a, int G, hipStream_t s)
@@ -448,7 +452,8 @@ template <RowKind KIND> void bwd_sizes(const BwdArgs &a, int G, hipStream_t s)
     case 256: return bwd_one<256, 1, KIND>(a, G, s);
     case 512: return bwd_one<512, 1, KIND>(a, G, s);
     }
-    return a.d <= 8192 ? bwd_one<1024, 1, KIND>(a, G, s) : bwd_one<1024, 2, KIND>(a, G, s);
+    if constexpr (KIND != FULL)
+        a.d <= 8192 ? bwd_one<1024, 1, KIND>(a, G, s) : bwd_one<1024, 2, KIND>(a, G, s);
 }
 
 } // namespace
