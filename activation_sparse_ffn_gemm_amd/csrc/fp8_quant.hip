@@ -9,10 +9,12 @@
 // the 16 lanes that share a row; column amaxes go over the thread's own rows,
 // the wave's other lanes and the workgroup's waves (LDS). The transpose is
 // turned in LDS as bytes. bf16 stays two to a word until it is quantised, and
-// its maxima are taken two at a time. Bound by HBM: x in, q (and q_t) out; a thread holds
-// few elements so that several tiles are on a CU, one loading while another
-// stores (64 elements a thread took 19.1 us for 8192 x 2048 bf16 and its
-// transpose).
+// its maxima are taken two at a time.
+//
+// Bound by HBM (x in, q and q_t out) with the arithmetic close behind: 8192 x
+// 2048 bf16 and its transpose 14.0 us, 4.9 TB/s; a thread holds few elements so
+// that several tiles are on a CU, one loading while another stores (64 elements
+// a thread 19.1, half as many workgroups a CU 16.1 where this was 15.9).
 #include <type_traits>
 
 #include "fp8.hpp"
