@@ -107,6 +107,14 @@ template <> struct Frag<TWELL_SUMS_F32> {
 // the stores drain beside its first steps (8192 x 5632 over 2048: 93 -> 88 us).
 // Stores write whole 128-byte lines, through LDS: float32 results stored from
 // the accumulators, 64 bytes of a row at a time, took 173 us there, so 165.
+//
+// What bounds a step: fast sums, the matrix unit with the scales' steps beside
+// it (a loop of registers alone runs at 3463 TF, 1.24 us a step of 256 x 256)
+// and the loads from L2 (11 TB/s; 1.5 us with them). Full sums, vector
+// instructions: widening a wave's 11 fragments (176 instructions for 24
+// products of 192 x 256) and the scales take turns with the matrix unit; a loop
+// of registers alone with this mix takes 2.56 us a step, the kernel 2.5,
+// whatever the order of the instructions.
 template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
     static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
