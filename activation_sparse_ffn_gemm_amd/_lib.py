@@ -33,6 +33,7 @@ DECODE_T = 64  # most tokens twell_decode_fwd takes (few-token kernels up to her
 FP8_BLOCK = 128  # columns that share a scale of an 8-bit matrix
 NORM_COLS = 16384  # widest row the norm takes
 SUMS_F32, SUMS_FP8 = 0, 1  # how twell_fp8_matmul adds products
+E_WORKSPACE = -5  # status: the call needs (more) workspace
 
 c_i32, c_sz, c_p = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
 
@@ -688,8 +689,11 @@ def _new_fp8(rows, cols, block_rows, device):
 def _gain(gain, d):
     if not isinstance(gain, torch.Tensor):
         raise TwellError("gain: expected a tensor")
-    _req(gain, "gain", (d,), gain.dtype)
-    return _dt(gain)
+    dt = _DT.get(gain.dtype)
+    if dt is None or gain.shape != (d,) or not gain.is_contiguous():
+        _req(gain, "gain", (d,), gain.dtype)
+        raise TwellError(f"unsupported dtype {gain.dtype}")
+    return dt
 
 
 def _gpu(named: dict) -> int:
@@ -828,9 +832,14 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=torch.bfloat16, fast_sums: bo
     if workspace is not None:
         _ws_form(workspace)
         on["workspace"] = workspace
-    dev = _gpu(on)
-    workspace = _ws(workspace, fp8_matmul_workspace_bytes(M, N, K), out.device)
-    _check(load().twell_fp8_matmul(ma, mb, mo, SUMS_FP8 if fast_sums else SUMS_F32,
-                                   _at(workspace), 0 if workspace is None else workspace.numel(),
-                                   _timing(timing), _raw_stream(dev)), "twell_fp8_matmul")
+    args = ma, mb, mo, SUMS_FP8 if fast_sums else SUMS_F32
+    end = _timing(timing), _raw_stream(_gpu(on))
+    rc = E_WORKSPACE
+    if workspace is None:  # most sizes need none, and the call says which do
+        rc = load().twell_fp8_matmul(*args, None, 0, *end)
+    if rc == E_WORKSPACE:
+        workspace = _ws(workspace, fp8_matmul_workspace_bytes(M, N, K), out.device)
+        rc = load().twell_fp8_matmul(*args, _at(workspace),
+                                     0 if workspace is None else workspace.numel(), *end)
+    _check(rc, "twell_fp8_matmul")
     return out
