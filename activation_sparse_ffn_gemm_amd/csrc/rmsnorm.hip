@@ -109,6 +109,32 @@ template <int LPR, class F> DEVI F row_sum(F v, F *buf)
     }
 }
 
+// Sum of N values by halves: short chains of additions, small errors.
+template <int N> DEVI float tree_sum(const float *p)
+{
+    if constexpr (N == 1)
+        return p[0];
+    else
+        return tree_sum<N / 2>(p) + tree_sum<N / 2>(p + N / 2);
+}
+
+// Two float sums over a row's lanes with one barrier.
+template <int LPR> DEVI void row_sum2(float &u, float &v, float *bu, float *bv)
+{
+    if constexpr (LPR <= 64) {
+        u = row_sum<LPR>(u, bu), v = row_sum<LPR>(v, bv);
+    } else {
+        constexpr int W = LPR / 64;
+        const int w = wave_id();
+        u = wave_sum(u), v = wave_sum(v);
+        if ((threadIdx.x & 63) == 0)
+            bu[w] = u, bv[w] = v;
+        __syncthreads();
+        const int w0 = w / W * W;
+        u = tree_sum<W>(bu + w0), v = tree_sum<W>(bv + w0);
+    }
+}
+
 struct FwdArgs {
     const void *x, *res, *gain;
     void *h, *n;
@@ -238,15 +264,6 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
     }
 }
 
-// Sum of N values by halves: short chains of additions, small errors.
-template <int N> DEVI float tree_sum(const float *p)
-{
-    if constexpr (N == 1)
-        return p[0];
-    else
-        return tree_sum<N / 2>(p) + tree_sum<N / 2>(p + N / 2);
-}
-
 struct BwdArgs {
     const void *dn, *h, *gain, *dres;
     void *dh;
@@ -303,8 +320,7 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
                 dot = fmaf(g.v[c][i] * dn.v[c][i], h.v[c][i], dot);
             }
         // two buffers in turn: a wave may still read the last row's sums
-        ss = row_sum<LPR>(ss, buf[it & 1][0]);
-        dot = row_sum<LPR>(dot, buf[it & 1][1]);
+        row_sum2<LPR>(ss, dot, buf[it & 1][0], buf[it & 1][1]);
         const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
         const float m = dot * r / (float)a.d; // mean(dg xh)
 #pragma unroll
