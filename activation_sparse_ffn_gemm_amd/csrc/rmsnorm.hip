@@ -420,15 +420,24 @@ RowKind row_kind(int d)
     return d & 7 ? RAGGED : d == 8 * l && l < 1024 ? FULL : EIGHTS;
 }
 
-// Workgroups (and partial rows of dgain) of the backward: one for rows that
-// take at most four turns (it writes dgain itself), else up to sixteen waves'
-// worth for each CU (at 8192 x 2048: 48 us; half of them 52, twice 53).
+// Workgroups (and partial rows of dgain) of the backward. One for rows that
+// take at most four turns: it writes dgain itself. Many rows: up to sixteen
+// waves for each CU (at 8192 x 2048: 49 us; half of them 52, twice 53). Between
+// these, where the partial rows weigh against the rows themselves, one
+// workgroup a CU, evenly loaded (1000 x 4096: 17.5 us, with 512 of them 20.0;
+// 4096 x 1024 15.4 and 15.1), unless that leaves CUs out.
 int bwd_groups(int T, int d)
 {
     const int lpr = row_lanes(d), rpb = bwd_threads(lpr) / lpr;
     const int64_t g = ((int64_t)T + rpb - 1) / rpb;
     const int most = 256 * 1024 / bwd_threads(lpr);
-    return g <= 4 ? (g > 0) : g < most ? (int)g : most;
+    if (g <= 4)
+        return g > 0;
+    if (g >= 448 && g <= 1024) {
+        const int64_t turns = (g + 255) / 256;
+        return (int)((g + turns - 1) / turns);
+    }
+    return g < most ? (int)g : most;
 }
 
 template <int LPR, int C, RowKind KIND> void fwd_one(const FwdArgs &a, hipStream_t s)
