@@ -112,6 +112,13 @@ DEVI uint2 quant8(const double *y)
                       f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
 }
 
+// Bytes 0 .. n - 1 of eight, n clamped to 0 .. 8.
+DEVI uint2 first_bytes(int n)
+{
+    const uint64_t m = n <= 0 ? 0 : n >= 8 ? ~(uint64_t)0 : ((uint64_t)1 << 8 * n) - 1;
+    return make_uint2((uint32_t)m, (uint32_t)(m >> 32));
+}
+
 // ---- rows of any alignment
 // 16 bytes at an address that is only element-aligned: gfx950 takes unaligned
 // vector accesses, so one instruction serves every row stride.

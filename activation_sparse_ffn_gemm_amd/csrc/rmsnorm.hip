@@ -12,7 +12,7 @@
 // and the quotient put one value in a million on the wrong side of a tie
 // between two e4m3 values, a sixteenth off. Beside a residual's memory traffic
 // the arithmetic is hidden (8192 x 2048: 29.0 us, bf16 out 29.6); of a bf16 x
-// alone, 50 MB, it is the bound (16.9 us).
+// alone, 50 MB, it is the bound (16.0 us).
 //
 // Backward, per row, with xh = h r and dg = dn gain:
 //   dh = r (dg - xh mean(dg xh)) + dres,   dgain = sum over rows of dn xh.
@@ -50,6 +50,10 @@ DEVI double row16_max(double v)
     v = fmax(v, dpp_mov<0x4E>(v));
     v = fmax(v, dpp_mov<0x141>(v));
     return fmax(v, dpp_mov<0x140>(v));
+}
+DEVI float upper_word(double v)
+{
+    return __uint_as_float((uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32));
 }
 // 1 / v and 1 / sqrt(v), from the hardware's estimates by a Newton step: within
 // 2^-40 or so, where the e4m3 quotient needs 2^-30. 1 / sqrt(infinity) is 0 and
@@ -238,26 +242,51 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
             ss = fma(p[c][i], p[c][i], ss);
             p[c][i] *= (double)g.v[c][i];
         }
+    // Amax of this lane's block of h gain: before the row's sum, beside whose
+    // barrier it costs less, but not in rows that fill their lanes, which have
+    // others in flight to hide the barrier and want the registers (2000 x 8192:
+    // 31.5 us, behind the sum 31.9; 8192 x 2048 of bf16 x alone: 17.3 and 16.0).
+    constexpr bool EARLY = KIND != FULL;
+    double m[C];
+    // The 64-bit maximum passes over NaN. The upper words, read as floats, are
+    // NaN where p is NaN or infinite (no finite p comes near 2^1017), and the
+    // 32-bit maximum keeps it: such a block's amax is infinity, its codes NaN.
+    auto amax = [&](int c) {
+        float top = 0.f;
+        m[c] = 0.;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[c] = fmax(m[c], fabs(p[c][i]));
+            top = __builtin_elementwise_maximum(top, fabsf(upper_word(p[c][i])));
+        }
+        m[c] = row16_max(top == top ? m[c] : __builtin_inf());
+    };
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (EARLY)
+            amax(c);
     ss = row_sum<LPR>(ss, buf);
     const double r = rsqrt64(ss * a.inv_d + (double)a.eps);
     const int64_t pitch = fp8_pitch(a.d);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int j = 8 * (lane + LPR * c);
-        double m = 0.;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = fmax(m, fabs(p[c][i]));
-        // scale = max(amax, 2^-64) / 448; a NaN stays
-        m = row16_max(m) * r;
-        m = m <= (double)FP8_AMAX_MIN ? (double)FP8_AMAX_MIN : m;
-        const float s = (float)(m * (1. / FP8_MAX));
-        const double k = r * rcp64((double)s); // y = p k = n / scale
+        if (!EARLY)
+            amax(c);
+        // scale = max(amax, 2^-64) / 448; a NaN of r stays
+        const double y = m[c] * r;
+        const float s = (float)((y <= (double)FP8_AMAX_MIN ? (double)FP8_AMAX_MIN : y) * (1. / FP8_MAX));
+        const double k = r * rcp64((double)s); // p k = n / scale
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             p[c][i] *= k;
+        uint2 q = quant8(p[c]);
+        if (KIND != FULL && j + 8 > a.d) { // zeros past the row, whatever k is
+            const uint2 in = first_bytes(a.d - j);
+            q.x &= in.x, q.y &= in.y;
+        }
         if (j < pitch && t < a.T) {
-            stg8_nt(a.q + t * pitch + j, quant8(p[c]));
+            stg8_nt(a.q + t * pitch + j, q);
             if ((lane & 15) == 0)
                 a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = s;
         }
