@@ -40,20 +40,24 @@ DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 // Scale of a block from the bits of its largest absolute value, and a little
 // over 1 / scale (2^-22 to 2^-20 of it). The scale is amax / 448 rounded once:
 // the product's error is one fused step away (amax - q 448 is exact in the
-// fused multiply-add). An infinite or NaN amax is the scale itself, and makes
-// 1 / scale NaN.
+// fused multiply-add). An infinite or NaN amax is the scale itself: it makes
+// NaN of every code, zero among them. The codes are those of 1 / scale = 0
+// then: NaN where the element is not finite, zeros elsewhere and past the edges.
 struct BlockScale {
-    float s, inv;
+    float s, inv; // as e4m3_quotient takes them
+    float held;   // the scale as it is stored
 };
 DEVI BlockScale fp8_scale(uint32_t amax_bits)
 {
     const uint32_t lo = __float_as_uint(FP8_AMAX_MIN);
     const float amax = __uint_as_float(amax_bits > lo ? amax_bits : lo);
     const float q = amax * (1.f / FP8_MAX);
+    const bool finite = amax_bits < 0x7f800000u;
     BlockScale b;
-    b.s = amax_bits >= 0x7f800000u ? amax : fmaf(fmaf(-q, FP8_MAX, amax), 1.f / FP8_MAX, q);
+    b.s = finite ? fmaf(fmaf(-q, FP8_MAX, amax), 1.f / FP8_MAX, q) : 1.f;
+    b.held = finite ? b.s : amax;
     const float y = __builtin_amdgcn_rcpf(b.s);
-    b.inv = fmaf(fmaf(-b.s, y, 1.f + 0x1p-21f), y, y); // NaN for an infinite scale
+    b.inv = finite ? fmaf(fmaf(-b.s, y, 1.f + 0x1p-21f), y, y) : 0.f;
     return b;
 }
 
@@ -110,13 +114,6 @@ DEVI uint2 quant8(const double *y)
     }
     return make_uint2(f32x4_to_e4m3x4(q[0], q[1], q[2], q[3]),
                       f32x4_to_e4m3x4(q[4], q[5], q[6], q[7]));
-}
-
-// Bytes 0 .. n - 1 of eight, n clamped to 0 .. 8.
-DEVI uint2 first_bytes(int n)
-{
-    const uint64_t m = n <= 0 ? 0 : n >= 8 ? ~(uint64_t)0 : ((uint64_t)1 << 8 * n) - 1;
-    return make_uint2((uint32_t)m, (uint32_t)(m >> 32));
 }
 
 // ---- rows of any alignment

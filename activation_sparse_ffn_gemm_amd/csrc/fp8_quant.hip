@@ -161,9 +161,9 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
         if (tid == 0) {
             // [column block][row block], and the same number for the transpose
             if (ROWS)
-                a.s[(int64_t)tc * fp8_blocks(a.R) + tr] = sb.s;
+                a.s[(int64_t)tc * fp8_blocks(a.R) + tr] = sb.held;
             if (COLS)
-                a.st[(int64_t)tr * fp8_blocks(a.C) + tc] = sb.s;
+                a.st[(int64_t)tr * fp8_blocks(a.C) + tc] = sb.held;
         }
     } else if constexpr (COLS) {
 #pragma unroll
@@ -188,7 +188,7 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
             cs[0][tid] = b.s;
             cs[1][tid] = b.inv;
             if (tc * TS + tid < a.C)
-                a.st[(int64_t)tr * a.C + tc * TS + tid] = b.s;
+                a.st[(int64_t)tr * a.C + tc * TS + tid] = b.held;
         }
     }
     uint2 q[RPT]; // this thread's rows in 8 bits
@@ -207,11 +207,11 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
             }
             b = fp8_scale(m);
             if (cc < RPT && r0 + cc < a.R)
-                a.s[(int64_t)tc * a.R + r0 + cc] = b.s;
+                a.s[(int64_t)tc * a.R + r0 + cc] = b.held;
         }
         auto row = [&](auto I) {
             constexpr int i = decltype(I)::value;
-            const BlockScale br = BLOCK ? b : BlockScale{quad_lane<i>(b.s), quad_lane<i>(b.inv)};
+            const BlockScale br = BLOCK ? b : BlockScale{quad_lane<i>(b.s), quad_lane<i>(b.inv), 0.f};
             float u[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -242,7 +242,7 @@ __global__ __launch_bounds__(NT) void fp8_quant_kernel(QuantArgs a)
             __syncthreads(); // cs
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const BlockScale b = {cs[0][cc * 8 + k], cs[1][cc * 8 + k]};
+                const BlockScale b = {cs[0][cc * 8 + k], cs[1][cc * 8 + k], 0.f};
                 const float u[RPT] = {v[0][k], v[1][k], v[2][k], v[3][k]};
                 turn[turn_word(cc * 8 + k, rr)] = quant4(u, b);
             }

@@ -11,8 +11,8 @@
 // nearest to n / scale: in 32 bits the roundings of h, h r, h r gain, the scale
 // and the quotient put one value in a million on the wrong side of a tie
 // between two e4m3 values, a sixteenth off. Beside a residual's memory traffic
-// the arithmetic is hidden (8192 x 2048: 29.0 us, bf16 out 29.6); of a bf16 x
-// alone, 50 MB, it is the bound (16.0 us).
+// the arithmetic is hidden (8192 x 2048: 28.4 us, bf16 out 29.2); of a bf16 x
+// alone, 50 MB, it is the bound (16.2 us).
 //
 // Backward, per row, with xh = h r and dg = dn gain:
 //   dh = r (dg - xh mean(dg xh)) + dres,   dgain = sum over rows of dn xh.
@@ -245,12 +245,12 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
     // Amax of this lane's block of h gain: before the row's sum, beside whose
     // barrier it costs less, but not in rows that fill their lanes, which have
     // others in flight to hide the barrier and want the registers (2000 x 8192:
-    // 31.5 us, behind the sum 31.9; 8192 x 2048 of bf16 x alone: 17.3 and 16.0).
+    // 31.5 us, behind the sum 31.9; 8192 x 2048 of bf16 x alone: 17.3 and 16.2).
     constexpr bool EARLY = KIND != FULL;
     double m[C];
     // The 64-bit maximum passes over NaN. The upper words, read as floats, are
     // NaN where p is NaN or infinite (no finite p comes near 2^1017), and the
-    // 32-bit maximum keeps it: such a block's amax is infinity, its codes NaN.
+    // 32-bit maximum keeps it: such a block's amax and scale are infinite.
     auto amax = [&](int c) {
         float top = 0.f;
         m[c] = 0.;
@@ -276,17 +276,13 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
         // scale = max(amax, 2^-64) / 448; a NaN of r stays
         const double y = m[c] * r;
         const float s = (float)((y <= (double)FP8_AMAX_MIN ? (double)FP8_AMAX_MIN : y) * (1. / FP8_MAX));
-        const double k = r * rcp64((double)s); // p k = n / scale
+        // p k = n / scale; zeros (and NaN, where p is) in a block of no finite scale
+        const double k = s < __builtin_inff() ? r * rcp64((double)s) : 0.;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             p[c][i] *= k;
-        uint2 q = quant8(p[c]);
-        if (KIND != FULL && j + 8 > a.d) { // zeros past the row, whatever k is
-            const uint2 in = first_bytes(a.d - j);
-            q.x &= in.x, q.y &= in.y;
-        }
         if (j < pitch && t < a.T) {
-            stg8_nt(a.q + t * pitch + j, q);
+            stg8_nt(a.q + t * pitch + j, quant8(p[c]));
             if ((lane & 15) == 0)
                 a.scale[(int64_t)(j / FP8_BLK) * a.T + t] = s;
         }

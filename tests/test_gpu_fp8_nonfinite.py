@@ -66,3 +66,27 @@ def test_norm_codes_past_the_columns(d, value):
     assert v[2, (d - 1) // 128 * 128:].isnan().all() and v[5, :128].isnan().all()
     assert v[[0, 1, 3, 4, 6, 7, 8]].isfinite().all()
     assert not _bytes(n)[:, d:].any()
+
+
+@pytest.mark.parametrize("layout", ["rows", "cols", "both"])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("R,C", [(1, 1), (3, 7), (129, 133), (200, 300), (250, 1001)])
+def test_quant_codes_past_the_edges(R, C, dtype, block_rows, layout):
+    """Not finite in the last block of both directions and in the first."""
+    print("[case] quantised edges", R, C, dtype, block_rows, layout, flush=True)
+    x = _rows(R, C, 1).to(dtype)
+    x[R - 1, C - 1], x[0, 0], x[R // 2, C // 2] = INF, NAN, -INF
+    o, t = tw.fp8_quant(x.to(DEV), block_rows=block_rows, layout=layout)
+    torch.cuda.synchronize()
+    for m, src in ((o, x), (t, x.t())):
+        if m is None:
+            continue
+        rows, cols = src.shape
+        v = m.float().cpu()
+        bad = torch.zeros(src.shape, dtype=torch.bool)
+        for i, j in (~src.isfinite()).nonzero().tolist():
+            i0, j0 = i // block_rows * block_rows, j // 128 * 128
+            bad[i0:i0 + block_rows, j0:j0 + 128] = True
+        assert v[bad].isnan().all() and v[~bad].isfinite().all()
+        assert not _bytes(m)[:, cols:].any()
