@@ -1,6 +1,8 @@
 // out = A B^T of two 8-bit matrices with block scales:
 //   out[m][n] = sum over blocks kb of 128 k of
 //               sa[kb][m] sb[kb][n] sum_{k in kb} qa[m][k] qb[n][k].
+// The product of two scales may be denormal or infinite where a result is
+// neither: they are applied one after the other, or with such cases set apart.
 // The inner sum starts from zero; its result joins the output's float32
 // accumulator scaled. It is taken either
 //   by one 16x16x128 instruction on the 8-bit values (TWELL_SUMS_FP8). That
@@ -45,33 +47,55 @@ DEVI floatx4_t mfma_e4m3(intx8_t a, intx8_t b)
     const floatx4_t zero = {0.f, 0.f, 0.f, 0.f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
+// the first operand times 2^(ea - 127)
+DEVI floatx4_t mfma_e4m3(intx8_t a, intx8_t b, int ea)
+{
+    const floatx4_t zero = {0.f, 0.f, 0.f, 0.f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, ea, 0, 127);
+}
 
 // the same sum over the operands widened to bfloat16, eight k of a lane's 32
-// at a time
-DEVI bf16x8_t widen8(int lo, int hi)
+// at a time, times two, a power of two
+DEVI bf16x8_t widen8(int lo, int hi, float two)
 {
     bf16x2_t p[4];
-    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, false);
-    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, 1.f, true);
-    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, false);
-    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, 1.f, true);
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, two, false);
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)lo, two, true);
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, two, false);
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)hi, two, true);
     return bf16x8_t{p[0][0], p[0][1], p[1][0], p[1][1], p[2][0], p[2][1], p[3][0], p[3][1]};
 }
+
+// Two scales' product may be denormal or infinite where the result is neither.
+// Where rows of B share a scale, its power of two (as far as 2^100) can go to
+// B's operand instead, and the rest, in [1, 2), to A's scale.
+struct Power {
+    int e; // of the float 2^(e - 127)
+    DEVI static Power of(float s) // zeros, denormals, infinities and NaN too
+    {
+        return {min(max((int)(__float_as_uint(s) >> 23 & 255), 27), 227)};
+    }
+    DEVI float two() const { return __uint_as_float((uint32_t)e << 23); }
+    DEVI float rest(float s) const { return ldexpf(s, 127 - e); }
+};
 // A 16-row fragment of one block of k, and the block's sums of two of them.
 template <int SUMS> struct Frag;
 template <> struct Frag<TWELL_SUMS_FP8> {
     intx8_t v;
     DEVI void set(intx8_t x) { v = x; }
+    DEVI void set(intx8_t x, Power) { v = x; }
     DEVI static floatx4_t mul(const Frag &a, const Frag &b) { return mfma_e4m3(a.v, b.v); }
+    DEVI static floatx4_t mul(const Frag &a, const Frag &b, Power p) { return mfma_e4m3(a.v, b.v, p.e); }
 };
 template <> struct Frag<TWELL_SUMS_F32> {
     bf16x8_t v[4];
-    DEVI void set(intx8_t x)
+    DEVI void set(intx8_t x, Power p = {127})
     {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            v[i] = widen8(x[2 * i], x[2 * i + 1]);
+            v[i] = widen8(x[2 * i], x[2 * i + 1], p.two());
     }
+    DEVI static floatx4_t mul(const Frag &a, const Frag &b, Power) { return mul(a, b); }
     DEVI static floatx4_t mul(const Frag &a, const Frag &b)
     {
         floatx4_t c = {0.f, 0.f, 0.f, 0.f};
@@ -283,6 +307,13 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
     // the next products' fragments as they lie in LDS: of B two in turn where
     // products take them as they are
     constexpr int RB = SUMS == TWELL_SUMS_FP8 ? 2 : 1;
+    // A 128-row scale of B and one of A make one factor a token. Where that is no
+    // normal float the results still have to be right: the small tiles split B's
+    // scale (2% of their time at most; one scale after the other costs 6%, the
+    // test below 12%, their steps are short). The large tiles test the factor
+    // once a step, and where it is not normal, seldom, add those tokens' products
+    // apart, one scale after the other (1 to 2%; splitting 3%).
+    constexpr bool SPLIT = BLKB && !C::STAY;
     intx8_t rb[RB], ra[C::MI];
     float sa[C::MI], sb = 1.f;
     floatx4_t sb4[2]; // B's scales of this and the next row of products
@@ -312,10 +343,34 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
             const int nxt = st * C::STAGE;
             Frag<SUMS> fa[C::MI], fb;
             float s[C::MI];
+            const Power two = Power::of(sb);
 #pragma unroll
             for (int j = 0; j < C::MI; ++j) {
                 fa[j].set(ra[j]);
-                s[j] = BLKB ? sa[j] * sb : sa[j];
+                s[j] = BLKB ? sa[j] * (SPLIT ? two.rest(sb) : sb) : sa[j];
+            }
+            if constexpr (BLKB && !SPLIT) {
+                bool odd = false;
+#pragma unroll
+                for (int j = 0; j < C::MI; ++j)
+                    odd |= !__builtin_isnormal(s[j]);
+                if (__builtin_expect(__any(odd), 0)) {
+#pragma unroll
+                    for (int i = 0; i < C::NI; ++i) {
+                        fb.set(frag(Bw + cur + i * 16 * FP8_BLK));
+#pragma unroll
+                        for (int j = 0; j < C::MI; ++j) {
+                            const floatx4_t p = Frag<SUMS>::mul(fb, fa[j]);
+                            const float t = __builtin_isnormal(s[j]) ? 0.f : sa[j];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc[i][j][e] = fmaf(p[e] * t, sb, acc[i][j][e]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < C::MI; ++j)
+                        s[j] = __builtin_isnormal(s[j]) ? s[j] : 0.f;
+                }
             }
             constexpr int NP = C::NI * C::MI;
             constexpr int LAG = SUMS == TWELL_SUMS_FP8 && C::MI > 2 ? 3 : 2;
@@ -324,8 +379,8 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
                 const int i = t / C::MI, j = t % C::MI;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = fmaf(v[t % (LAG + 1)][e], BLKB ? s[j] : s[j] * sb4[i & 1][e],
-                                        acc[i][j][e]);
+                    acc[i][j][e] = BLKB ? fmaf(v[t % (LAG + 1)][e], s[j], acc[i][j][e])
+                                        : fmaf(v[t % (LAG + 1)][e] * s[j], sb4[i & 1][e], acc[i][j][e]);
             };
 #pragma unroll
             for (int t = 0; t < NP; ++t) {
@@ -333,7 +388,10 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
                 if (j == 0) {
                     if (i == C::NI - 1)
                         sync(kb1 - kb - 1);
-                    fb.set(rb[i % RB]);
+                    if constexpr (SPLIT)
+                        fb.set(rb[i % RB], two);
+                    else
+                        fb.set(rb[i % RB]);
                     if (i < C::NI - 1) {
                         rb[(i + 1) % RB] = frag(Bw + cur + (i + 1) * 16 * FP8_BLK);
                     } else {
@@ -342,7 +400,10 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp8_mm_tile_kernel(MmArgs a
                             sb = *(const float *)((const uint8_t *)sbw + nxt);
                     }
                 }
-                v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j]);
+                if constexpr (SPLIT)
+                    v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j], two);
+                else
+                    v[t % (LAG + 1)] = Frag<SUMS>::mul(fb, fa[j]);
                 if (t >= LAG)
                     scale(t - LAG);
                 static_assert(LAG <= C::MI, "the last row's scales are used by then");
@@ -587,7 +648,7 @@ __global__ __launch_bounds__(64 * WV) void fp8_mm_rows_kernel(MmArgs a)
                     const floatx4_t p = Frag<SUMS>::mul(fb[i], fa);
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        acc[i][t][e] = fmaf(p[e], sa * sb[i][e], acc[i][t][e]);
+                        acc[i][t][e] = fmaf(p[e] * sa, sb[i][e], acc[i][t][e]);
                 }
             }
             // the reads are done before the piece is loaded again
