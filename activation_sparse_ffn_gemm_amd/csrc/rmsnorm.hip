@@ -146,6 +146,7 @@ struct FwdArgs {
     float *scale;
     int64_t ldx, ldr, ldh, ldn;
     int T, d, dtx, dtr, dtg, dtn;
+    int t0; // the launch's first row
     float eps;
     double inv_d; // 1 / d
 };
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd_kernel(FwdArgs a
     constexpr int RPB = fwd_threads(LPR) / LPR; // rows per workgroup
     __shared__ float buf[fwd_threads(LPR) / 64];
     const int lane = row_lane<LPR>();
-    const int64_t t = (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
+    const int64_t t = a.t0 + (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
     // a workgroup's rows past T store nothing; they read the last row
     const int d = t < a.T ? a.d : 0;
     const int64_t tl = t < a.T ? t : a.T - 1;
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(fwd_threads(LPR)) void rmsnorm_fwd8_kernel(FwdArgs 
     constexpr int RPB = fwd_threads(LPR) / LPR;
     __shared__ double buf[fwd_threads(LPR) / 64];
     const int lane = row_lane<LPR>();
-    const int64_t t = (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
+    const int64_t t = a.t0 + (int64_t)blockIdx.x * RPB + (LPR >= 64 ? wave_id() * 64 : (int)threadIdx.x) / LPR;
     const int d = t < a.T ? a.d : 0;
     const int64_t tl = t < a.T ? t : a.T - 1;
     double p[C][8]; // h, then h gain
@@ -465,14 +466,19 @@ int bwd_groups(int T, int d)
     return g < most ? (int)g : most;
 }
 
-template <int LPR, int C, RowKind KIND> void fwd_one(const FwdArgs &a, hipStream_t s)
+// A launch has fewer than 2^32 threads: at most 2^31 here, further rows in
+// launches of their own.
+template <int LPR, int C, RowKind KIND> void fwd_one(FwdArgs a, hipStream_t s)
 {
-    constexpr int NT = fwd_threads(LPR), RPB = NT / LPR;
-    const dim3 grid((a.T + RPB - 1) / RPB);
-    if (a.q)
-        rmsnorm_fwd8_kernel<LPR, C, KIND><<<grid, NT, 0, s>>>(a);
-    else
-        rmsnorm_fwd_kernel<LPR, C, KIND><<<grid, NT, 0, s>>>(a);
+    constexpr int NT = fwd_threads(LPR), RPB = NT / LPR, MOST = (int)((1u << 31) / LPR);
+    for (a.t0 = 0; a.t0 < a.T; a.t0 += MOST) {
+        const int rows = a.T - a.t0 < MOST ? a.T - a.t0 : MOST;
+        const dim3 grid((rows + RPB - 1) / RPB);
+        if (a.q)
+            rmsnorm_fwd8_kernel<LPR, C, KIND><<<grid, NT, 0, s>>>(a);
+        else
+            rmsnorm_fwd_kernel<LPR, C, KIND><<<grid, NT, 0, s>>>(a);
+    }
 }
 
 template <RowKind KIND> void fwd_sizes(const FwdArgs &a, hipStream_t s)
