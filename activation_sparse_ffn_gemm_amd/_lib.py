@@ -834,9 +834,9 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=torch.bfloat16, fast_sums: bo
         on["workspace"] = workspace
     args = ma, mb, mo, SUMS_FP8 if fast_sums else SUMS_F32
     end = _timing(timing), _raw_stream(_gpu(on))
-    rc = E_WORKSPACE
-    if workspace is None:  # most sizes need none, and the call says which do
-        rc = load().twell_fp8_matmul(*args, None, 0, *end)
+    # most sizes need no workspace, and the call says which do
+    rc = load().twell_fp8_matmul(*args, _at(workspace),
+                                 0 if workspace is None else workspace.numel(), *end)
     if rc == E_WORKSPACE:
         workspace = _ws(workspace, fp8_matmul_workspace_bytes(M, N, K), out.device)
         rc = load().twell_fp8_matmul(*args, _at(workspace),

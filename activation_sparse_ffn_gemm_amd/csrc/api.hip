@@ -37,8 +37,8 @@ hipError_t launch_rmsnorm_bwd(const twell_mat_t *dn, const twell_mat_t *h, const
 hipError_t launch_fp8_quant(const twell_mat_t *x, const twell_fp8_t *o, const twell_fp8_t *ot,
                             twell_timing_t *timing, hipStream_t s);
 size_t fp8_mm_workspace(int M, int N, int K);
-hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out,
-                         int sums, void *ws, twell_timing_t *timing, hipStream_t s);
+int launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out, int sums,
+                  void *ws, size_t ws_bytes, twell_timing_t *timing, hipStream_t s);
 
 namespace {
 
@@ -484,12 +484,9 @@ int twell_fp8_matmul(const twell_fp8_t *a, const twell_fp8_t *b, const twell_mat
         return rc;
     if (!a16(workspace))
         return TWELL_E_ALIGN;
-    const size_t need = twell_fp8_matmul_workspace_bytes(a->rows, b->rows, a->cols);
-    if (workspace_bytes < need || (need && !workspace))
-        return TWELL_E_WORKSPACE;
     if (a->rows == 0 || b->rows == 0)
         return TWELL_OK;
-    return hip_rc(launch_fp8_mm(a, b, out, sums, workspace, timing, (hipStream_t)stream));
+    return launch_fp8_mm(a, b, out, sums, workspace, workspace_bytes, timing, (hipStream_t)stream);
 }
 
 } // extern "C"

@@ -739,6 +739,8 @@ Plan plan(int M, int N, int nkb, int sums, int rb)
                 {ROWS_2_2_8, 2, 2, 8, 1}};
     for (const auto &r : rows) {
         const double wg = up(M, 16 * r.tb) * up(N, 16 * r.nb);
+        if (wg * 64 * r.wv > 4294967295.) // threads of a launch
+            continue;
         const double lat = up(wg, 256 * r.occ) * (up(nkb, r.wv) * 0.15 * (r.tb + r.nb) + 0.8);
         const double mem = wg * 16 * (r.tb + r.nb) * nkb * FP8_BLK / 12e6;
         offer(r.k, 1, 2.0 + (lat > mem ? lat : mem));
@@ -799,8 +801,8 @@ size_t fp8_mm_workspace(int M, int N, int K)
     return parts > 1 ? (size_t)parts * M * N * 4 : 0;
 }
 
-hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out,
-                         int sums, void *ws, twell_timing_t *timing, hipStream_t s)
+int launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out, int sums,
+                  void *ws, size_t ws_bytes, twell_timing_t *timing, hipStream_t s)
 {
     MmArgs a = {};
     a.qa = A->q, a.sa = A->scale, a.qb = B->q, a.sb = B->scale;
@@ -809,9 +811,11 @@ hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell
     a.M = A->rows, a.N = B->rows, a.nkb = fp8_blocks(A->cols);
     a.ra = A->block_rows, a.rb = B->block_rows;
     a.nsa = (a.M + a.ra - 1) / a.ra, a.nsb = (a.N + a.rb - 1) / a.rb;
-    Timer tm(timing, s);
     const Plan p = plan(a.M, a.N, a.nkb, sums, a.rb);
+    if (p.parts > 1 && (!ws || ws_bytes < (size_t)p.parts * a.M * a.N * 4))
+        return TWELL_E_WORKSPACE;
     a.parts = p.parts, a.per = p.per, a.part = (float *)ws;
+    Timer tm(timing, s);
     const bool blkb = a.rb == FP8_BLK;
     if (sums == TWELL_SUMS_FP8)
         blkb ? launch_sums<TWELL_SUMS_FP8, true>(a, p.k, s)
@@ -828,5 +832,5 @@ hipError_t launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell
         fp8_mm_join_kernel<<<(uint32_t)((q + 255) / 256), 256, 0, s>>>(a);
         tm.mark("fp8_mm_join");
     }
-    return hipGetLastError();
+    return hipGetLastError() == hipSuccess ? TWELL_OK : TWELL_E_HIP;
 }

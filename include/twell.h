@@ -413,8 +413,10 @@ int twell_fp8_quant(const twell_mat_t *x, const twell_fp8_t *out, const twell_fp
  * on the matrices twell_fp8_quant makes. a.cols = b.cols <= TWELL_MAX_K.
  * Scales may be any float32 numbers, a's up to 2^102 in size (a block's sum
  * times a's scale has to be finite: values of a up to 2^110).
- *   workspace: at least twell_fp8_matmul_workspace_bytes(...) bytes, 0 (and
- *   workspace may be NULL) where the contraction is not split.
+ *   workspace: twell_fp8_matmul_workspace_bytes(...) bytes are enough, 0 (and
+ *   workspace may be NULL) where the contraction is not split. That is the most
+ *   that any sums and block_rows take at these sizes; a call that itself takes
+ *   less asks for no more.
  * Errors: NULL / SHAPE / DTYPE / ALIGN / WORKSPACE / HIP.
  */
 enum { TWELL_SUMS_F32 = 0, TWELL_SUMS_FP8 = 1 };
