@@ -122,8 +122,26 @@ template <int N> DEVI float tree_sum(const float *p)
         return tree_sum<N / 2>(p) + tree_sum<N / 2>(p + N / 2);
 }
 
-// Two float sums over a row's lanes with one barrier.
-template <int LPR> DEVI void row_sum2(float &u, float &v, float *bu, float *bv)
+// The same of W <= 16 values in LDS, a lane of each W taking one of them.
+template <int W> DEVI float tree_sum_lanes(const float *p)
+{
+    float v = p[threadIdx.x & (W - 1)];
+    if constexpr (W > 1)
+        v += dpp_mov<0xB1>(v);
+    if constexpr (W > 2)
+        v += dpp_mov<0x4E>(v);
+    if constexpr (W > 4)
+        v += dpp_mov<0x141>(v);
+    if constexpr (W > 8)
+        v += dpp_mov<0x140>(v);
+    return v;
+}
+
+// Two float sums over a row's lanes with one barrier. FEW: without the 32
+// registers that a row's sixteen pairs take in every lane, which rows of two
+// chunks a lane do not have (in scratch 2000 x 16384 took 105 us, so 102; 2000 x
+// 16383 124 and 112; rows of one chunk lose 1%).
+template <int LPR, bool FEW> DEVI void row_sum2(float &u, float &v, float *bu, float *bv)
 {
     if constexpr (LPR <= 64) {
         u = row_sum<LPR>(u, bu), v = row_sum<LPR>(v, bv);
@@ -135,7 +153,10 @@ template <int LPR> DEVI void row_sum2(float &u, float &v, float *bu, float *bv)
             bu[w] = u, bv[w] = v;
         __syncthreads();
         const int w0 = w / W * W;
-        u = tree_sum<W>(bu + w0), v = tree_sum<W>(bv + w0);
+        if constexpr (FEW)
+            u = tree_sum_lanes<W>(bu + w0), v = tree_sum_lanes<W>(bv + w0);
+        else
+            u = tree_sum<W>(bu + w0), v = tree_sum<W>(bv + w0);
     }
 }
 
@@ -346,7 +367,7 @@ __global__ __launch_bounds__(bwd_threads(LPR)) void rmsnorm_bwd_kernel(BwdArgs a
                 dot = fmaf(g.v[c][i] * dn.v[c][i], h.v[c][i], dot);
             }
         // two buffers in turn: a wave may still read the last row's sums
-        row_sum2<LPR>(ss, dot, buf[it & 1][0], buf[it & 1][1]);
+        row_sum2<LPR, (C > 1)>(ss, dot, buf[it & 1][0], buf[it & 1][1]);
         const float r = 1.f / sqrtf(ss / (float)a.d + a.eps);
         const float m = dot * r / (float)a.d; // mean(dg xh)
 #pragma unroll
