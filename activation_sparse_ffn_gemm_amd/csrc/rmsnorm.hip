@@ -467,24 +467,32 @@ RowKind row_kind(int d)
     return d & 7 ? RAGGED : d == 8 * l && l < 1024 ? FULL : EIGHTS;
 }
 
-// Workgroups (and partial rows of dgain) of the backward. One for rows that
-// take at most four turns: it writes dgain itself. Many rows: up to sixteen
-// waves for each CU (at 8192 x 2048: 49 us; half of them 52, twice 53). Between
-// these, where the partial rows weigh against the rows themselves, one
-// workgroup a CU, evenly loaded (1000 x 4096: 17.5 us, with 512 of them 20.0;
-// 4096 x 1024 15.4 and 15.1), unless that leaves CUs out.
+// Workgroups (and partial rows of dgain) of the backward, of the g turns that
+// all the rows make.
+// Up to two turns: one workgroup, which writes dgain itself (two turns of 1024
+// columns 4.4 us, as two workgroups and a second launch 5.4; three 5.5 and 5.4,
+// four of 64 columns 8.5 and 5.7).
+// Workgroups of sixteen waves: one a CU. Of eight: two a CU, unless their
+// partial rows weigh more than they gain, one for each 3/8 columns' turns (one
+// and two a CU, us: 4096 columns, 1000 turns 17.4 and 19.9, 8192 turns 96.7 and
+// 93.0; 2304 columns, 600 turns 12.2 and 12.7, 8192 turns 80.7 and 59.5; 1500
+// columns, 513 turns 14.6 and 12.7, 1200 turns 20.6 and 18.2).
+// All have the same number of turns or one less (4096 columns, 300 turns: 11.5
+// with 150, 13.7 with 300; 8192 columns, 513 turns: 20.8 with 171, 22.9 with 256).
+// With two a CU and more than two turns they are 512 even so: fewer no longer
+// fill the memory's queues (2048 columns, 2049 turns: 28.1, with 410 30.5).
 int bwd_groups(int T, int d)
 {
-    const int lpr = row_lanes(d), rpb = bwd_threads(lpr) / lpr;
+    constexpr int CUS = 256;
+    const int lpr = row_lanes(d), nt = bwd_threads(lpr), rpb = nt / lpr;
     const int64_t g = ((int64_t)T + rpb - 1) / rpb;
-    const int most = 256 * 1024 / bwd_threads(lpr);
-    if (g <= 4)
+    if (g <= 2)
         return g > 0;
-    if (g >= 448 && g <= 1024) {
-        const int64_t turns = (g + 255) / 256;
-        return (int)((g + turns - 1) / turns);
-    }
-    return g < most ? (int)g : most;
+    const int most = nt == 512 && 8 * g > 3 * (int64_t)d ? 2 * CUS : CUS;
+    const int64_t turns = (g + most - 1) / most;
+    if (most > CUS && turns > 2)
+        return most;
+    return (int)((g + turns - 1) / turns);
 }
 
 // A launch has fewer than 2^32 threads: at most 2^31 here, further rows in
