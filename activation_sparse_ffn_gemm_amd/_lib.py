@@ -599,10 +599,6 @@ class Fp8:
     def rows(self):
         return self.q.shape[0]
 
-    def c(self) -> Fp8C:
-        return Fp8C(self.q.shape[0], self.cols, self.block_rows, self.q.data_ptr(),
-                    self.scale.data_ptr())
-
     def float(self) -> torch.Tensor:
         """The float32 values the matrix stands for."""
         s = self.scale.t().repeat_interleave(self.block_rows, 0)[:self.rows]

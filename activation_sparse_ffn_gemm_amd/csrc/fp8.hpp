@@ -35,7 +35,6 @@ DEVI uint32_t row16_umax(uint32_t v)
     step((uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false));
     return v;
 }
-DEVI uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Scale of a block from the bits of its largest absolute value, and a little
 // over 1 / scale (2^-22 to 2^-20 of it). The scale is amax / 448 rounded once:

@@ -593,11 +593,12 @@ __global__ __launch_bounds__(64 * WV) void fp8_mm_rows_kernel(MmArgs a)
                        (int)v.x, (int)v.y, (int)v.z, (int)v.w};
     };
     // The i-th block of this wave among the SCB from k0, nkb when there is none.
-    // Workgroups begin an eighth of the way apart (by their n, so that a token's
-    // sums do not depend on the tokens beside it): rows whose pitch is a large
+    // Workgroups begin an eighth of the way apart: rows whose pitch is a large
     // power of two would otherwise be read from the same few memory channels by
     // all workgroups at once (one token by 8192 over 8192: 16.8 -> 13.8 us,
-    // 16 by 4096 over 4096: 6.8 -> 6.3).
+    // 16 by 4096 over 4096: 6.8 -> 6.3). It goes by their n, so that within one
+    // kernel a token's sums do not depend on the tokens beside it; how many these
+    // are chooses the kernel, and so the order of its additions.
     const uint32_t turn = (uint32_t)n0 / (128 * NB) & 7;
     auto steps = [&](int k0) {
         return (int)((uint32_t)(min(SCB, a.nkb - k0) - w + WV - 1) / WV);
@@ -713,12 +714,16 @@ template <class C, int SUMS, bool BLKB> void launch_tile(const MmArgs &a, hipStr
 
 // Which kernel takes a product, and in how many parts of the contraction: the
 // least of the times that these measured figures give (us; they order the
-// kernels, no more). A tile kernel runs a tile per CU at a time, a step of 128 k
-// at `step` and `tile` for its beginning and end; full sums cost what widening
-// and the bfloat16 instruction do. Parts add a second launch and the partial
-// sums' way through memory. A rows kernel's wave takes 0.15 for each fragment
-// of a block of k (its loads' issue), unless all the workgroups' reads together
-// pass what the L2s serve (12 MB a us).
+// kernels, no more). A tile kernel is counted as a tile per CU at a time, a step
+// of 128 k at `step` and `tile` for its beginning and end; full sums cost what
+// widening and the bfloat16 instruction do. (Two tiles of 64 x 128 fit a CU and
+// share it: a second round of them is counted 10 to 20% dearer than it is, and
+// rounds that leave CUs idle run faster than counted, at higher clocks. Of 27
+// sizes from 130 to 4096 tokens, each in three modes, the choice was the fastest
+// or within 5% in 73 of 81, and at worst 19% behind: 2000 x 4100 over 700.) Parts
+// add a second launch and the partial sums' way through memory. A rows kernel's
+// wave takes 0.15 for each fragment of a block of k (its loads' issue), unless all
+// the workgroups' reads together pass what the L2s serve (12 MB a us).
 enum Kernel { ROWS_1_1, ROWS_1_2, ROWS_2_2, ROWS_2_2_8, TILE_64, TILE_128, TILE_192, TILE_256 };
 struct Plan {
     Kernel k;
