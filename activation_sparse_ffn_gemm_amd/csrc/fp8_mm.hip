@@ -131,9 +131,10 @@ template <> struct Frag<TWELL_SUMS_F32> {
 // Of the two large tiles a CU holds one workgroup, so there is nobody to work
 // while it begins and ends. There the workgroups stay and take further tiles:
 // the next tile's first loads go out before this one's results are stored, and
-// the stores drain beside its first steps (8192 x 5632 over 2048: 93 -> 88 us).
-// Stores write whole 128-byte lines, through LDS: float32 results stored from
-// the accumulators, 64 bytes of a row at a time, took 173 us there, so 165.
+// the stores drain beside its first steps (8192 x 5632 over 2048: 93 -> 88 us; 90
+// with the scales' test). Stores write whole 128-byte lines, through LDS: float32
+// results stored from the accumulators, 64 bytes of a row at a time, took 173 us
+// there, so 165 (168 with the test).
 //
 // What bounds a step: fast sums, the matrix unit with the scales' steps beside
 // it (a loop of registers alone runs at 3463 TF, 1.24 us a step of 256 x 256)
@@ -764,7 +765,8 @@ Plan plan(int M, int N, int nkb, int sums, int rb)
     for (const auto &c : tiles) {
         // full sums hold their operands widened: with a scale for each row of B
         // as well, 256 x 256 does not fit the registers (4.0 a step, 192 x 256
-        // 2.4)
+        // 2.4); with 128-row scales it keeps five lane constants of a tile, none
+        // of a step, in scratch
         if (c.k == TILE_256 && full && !blkb)
             continue;
         for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
