@@ -101,3 +101,28 @@ def test_scales_that_are_not_numbers(M, N, K):
             _within(got[fin][:, :n0], want, rel * mag, f"{M} {N} {K} {rb} {fast}")
             assert (got[2, :n0] == float("inf")).all() and got[3].isnan().all()
             assert not got[:, n0:].isfinite().any()
+
+
+@pytest.mark.parametrize("M,N,K", [(4173, 4226, 300), (2500, 6151, 641), (24577, 513, 384),
+                                   (1029, 2811, 640), (50, 2304, 1000)])
+@pytest.mark.parametrize("sign", [False, True], ids=["positive", "signed"])
+def test_scales_of_all_sizes_at_once(M, N, K, sign):
+    """Every block and every row its own size, from the smallest scale to 2^40:
+    tokens whose factor is a normal float beside tokens where it is not, in
+    workgroups that go on to further tiles, whole and cut."""
+    for rb in (128, 1):
+        a, b = _matrix(M, K, 1, 0, 1), _matrix(N, K, rb, 0, 2)
+        g = torch.Generator(DEV).manual_seed(M)
+        for m in (a, b):
+            m.scale *= 2.0 ** torch.randint(-73, 41, m.scale.shape, generator=g, device=DEV)
+            if sign:
+                m.scale *= torch.randint(0, 2, m.scale.shape, generator=g, device=DEV) * 2.0 - 1
+        da, db = _value(a), _value(b)
+        want, mag = da @ db.t(), da.abs() @ db.abs().t()
+        nkb = a.scale.shape[0]
+        for fast in (False, True):
+            print("[case] mixed scales", M, N, K, rb, fast, flush=True)
+            got = tw.fp8_matmul(a, b, out_dtype=F32, fast_sums=fast)
+            torch.cuda.synchronize()
+            rel = (128 + 2 + nkb + 64) * ref.U32 + ref.U32 + (ref.FAST if fast else 0)
+            _within(got, want, rel * mag + (nkb + 66) * 2.0 ** -150, f"{M} {N} {K} {rb} {fast}")
