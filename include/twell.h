@@ -337,7 +337,8 @@ typedef struct {
  *   scale  [ceil(cols / 128)][ceil(rows / block_rows)] float32
  * The library writes scale = max(amax, 2^-64) / 448 over the block, rounded to
  * float32, and for q the e4m3 value nearest to x / scale, ties to even. A NaN
- * or infinity in a block makes the values that it stands for NaN.
+ * or infinity in a block makes the values that it stands for NaN (its scale is
+ * infinite or NaN, its codes zeros and NaN).
  */
 typedef struct {
     int32_t rows, cols, block_rows;
