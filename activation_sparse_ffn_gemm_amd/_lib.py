@@ -27,10 +27,15 @@ EXPORTS = ("twell_gate_pack", "twell_gate_workspace_bytes", "twell_ffn_fwd", "tw
            "hybrid_fwd_workspace_bytes", "hybrid_ffn_bwd", "hybrid_bwd_workspace_bytes",
            "twell_status_str", "twell_decode_fwd_noalloc", "twell_rmsnorm_fwd",
            "twell_rmsnorm_bwd", "twell_rmsnorm_bwd_workspace_bytes", "twell_fp8_quant",
-           "twell_fp8_matmul", "twell_fp8_matmul_workspace_bytes")
+           "twell_fp8_matmul", "twell_fp8_matmul_workspace_bytes", "twell_fp4_quant",
+           "twell_fp4_dequant", "twell_fp4_matmul", "twell_fp4_matmul_workspace_bytes",
+           "twell_fp4_matmul_dx", "twell_fp4_matmul_dx_workspace_bytes", "twell_fp4_decode_fwd",
+           "twell_fp4_decode_workspace_bytes")
 STATIC_SCRATCH_BYTES = 12 << 20  # twell_decode_fwd_noalloc's scratch per GPU
 DECODE_T = 64  # most tokens twell_decode_fwd takes (few-token kernels up to here)
 FP8_BLOCK = 128  # columns that share a scale of an 8-bit matrix
+FP4_BLOCK = 128  # columns that a row of a 4-bit matrix is padded to
+FP4_GROUPS = (32, 64, 128)  # columns that may share a scale of a 4-bit matrix
 NORM_COLS = 16384  # widest row the norm takes
 SUMS_F32, SUMS_FP8 = 0, 1  # how twell_fp8_matmul adds products
 E_WORKSPACE = -5  # status: the call needs (more) workspace
@@ -99,6 +104,10 @@ class Fp8C(ctypes.Structure):
                 ("scale", c_p)]
 
 
+class Fp4C(ctypes.Structure):
+    _fields_ = [("rows", c_i32), ("cols", c_i32), ("group", c_i32), ("q", c_p), ("scale", c_p)]
+
+
 _lib = None
 
 
@@ -148,11 +157,22 @@ def load() -> ctypes.CDLL:
     L.twell_fp8_matmul.argtypes = [Q, Q, M, I, P, S, P, P]
     L.twell_fp8_matmul_workspace_bytes.argtypes = [I, I, I]
     L.twell_fp8_matmul_workspace_bytes.restype = S
+    L.twell_fp4_quant.argtypes = [M, Q, P, P]
+    L.twell_fp4_dequant.argtypes = [Q, M, P, P]
+    for f in ("twell_fp4_matmul", "twell_fp4_matmul_dx"):
+        getattr(L, f).argtypes = [M, Q, M, P, S, P, P]
+        getattr(L, f).restype = ctypes.c_int
+        getattr(L, f + "_workspace_bytes").argtypes = [ctypes.c_int, I, I, I]
+        getattr(L, f + "_workspace_bytes").restype = S
+    L.twell_fp4_decode_fwd.argtypes = [M, Q, Q, Q, P, P, S, P, P]
+    L.twell_fp4_decode_workspace_bytes.argtypes = [ctypes.c_int, I, I, I]
+    L.twell_fp4_decode_workspace_bytes.restype = S
     L.twell_status_str.argtypes = [ctypes.c_int]
     L.twell_status_str.restype = ctypes.c_char_p
     for f in ("twell_gate_pack", "twell_ffn_fwd", "twell_decode_fwd", "twell_to_hybrid",
               "hybrid_ffn_fwd", "hybrid_ffn_bwd", "twell_decode_fwd_noalloc", "twell_rmsnorm_fwd",
-              "twell_rmsnorm_bwd", "twell_fp8_quant", "twell_fp8_matmul"):
+              "twell_rmsnorm_bwd", "twell_fp8_quant", "twell_fp8_matmul", "twell_fp4_quant",
+              "twell_fp4_dequant", "twell_fp4_decode_fwd"):
         getattr(L, f).restype = ctypes.c_int
     _lib = L
     return L
@@ -840,3 +860,184 @@ def fp8_matmul(a: Fp8, b: Fp8, out=None, out_dtype=torch.bfloat16, fast_sums: bo
                                      0 if workspace is None else workspace.numel(), *end)
     _check(rc, "twell_fp8_matmul")
     return out
+
+
+# ---- weights in 4 bits
+@dataclass
+class Fp4:
+    """A matrix [rows][cols] in 4 bits: element (r, c) stands for
+    value(code) * scale[c // group][r], the code of column 2b in the low half
+    of byte b of q's row."""
+
+    q: torch.Tensor      # [rows][cols rounded up to 128, / 2] uint8, zeros past cols
+    scale: torch.Tensor  # [cols rounded up to 128, / group][rows] bfloat16
+    cols: int
+    group: int = 128
+
+    @property
+    def rows(self):
+        return self.q.shape[0]
+
+    def float(self) -> torch.Tensor:
+        """The float32 values the matrix stands for (on any device)."""
+        v = torch.tensor(_E2M1 + tuple(-v for v in _E2M1), device=self.q.device)
+        c = torch.stack((self.q & 15, self.q >> 4), 2).flatten(1)
+        s = self.scale.float().t().repeat_interleave(self.group, 1)
+        return (v[c.int()] * s)[:, :self.cols]
+
+
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+_U8, _BF = torch.uint8, torch.bfloat16
+
+
+def empty_fp4(rows, cols, group, device) -> Fp4:
+    nb = -(-cols // FP4_BLOCK)
+    return Fp4(torch.empty(rows, nb * (FP4_BLOCK // 2), dtype=_U8, device=device),
+               torch.empty(nb * (FP4_BLOCK // group), rows, dtype=_BF, device=device), cols, group)
+
+
+def _check_fp4(m, name, rows=None, cols=None):
+    """(structure, rows) of a well-formed Fp4 [rows][cols]."""
+    if not isinstance(m, Fp4):
+        raise TwellError(f"{name}: expected an Fp4")
+    q, s, g, mc = m.q, m.scale, m.group, m.cols
+    if g not in FP4_GROUPS:
+        raise TwellError(f"{name}.group: {g}, expected one of {FP4_GROUPS}")
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise TwellError(f"{name}.q: expected a [rows][cols up to 128, / 2] tensor")
+    r, pitch = q.shape
+    nb = -(-mc // FP4_BLOCK)
+    sshape = (nb * (FP4_BLOCK // g), r)
+    if not (isinstance(s, torch.Tensor) and pitch == nb * (FP4_BLOCK // 2) and s.shape == sshape
+            and q.dtype == _U8 and s.dtype == _BF and q.is_contiguous() and s.is_contiguous()
+            and (cols is None or (mc == cols and r == rows))):
+        if cols is not None and mc != cols:
+            raise TwellError(f"{name}: {mc} columns, expected {cols}")
+        if rows is None:
+            rows = r
+        _req(q, f"{name}.q", (rows, nb * (FP4_BLOCK // 2)), _U8)
+        _req(s, f"{name}.scale", sshape, _BF)
+    return _pack_fp8(r, mc, g, q.data_ptr(), s.data_ptr()), r  # Fp4C: the same fields
+
+
+assert ctypes.sizeof(Fp4C) == ctypes.sizeof(Fp8C)
+
+
+def fp4_quant(w, group: int = 128, out: Fp4 | None = None,
+              timing: KernelTimer | None = None) -> Fp4:
+    """w in 4 bits, one scale for each `group` (32, 64 or 128) columns of a row."""
+    mw, R, C = _mat(w, "w")
+    if group not in FP4_GROUPS:
+        raise TwellError(f"group: {group}, expected one of {FP4_GROUPS}")
+    if out is None:
+        out = empty_fp4(R, C, group, w.device)
+    mo = _check_fp4(out, "out", R, C)[0]
+    if out.group != group:
+        raise TwellError(f"out: group {out.group}, expected {group}")
+    dev = _gpu({"w": w, "out.q": out.q, "out.scale": out.scale})
+    _check(load().twell_fp4_quant(mw, mo, _timing(timing), _raw_stream(dev)), "twell_fp4_quant")
+    return out
+
+
+def fp4_dequant(w: Fp4, out=None, out_dtype=torch.bfloat16, timing: KernelTimer | None = None):
+    """The matrix that w stands for, in bfloat16 (exact for fp4_quant's scales)
+    or float32."""
+    mw, R = _check_fp4(w, "w")
+    on = {"w.q": w.q, "w.scale": w.scale}
+    if out is None:
+        out, mo = _new_mat(R, w.cols, out_dtype, w.q.device)
+    else:
+        mo = _mat(out, "out", R, w.cols, out_dtype)[0]
+        on["out"] = out
+    _check(load().twell_fp4_dequant(mw, mo, _timing(timing), _raw_stream(_gpu(on))),
+           "twell_fp4_dequant")
+    return out
+
+
+def fp4_matmul_workspace_bytes(dtype, T, N, K) -> int:
+    return int(load().twell_fp4_matmul_workspace_bytes(dtype, T, N, K))
+
+
+def fp4_matmul_dx_workspace_bytes(dtype, T, N, K) -> int:
+    return int(load().twell_fp4_matmul_dx_workspace_bytes(dtype, T, N, K))
+
+
+def _fp4_mm(name, x, xname, w, out, out_dtype, workspace, timing):
+    mw, N = _check_fp4(w, "w")
+    mx, T, C = _mat(x, xname)
+    fwd = name == "twell_fp4_matmul"
+    take, give = (w.cols, N) if fwd else (N, w.cols)
+    if C != take:
+        raise TwellError(f"{xname}: {C} columns, w has {take} {'columns' if fwd else 'rows'}")
+    on = {xname: x, "w.q": w.q, "w.scale": w.scale}
+    if out is None:
+        out, mo = _new_mat(T, give, out_dtype, x.device)
+    else:
+        mo = _mat(out, "out", T, give, out_dtype)[0]
+        on["out"] = out
+    if workspace is not None:
+        _ws_form(workspace)
+        on["workspace"] = workspace
+    L = load()
+    call = getattr(L, name)
+    end = _timing(timing), _raw_stream(_gpu(on))
+    # few tokens need no workspace, and the call says which do
+    rc = call(mx, mw, mo, _at(workspace), 0 if workspace is None else workspace.numel(), *end)
+    if rc == E_WORKSPACE:
+        need = getattr(L, name + "_workspace_bytes")(_dt(x), T, N, w.cols)
+        workspace = _ws(workspace, need, x.device)
+        rc = call(mx, mw, mo, workspace.data_ptr(), workspace.numel(), *end)
+    _check(rc, name)
+    return out
+
+
+def fp4_matmul(x, w: Fp4, out=None, out_dtype=torch.bfloat16, workspace=None,
+               timing: KernelTimer | None = None):
+    """out [T][w.rows] = x w^T, x [T][w.cols] and out each float32 or bfloat16.
+    Products are exact, sums float32; any number of tokens, one upwards."""
+    return _fp4_mm("twell_fp4_matmul", x, "x", w, out, out_dtype, workspace, timing)
+
+
+def fp4_matmul_dx(dy, w: Fp4, out=None, out_dtype=torch.bfloat16, workspace=None,
+                  timing: KernelTimer | None = None):
+    """fp4_matmul's gradient for x: out [T][w.cols] = dy w, dy [T][w.rows]."""
+    return _fp4_mm("twell_fp4_matmul_dx", dy, "dy", w, out, out_dtype, workspace, timing)
+
+
+def fp4_decode_workspace_bytes(dtype, T, d_model, d_ff) -> int:
+    return int(load().twell_fp4_decode_workspace_bytes(dtype, T, d_model, d_ff))
+
+
+def fp4_decode_fwd(x, wg_t: Fp4, wu_t: Fp4, wd: Fp4, y=None, workspace=None,
+                   timing: KernelTimer | None = None):
+    """The sparse layer for T <= DECODE_T tokens from 4-bit weights [d_ff][d_model]
+    of one group: y [T][d_model] float32, (relu(x Wg) * (x Wu)) Wd with g and u
+    in float32."""
+    mx, T, dm = _mat(x, "x")
+    if T > DECODE_T:
+        raise TwellError(f"fp4_decode_fwd takes at most {DECODE_T} tokens, got {T}")
+    mg, f = _check_fp4(wg_t, "wg_t")
+    on = {"x": x, "wg_t.q": wg_t.q, "wg_t.scale": wg_t.scale}
+    ms = []
+    for name, m in (("wu_t", wu_t), ("wd", wd)):
+        ms.append(_check_fp4(m, name, f, dm)[0])
+        if m.group != wg_t.group:
+            raise TwellError(f"{name}: group {m.group}, wg_t has {wg_t.group}")
+        on[name + ".q"], on[name + ".scale"] = m.q, m.scale
+    if wg_t.cols != dm:
+        raise TwellError(f"wg_t: {wg_t.cols} columns, expected {dm}")
+    if y is None:
+        y = torch.empty(T, dm, dtype=torch.float32, device=x.device)
+    else:
+        _req(y, "y", (T, dm), torch.float32)
+        on["y"] = y
+    if workspace is not None:
+        _ws_form(workspace)
+        on["workspace"] = workspace
+    dev = _gpu(on)
+    workspace = _ws(workspace, fp4_decode_workspace_bytes(_dt(x), T, dm, f), x.device)
+    _check(load().twell_fp4_decode_fwd(mx, mg, *ms, y.data_ptr(), _at(workspace),
+                                       0 if workspace is None else workspace.numel(),
+                                       _timing(timing), _raw_stream(dev)),
+           "twell_fp4_decode_fwd")
+    return y

@@ -40,6 +40,18 @@ size_t fp8_mm_workspace(int M, int N, int K);
 int launch_fp8_mm(const twell_fp8_t *A, const twell_fp8_t *B, const twell_mat_t *out, int sums,
                   void *ws, size_t ws_bytes, twell_timing_t *timing, hipStream_t s);
 
+hipError_t launch_fp4_quant(const twell_mat_t *x, const twell_fp4_t *o, twell_timing_t *timing,
+                            hipStream_t s);
+hipError_t launch_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing_t *timing,
+                              hipStream_t s);
+size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx);
+int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w, const twell_mat_t *out, bool dx,
+                  void *ws, size_t ws_bytes, twell_timing_t *timing, hipStream_t s);
+size_t fp4_layer_workspace(const twell_mat_t *x, int d_ff);
+hipError_t launch_fp4_layer(const twell_mat_t *x, const twell_fp4_t *wg, const twell_fp4_t *wu,
+                            const twell_fp4_t *wd, float *y, void *ws, twell_timing_t *timing,
+                            hipStream_t s);
+
 namespace {
 
 bool a16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
@@ -135,6 +147,16 @@ int check_fp8(const twell_fp8_t *m)
     return a16(m->q) && aligned(m->scale, 4) ? TWELL_OK : TWELL_E_ALIGN;
 }
 
+int check_fp4(const twell_fp4_t *m)
+{
+    if (m->rows < 0 || m->rows > TWELL_MAX_ROWS || m->cols < 0 || m->cols > TWELL_MAX_ROWS ||
+        (m->group != 32 && m->group != 64 && m->group != 128))
+        return TWELL_E_SHAPE;
+    if (m->rows > 0 && m->cols > 0 && (!m->q || !m->scale))
+        return TWELL_E_NULL;
+    return a16(m->q) && aligned(m->scale, 2) ? TWELL_OK : TWELL_E_ALIGN;
+}
+
 bool eps_ok(float eps) { return eps >= 0.f && eps <= 3.4e38f; }
 
 // rows and columns of the norm
@@ -147,6 +169,39 @@ bool norm_sizes_ok(int32_t rows, int32_t cols)
 bool tiles_ok(int64_t rows, int64_t cols, int64_t tr, int64_t tc)
 {
     return ((rows + tr - 1) / tr) * ((cols + tc - 1) / tc) <= INT32_MAX;
+}
+
+// sizes of a 4-bit product (dx: of its gradient): T tokens, w [N][K]
+bool fp4_sizes_ok(int32_t T, int32_t N, int32_t K, bool dx)
+{
+    return T >= 0 && T <= TWELL_MAX_ROWS && N >= 0 && N <= TWELL_MAX_ROWS && K >= 0 &&
+           K <= TWELL_MAX_ROWS && (dx ? N : K) <= TWELL_MAX_K && tiles_ok(T, dx ? K : N, 16, 16);
+}
+
+// a matrix whose rows take the most workspace that any strides make them take
+twell_mat_t worst_mat(twell_dtype dt, int32_t rows, int32_t cols)
+{
+    return {rows, cols, cols, dt, (void *)(uintptr_t)2};
+}
+
+int fp4_mm(const twell_mat_t *x, const twell_fp4_t *w, const twell_mat_t *out, bool dx,
+           void *workspace, size_t workspace_bytes, twell_timing_t *timing, void *stream)
+{
+    if (!x || !w || !out)
+        return TWELL_E_NULL;
+    if (int rc = check_fp4(w))
+        return rc;
+    if (!fp4_sizes_ok(x->rows, w->rows, w->cols, dx))
+        return TWELL_E_SHAPE;
+    if (int rc = check_mat(x, x->rows, dx ? w->rows : w->cols))
+        return rc;
+    if (int rc = check_mat(out, x->rows, dx ? w->cols : w->rows))
+        return rc;
+    if (!a16(workspace))
+        return TWELL_E_ALIGN;
+    if (out->rows == 0 || out->cols == 0)
+        return TWELL_OK;
+    return launch_fp4_mm(x, w, out, dx, workspace, workspace_bytes, timing, (hipStream_t)stream);
 }
 
 } // namespace
@@ -487,6 +542,104 @@ int twell_fp8_matmul(const twell_fp8_t *a, const twell_fp8_t *b, const twell_mat
     if (a->rows == 0 || b->rows == 0)
         return TWELL_OK;
     return launch_fp8_mm(a, b, out, sums, workspace, workspace_bytes, timing, (hipStream_t)stream);
+}
+
+int twell_fp4_quant(const twell_mat_t *x, const twell_fp4_t *out, twell_timing_t *timing,
+                    void *stream)
+{
+    if (!x || !out)
+        return TWELL_E_NULL;
+    if (int rc = check_fp4(out))
+        return rc;
+    if (int rc = check_mat(x, out->rows, out->cols))
+        return rc;
+    if (x->rows == 0 || x->cols == 0)
+        return TWELL_OK;
+    return hip_rc(launch_fp4_quant(x, out, timing, (hipStream_t)stream));
+}
+
+int twell_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing_t *timing,
+                      void *stream)
+{
+    if (!w || !out)
+        return TWELL_E_NULL;
+    if (int rc = check_fp4(w))
+        return rc;
+    if (int rc = check_mat(out, w->rows, w->cols))
+        return rc;
+    if (w->rows == 0 || w->cols == 0)
+        return TWELL_OK;
+    return hip_rc(launch_fp4_dequant(w, out, timing, (hipStream_t)stream));
+}
+
+size_t twell_fp4_matmul_workspace_bytes(twell_dtype x_dtype, int32_t T, int32_t N, int32_t K)
+{
+    if (!dtype_ok(x_dtype) || !fp4_sizes_ok(T, N, K, false) || T == 0 || N == 0)
+        return 0;
+    const twell_mat_t x = worst_mat(x_dtype, T, K);
+    return fp4_mm_workspace(&x, N, K, false);
+}
+
+int twell_fp4_matmul(const twell_mat_t *x, const twell_fp4_t *w, const twell_mat_t *out,
+                     void *workspace, size_t workspace_bytes, twell_timing_t *timing,
+                     void *stream)
+{
+    return fp4_mm(x, w, out, false, workspace, workspace_bytes, timing, stream);
+}
+
+size_t twell_fp4_matmul_dx_workspace_bytes(twell_dtype dy_dtype, int32_t T, int32_t N, int32_t K)
+{
+    if (!dtype_ok(dy_dtype) || !fp4_sizes_ok(T, N, K, true) || T == 0 || K == 0)
+        return 0;
+    const twell_mat_t dy = worst_mat(dy_dtype, T, N);
+    return fp4_mm_workspace(&dy, N, K, true);
+}
+
+int twell_fp4_matmul_dx(const twell_mat_t *dy, const twell_fp4_t *w, const twell_mat_t *dx,
+                        void *workspace, size_t workspace_bytes, twell_timing_t *timing,
+                        void *stream)
+{
+    return fp4_mm(dy, w, dx, true, workspace, workspace_bytes, timing, stream);
+}
+
+size_t twell_fp4_decode_workspace_bytes(twell_dtype x_dtype, int32_t T, int32_t d_model,
+                                        int32_t d_ff)
+{
+    if (!dtype_ok(x_dtype) || T < 0 || T > TWELL_DECODE_T || check_dm(TWELL_BF16, d_model) ||
+        check_dff(d_ff))
+        return 0;
+    const twell_mat_t x = worst_mat(x_dtype, T, d_model);
+    return fp4_layer_workspace(&x, d_ff);
+}
+
+int twell_fp4_decode_fwd(const twell_mat_t *x, const twell_fp4_t *wg_t, const twell_fp4_t *wu_t,
+                         const twell_fp4_t *wd, float *y, void *workspace, size_t workspace_bytes,
+                         twell_timing_t *timing, void *stream)
+{
+    if (!x || !wg_t || !wu_t || !wd || (x->rows > 0 && !y))
+        return TWELL_E_NULL;
+    if (x->rows < 0 || x->rows > TWELL_DECODE_T)
+        return TWELL_E_SHAPE;
+    if (int rc = check_dm(TWELL_BF16, x->cols))
+        return rc;
+    if (int rc = check_dff(wg_t->rows))
+        return rc;
+    for (const twell_fp4_t *m : {wg_t, wu_t, wd}) {
+        if (int rc = check_fp4(m))
+            return rc;
+        if (m->rows != wg_t->rows || m->cols != x->cols || m->group != wg_t->group)
+            return TWELL_E_SHAPE;
+    }
+    if (int rc = check_mat(x, x->rows, x->cols))
+        return rc;
+    if (!a16(y) || !a16(workspace))
+        return TWELL_E_ALIGN;
+    if (x->rows == 0)
+        return TWELL_OK;
+    const size_t need = fp4_layer_workspace(x, wg_t->rows);
+    if (workspace_bytes < need || !workspace)
+        return TWELL_E_WORKSPACE;
+    return hip_rc(launch_fp4_layer(x, wg_t, wu_t, wd, y, workspace, timing, (hipStream_t)stream));
 }
 
 } // extern "C"

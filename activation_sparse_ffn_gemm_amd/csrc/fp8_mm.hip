@@ -169,19 +169,10 @@ template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
     static_assert(OUTB <= NST * STAGE && LDS <= 160 * 1024, "LDS");
 };
 
+using ng::dma16;
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
-// If kb < kb1: lane l's 16 (4) bytes at base + off go to LDS byte lds + 16 l
-// (4 l). As assembly for the reason given at ng::lds_dma16; the test is inside
-// it so that the step stays one block for the compiler.
-DEVI void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int kb, int kb1)
-{
-    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lskip%=\n\t"
-                 "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n.Lskip%=:"
-                 :
-                 : "v"(off), "s"(base), "s"(lds), "s"(kb), "s"(kb1)
-                 : "m0", "scc");
-}
+// ng::dma16 for four bytes a lane
 DEVI void dma4(const float *base, uint32_t off, uint32_t lds, int kb, int kb1)
 {
     asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lskip%=\n\t"

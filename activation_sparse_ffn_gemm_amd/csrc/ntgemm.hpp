@@ -83,6 +83,16 @@ DEVI void lds_dma16(const uint8_t *g, uint32_t lds)
                  : "v"(g), "s"(lds)
                  : "m0");
 }
+// If kb < kb1: lane l's 16 bytes at base + off go to LDS byte lds + 16 l. The
+// test is inside the assembly so that a step stays one block for the compiler.
+DEVI void dma16(const uint8_t *base, uint32_t off, uint32_t lds, int kb, int kb1)
+{
+    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lskip%=\n\t"
+                 "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1\n.Lskip%=:"
+                 :
+                 : "v"(off), "s"(base), "s"(lds), "s"(kb), "s"(kb1)
+                 : "m0", "scc");
+}
 #pragma clang diagnostic pop
 
 // Byte offset of 16-byte chunk c of LDS row r. With 64-byte rows, rows r,

@@ -434,6 +434,105 @@ int twell_fp8_matmul(const twell_fp8_t *a, const twell_fp8_t *b, const twell_mat
  * (0 when it needs none, and on invalid arguments). */
 size_t twell_fp8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K);
 
+/*
+ * ---- Weights in 4 bits, for serving (every byte of the weights is read for
+ * each token there) and for training beside frozen weights.
+ *
+ * twell_fp4_t: a matrix in 4 bits (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives) with one bfloat16 scale for each `group` (32, 64 or 128) columns
+ * of a row. Element (r, c) stands for value(code) * scale[c / group][r].
+ *   q      [rows][cols rounded up to 128, / 2] uint8, 16-byte aligned: column
+ *          2b in the low half of byte b, 2b + 1 in the high half; bit 3 of a
+ *          code is the sign, bits 0 to 2 number the values above. The columns
+ *          past `cols` hold codes of zero
+ *   scale  [cols rounded up to 128, / group][rows] bfloat16, 2-byte aligned
+ * The library writes scale = amax / 6 over the group, amax held within
+ * [2^-64, 2^127], rounded to six significant bits (ties to even): each value
+ * times its scale is then a bfloat16 number. A code is that of the value
+ * nearest to w / scale, ties to even, at most 6. A group that holds a NaN or
+ * an infinity gets the scale NaN and codes of zero, so that all of it stands
+ * for NaN. Groups past `cols` get the scale of a group of zeros.
+ * Other scales are taken as well; where one times a value is no bfloat16
+ * number, products of many tokens and dY W take it rounded to the nearest.
+ */
+#define TWELL_FP4_BLOCK 128 /* columns that a row is padded to */
+typedef struct {
+    int32_t rows, cols, group;
+    uint8_t *q;
+    uint16_t *scale;
+} twell_fp4_t;
+
+/*
+ * x in 4 bits: out of x's size. 0 <= rows, cols <= TWELL_MAX_ROWS.
+ * Errors: NULL / SHAPE / DTYPE / ALIGN / HIP.
+ */
+int twell_fp4_quant(const twell_mat_t *x, const twell_fp4_t *out, twell_timing_t *timing,
+                    void *stream);
+
+/*
+ * The values that w stands for, in out of its size (a bfloat16 copy holds the
+ * library's own exactly: the weights of a long prefill, or of a forward whose
+ * float32 masters are trained). Errors: NULL / SHAPE / DTYPE / ALIGN / HIP.
+ */
+int twell_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing_t *timing,
+                      void *stream);
+
+/*
+ * out[t][n] = sum over k of x[t][k] w[n][k] for w in 4 bits: x [T][w.cols],
+ * out [T][w.rows], each float32 or bfloat16 with rows any stride apart. Every
+ * product is exact (float32 activations are taken as three bfloat16 numbers
+ * that add up to them), sums are float32, out is rounded once. out must not
+ * overlap x. w.cols <= TWELL_MAX_K.
+ *   workspace: twell_fp4_matmul_workspace_bytes(...) bytes are enough for any
+ *   strides and alignment; a call that itself takes less asks for no more, 0
+ *   (and workspace may be NULL) among others for few tokens of bfloat16, 16-byte
+ *   aligned, cols a multiple of 128.
+ * Errors: NULL / SHAPE / DTYPE / ALIGN / WORKSPACE / HIP.
+ */
+int twell_fp4_matmul(const twell_mat_t *x, const twell_fp4_t *w, const twell_mat_t *out,
+                     void *workspace, size_t workspace_bytes, twell_timing_t *timing,
+                     void *stream);
+
+/* Workspace bytes twell_fp4_matmul needs for x [T][K] of type x_dtype and w
+ * [N][K] (0 when it needs none, and on invalid arguments). */
+size_t twell_fp4_matmul_workspace_bytes(twell_dtype x_dtype, int32_t T, int32_t N, int32_t K);
+
+/*
+ * The product's gradient for x: dx[t][k] = sum over n of dy[t][n] w[n][k], dy
+ * [T][w.rows], dx [T][w.cols]; otherwise as twell_fp4_matmul (w.rows <=
+ * TWELL_MAX_K). The weights have none: they are frozen.
+ * Errors: NULL / SHAPE / DTYPE / ALIGN / WORKSPACE / HIP.
+ */
+int twell_fp4_matmul_dx(const twell_mat_t *dy, const twell_fp4_t *w, const twell_mat_t *dx,
+                        void *workspace, size_t workspace_bytes, twell_timing_t *timing,
+                        void *stream);
+
+/* Workspace bytes twell_fp4_matmul_dx needs for dy [T][N] of type dy_dtype and
+ * w [N][K]. */
+size_t twell_fp4_matmul_dx_workspace_bytes(twell_dtype dy_dtype, int32_t T, int32_t N, int32_t K);
+
+/*
+ * The sparse layer for few tokens, its three matrices in 4 bits:
+ *   g = x wg_t^T,  u = x wu_t^T,  y = sum over neurons i with g_i > 0 of
+ *   g_i u_i wd[i]
+ * in float32 throughout (g and u are not rounded to a storage type; a NaN of g
+ * counts as positive). wu_t's and wd's rows are read only where some gate is
+ * open.
+ *   x [T][d_model] float32 or bfloat16, 0 <= T <= TWELL_DECODE_T, rows any
+ *   stride apart; wg_t, wu_t, wd [d_ff][d_model] of one group, d_model and d_ff
+ *   within the layer's limits (d_model <= 4096); y [T][d_model] float32.
+ *   workspace: at least twell_fp4_decode_workspace_bytes(...) bytes.
+ * Nothing is allocated or synchronised; a caller may capture the call.
+ * Errors: NULL / SHAPE / DTYPE / ALIGN / WORKSPACE / HIP.
+ */
+int twell_fp4_decode_fwd(const twell_mat_t *x, const twell_fp4_t *wg_t, const twell_fp4_t *wu_t,
+                         const twell_fp4_t *wd, float *y, void *workspace, size_t workspace_bytes,
+                         twell_timing_t *timing, void *stream);
+
+/* Workspace bytes twell_fp4_decode_fwd needs (0 on invalid arguments). */
+size_t twell_fp4_decode_workspace_bytes(twell_dtype x_dtype, int32_t T, int32_t d_model,
+                                        int32_t d_ff);
+
 /* Static text for a TWELL_* status code (host). */
 const char *twell_status_str(int code);
 
