@@ -198,6 +198,195 @@ template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
         rows_one<G, 2, 16, 8, 2>(a, s);
 }
 
+// ---------------------------------------------------------------- dY W, few tokens
+// The contraction runs over W's rows here, so a lane needs the codes of eight
+// rows at one column. It loads a dword, eight columns, of each of eight rows
+// (16 lanes a row's 64 bytes, straight to registers) and turns the 8 x 8 codes
+// in place: dword j then holds column 8 l + j of the eight rows, and gets the
+// rows' scales (a bfloat16 number each, for six-bit scales exactly). Tile j of
+// the eight 16 x 16 tiles is columns j, 8 + j, 16 + j ..., and a lane's results
+// of one token are runs of eight columns.
+// A workgroup takes a block of 128 columns and one of `parts` runs of rows; its
+// waves take 32 rows at a time. The activations of CN rows are staged in LDS.
+// Parts are joined by a second launch.
+struct ColsArgs {
+    const uint8_t *x;
+    int64_t xrow;
+    int R, nkx; // columns of activations, blocks of 128 that they are padded to
+    Fp4 w;
+    float *part; // [parts][R][128 nkb]
+    int parts, per; // rows of a part: a multiple of CN
+};
+
+// Eight rows of eight codes to eight columns of eight codes: neighbouring rows'
+// nibbles to bytes, then 4 x 4 bytes by permutes.
+DEVI void turn8(uint32_t *v)
+{
+    constexpr uint32_t M = 0x0f0f0f0fu;
+    uint32_t a[2][4]; // [column's parity][pair of rows]: byte b is column 2b + parity
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t lo = v[2 * p], hi = v[2 * p + 1];
+        a[0][p] = (lo & M) | (hi << 4 & ~M);
+        a[1][p] = (lo >> 4 & M) | (hi & ~M);
+    }
+#pragma unroll
+    for (int o = 0; o < 2; ++o) {
+        const uint32_t t0 = __builtin_amdgcn_perm(a[o][1], a[o][0], 0x05010400);
+        const uint32_t t1 = __builtin_amdgcn_perm(a[o][1], a[o][0], 0x07030602);
+        const uint32_t t2 = __builtin_amdgcn_perm(a[o][3], a[o][2], 0x05010400);
+        const uint32_t t3 = __builtin_amdgcn_perm(a[o][3], a[o][2], 0x07030602);
+        v[o] = __builtin_amdgcn_perm(t2, t0, 0x05040100);
+        v[2 + o] = __builtin_amdgcn_perm(t2, t0, 0x07060302);
+        v[4 + o] = __builtin_amdgcn_perm(t3, t1, 0x05040100);
+        v[6 + o] = __builtin_amdgcn_perm(t3, t1, 0x07060302);
+    }
+}
+
+// Eight codes times their scales, each rounded to bfloat16.
+DEVI bf16x8_t scaled8(uint32_t q, const float *s)
+{
+    float c[8];
+    fp4x8_to_f32(q, c);
+    return __builtin_bit_cast(bf16x8_t, make_uint4(f32x2_to_bf16x2(c[0] * s[0], c[1] * s[1]),
+                                                   f32x2_to_bf16x2(c[2] * s[2], c[3] * s[3]),
+                                                   f32x2_to_bf16x2(c[4] * s[4], c[5] * s[5]),
+                                                   f32x2_to_bf16x2(c[6] * s[6], c[7] * s[7])));
+}
+
+constexpr int CWV = 8, CN = 32 * CWV; // waves, rows staged at a time
+template <int TB> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(ColsArgs a)
+{
+    constexpr int XB = 16 * TB * CN * 2, OROW = FP4_BLK + 4; // floats
+    constexpr int OB = CWV * 16 * OROW * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t L[XB > OB ? XB : OB];
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = lane >> 4;
+    // an XCD takes a run of neighbouring blocks: two share W's 128-byte lines
+    const int total = a.w.nkb * a.parts, each = (total + NXCD - 1) / NXCD;
+    const int at = (int)blockIdx.x / NXCD, id = (int)(blockIdx.x % NXCD) * each + at;
+    if (at >= each || id >= total)
+        return;
+    const int part = id / a.w.nkb, kb = id % a.w.nkb;
+    const int n_lo = part * a.per, n_hi = min(n_lo + a.per, a.w.rows);
+    const uint8_t *wq = a.w.q + (int64_t)kb * FP4_BYTES + l16 * 4;
+    const uint16_t *sc = a.w.scale + (int64_t)((kb * FP4_BLK + l16 * 8) / a.w.group) * a.w.rows;
+    floatx4_t acc[8][TB];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            acc[j][t] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+    for (int n0 = n_lo; n0 < n_hi; n0 += CN) {
+        // this wave's rows: past the matrix the last one, whose activations are zeros
+        const int n = n0 + w * 32 + q4 * 8;
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = *(const uint32_t *)(wq + (int64_t)min(n + i, a.w.rows - 1) * a.w.pitch);
+        float s[8];
+        if (n + 8 <= a.w.rows) {
+            elem<TWELL_BF16>::widen(ldg16u(sc + n), s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                s[i] = bf16_to_f32(sc[min(n + i, a.w.rows - 1)]);
+        }
+        if (n0 > n_lo)
+            __syncthreads(); // the last rows' activations are used
+        constexpr int CH = CN / 8; // chunks of 16 bytes of a column
+#pragma unroll
+        for (int i = 0; i < 16 * TB * CH / (64 * CWV); ++i) {
+            const int q = i * 64 * CWV + threadIdx.x, c = q / CH, k = q % CH;
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (c < a.R && n0 + k * 8 < a.nkx * FP4_BLK)
+                u = ldg16(a.x + c * a.xrow + (int64_t)(n0 + k * 8) * 2);
+            *(uint4 *)(L + c * CN * 2 + ((k ^ (c & 15)) << 4)) = u;
+        }
+        __syncthreads();
+        turn8(v);
+        bf16x8_t xf[TB];
+#pragma unroll
+        for (int t = 0; t < TB; ++t)
+            xf[t] = __builtin_bit_cast(
+                bf16x8_t, *(const uint4 *)(L + (t * 16 + l16) * CN * 2 + (((w * 4 + q4) ^ l16) << 4)));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const bf16x8_t f = scaled8(v[j], s);
+#pragma unroll
+            for (int t = 0; t < TB; ++t)
+                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, xf[t], acc[j][t], 0, 0, 0);
+        }
+    }
+    // the waves' sums meet in LDS, 16 columns of activations at a time
+    float(*O)[16][OROW] = (float(*)[16][OROW])L;
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float *p = &O[w][l16][(q4 * 4 + e) * 8];
+            *(floatx4_t *)p = floatx4_t{acc[0][t][e], acc[1][t][e], acc[2][t][e], acc[3][t][e]};
+            *(floatx4_t *)(p + 4) =
+                floatx4_t{acc[4][t][e], acc[5][t][e], acc[6][t][e], acc[7][t][e]};
+        }
+        __syncthreads();
+        const int c = threadIdx.x / 32, k = threadIdx.x % 32 * 4;
+        floatx4_t o = *(const floatx4_t *)&O[0][c][k];
+#pragma unroll
+        for (int u = 1; u < CWV; ++u)
+            o += *(const floatx4_t *)&O[u][c][k];
+        if (t * 16 + c < a.R)
+            *(floatx4_t *)(a.part + ((int64_t)part * a.R + t * 16 + c) * a.w.nkb * FP4_BLK +
+                           kb * FP4_BLK + k) = o;
+    }
+}
+
+// out [T][N] = the sum of the parts, in order, of a token's `planes` rows; the
+// smaller planes first. Four columns a thread.
+struct JoinArgs {
+    const float *part;
+    int parts, T, planes, N;
+    int64_t pitch; // floats of a row of a part
+    void *out;
+    int64_t ldo;
+    int dto;
+};
+__global__ __launch_bounds__(256) void fp4_join_kernel(JoinArgs a)
+{
+    const int64_t n4 = (a.N + 3) / 4, total = n4 * a.T;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total;
+         q += (int64_t)gridDim.x * 256) {
+        const int64_t t = q / n4;
+        const int n = (int)(q % n4) * 4;
+        const int64_t stride = (int64_t)a.T * a.planes * a.pitch;
+        floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
+        for (int p = a.planes - 1; p >= 0; --p) {
+            const float *src = a.part + (t * a.planes + p) * a.pitch + n;
+            floatx4_t v = *(const floatx4_t *)src;
+            for (int i = 1; i < a.parts; ++i)
+                v += *(const floatx4_t *)(src + i * stride);
+            sum += v;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < a.N) {
+                if (a.dto == TWELL_BF16)
+                    ((uint16_t *)a.out)[t * a.ldo + n + e] = (uint16_t)f32x2_to_bf16x2(sum[e], 0.f);
+                else
+                    ((float *)a.out)[t * a.ldo + n + e] = sum[e];
+            }
+    }
+}
+
+// Parts of the contraction: about a workgroup a CU, of at least CN rows each.
+int cols_parts(int N, int nkb, int *per)
+{
+    const int most = (N + CN - 1) / CN, want = nkb < 256 ? 256 / nkb : 1;
+    const int parts = most < want ? (most > 0 ? most : 1) : want;
+    *per = ((N + parts - 1) / parts + CN - 1) / CN * CN;
+    return *per ? (N + *per - 1) / *per : 1;
+}
+
 // ---------------------------------------------------------------- many tokens
 // The values as bfloat16 in the workspace, then a dense product on the shared
 // main loop, over a float32 token's three rows in turn.
@@ -294,14 +483,19 @@ void fp4_rows(const Acts &x, const Fp4 &w, void *out, int64_t ldo, int dto, hipS
         rows_group<128>(a, s);
 }
 
-// Workspace: the packed activations, then the weights' values. dx: of dY W.
+// Workspace: the packed activations, then the parts' sums or the weights' values.
 size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
 {
-    const size_t pack = fp4_pack_bytes(x);
-    if (!dx && few(x->rows, x->dtype == TWELL_BF16 ? 1 : 3))
-        return pack;
-    const size_t r = dx ? (size_t)fp4_blocks(rows) * FP4_BLK : rows;
-    return up256(pack) + r * fp4_blocks(cols) * FP4_BLK * 2;
+    const size_t pack = fp4_pack_bytes(x), pitch = (size_t)fp4_blocks(cols) * FP4_BLK;
+    const int planes = x->dtype == TWELL_BF16 ? 1 : 3;
+    if (few(x->rows, planes)) {
+        if (!dx)
+            return pack;
+        int per;
+        return up256(pack) + (size_t)cols_parts(rows, fp4_blocks(cols), &per) * x->rows * planes *
+                                 pitch * 4;
+    }
+    return up256(pack) + (dx ? (size_t)fp4_blocks(rows) * FP4_BLK : rows) * pitch * 2;
 }
 
 int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t *out, bool dx,
@@ -316,15 +510,32 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
     const Acts a = fp4_pack(x, ws, s, &packed);
     if (packed)
         tm.mark("fp4_pack");
-    if (!dx && few(a.T, a.planes)) {
+    uint8_t *ws2 = (uint8_t *)ws + up256(fp4_pack_bytes(x));
+    if (few(a.T, a.planes) && !dx) {
         fp4_rows(a, w, out->data, out->ld, out->dtype, s);
         tm.mark("fp4_rows");
+    } else if (few(a.T, a.planes)) {
+        ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T * a.planes, a.nkb, w,
+                      (float *)ws2, 0, 0};
+        c.parts = cols_parts(w.rows, w.nkb, &c.per);
+        const uint32_t grid = (uint32_t)((w.nkb * c.parts + NXCD - 1) / NXCD * NXCD);
+        if (c.R <= 16)
+            fp4_cols_kernel<1><<<grid, 64 * CWV, 0, s>>>(c);
+        else if (c.R <= 32)
+            fp4_cols_kernel<2><<<grid, 64 * CWV, 0, s>>>(c);
+        else
+            fp4_cols_kernel<4><<<grid, 64 * CWV, 0, s>>>(c);
+        tm.mark("fp4_cols");
+        const JoinArgs j = {c.part, c.parts, a.T, a.planes, w.cols, (int64_t)w.nkb * FP4_BLK,
+                            out->data, out->ld, (int)out->dtype};
+        const int64_t threads = (int64_t)((w.cols + 3) / 4) * a.T;
+        fp4_join_kernel<<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(j);
+        tm.mark("fp4_join");
     } else {
-        uint8_t *wv = (uint8_t *)ws + up256(fp4_pack_bytes(x));
         const int cols = w.nkb * FP4_BLK, rows = dx ? fp4_blocks(w.rows) * FP4_BLK : w.rows;
-        fp4_dequant(w, wv, cols, TWELL_BF16, rows, cols, s);
+        fp4_dequant(w, ws2, cols, TWELL_BF16, rows, cols, s);
         tm.mark("fp4_dequant");
-        const GemmArgs g = {a, wv, (int64_t)cols * 2, dx ? w.cols : w.rows, dx ? cols : rows,
+        const GemmArgs g = {a, ws2, (int64_t)cols * 2, dx ? w.cols : w.rows, dx ? cols : rows,
                             out->data, out->ld, (int)out->dtype};
         dx ? gemm<ng::KM>(g, s) : gemm<ng::KC>(g, s);
         tm.mark("fp4_gemm");
