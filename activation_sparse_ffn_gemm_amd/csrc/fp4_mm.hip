@@ -4,9 +4,29 @@
 // with c the code's value. Codes are bfloat16 numbers and float32 activations
 // are three of them (see Acts), so the bfloat16 matrix instruction forms every
 // product exactly; sums are float32.
+#include <cmath>
+#include <cstdlib>
+
 #include "fp4.hpp"
 
 namespace {
+
+// Eight codes times their scales, each rounded to bfloat16 (exact for scales of
+// six bits).
+DEVI bf16x8_t scaled8(uint32_t q, const float *s)
+{
+    float c[8];
+    fp4x8_to_f32(q, c);
+    return __builtin_bit_cast(bf16x8_t, make_uint4(f32x2_to_bf16x2(c[0] * s[0], c[1] * s[1]),
+                                                   f32x2_to_bf16x2(c[2] * s[2], c[3] * s[3]),
+                                                   f32x2_to_bf16x2(c[4] * s[4], c[5] * s[5]),
+                                                   f32x2_to_bf16x2(c[6] * s[6], c[7] * s[7])));
+}
+DEVI bf16x8_t scaled8(uint32_t q, float s)
+{
+    const float v[8] = {s, s, s, s, s, s, s, s};
+    return scaled8(q, v);
+}
 
 // ---------------------------------------------------------------- few tokens
 // A workgroup computes 16 NB rows of W for up to 16 columns (tokens, or a
@@ -243,17 +263,6 @@ DEVI void turn8(uint32_t *v)
     }
 }
 
-// Eight codes times their scales, each rounded to bfloat16.
-DEVI bf16x8_t scaled8(uint32_t q, const float *s)
-{
-    float c[8];
-    fp4x8_to_f32(q, c);
-    return __builtin_bit_cast(bf16x8_t, make_uint4(f32x2_to_bf16x2(c[0] * s[0], c[1] * s[1]),
-                                                   f32x2_to_bf16x2(c[2] * s[2], c[3] * s[3]),
-                                                   f32x2_to_bf16x2(c[4] * s[4], c[5] * s[5]),
-                                                   f32x2_to_bf16x2(c[6] * s[6], c[7] * s[7])));
-}
-
 constexpr int CWV = 8, CN = 32 * CWV; // waves, rows staged at a time
 template <int TB> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(ColsArgs a)
 {
@@ -387,6 +396,292 @@ int cols_parts(int N, int nkb, int *per)
     return *per ? (N + *per - 1) / *per : 1;
 }
 
+// ---------------------------------------------------------------- X W^T, many tokens
+// A workgroup computes BM tokens x BN rows of W. A step is 64 k: the tokens' 128
+// bytes and W's 32 go straight from global memory to LDS, NST steps resident,
+// the tokens' chunks XOR-swizzled so that the 16 rows of a fragment lie on
+// distinct banks. A wave owns WM x WN of the tile, NI fragments of W (the first
+// operand) by MI of tokens. W's codes become bfloat16 numbers times their scales
+// in registers, a fragment at a time beside the products of the one before, so
+// they cost LDS and memory a quarter of what values do.
+// The step's one barrier stands before its last row of products: by then every
+// read of its stage is done and the next stage's loads are in, and the next
+// step's first fragments are read beside that row.
+template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
+    static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
+    static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 16, NI = WN / 16;
+    static constexpr int ABYTES = BM * 128, STAGE = ABYTES + BN * 32;
+    static constexpr int WBA = BM / 8 / NWV, WBB = BN / 32 / NWV, WB = WBA + WBB;
+    static constexpr int SG = 64; // groups of scales staged at a time
+    static constexpr int OROW = 128 + 16, OUTB = 16 * OROW * NWV; // the epilogue's rows
+    static_assert(BM % (8 * NWV) == 0 && BN % (32 * NWV) == 0, "whole loads");
+    static_assert(WN % 32 == 0 && MI * NI >= WB + MI, "loads go out before the last row");
+    static_assert(NST >= 3 && (NST - 2) * WB < 64, "loads in flight must fit vmcnt");
+    static_assert(OUTB <= NST * STAGE && NST * STAGE + SG * BN * 2 <= 160 * 1024, "LDS");
+};
+
+struct TileArgs {
+    Acts x;
+    Fp4 w;
+    void *out;
+    int64_t ldo;
+    int dto;
+    float *part; // split contraction: [parts][T][ldo of a part]
+    int64_t ldp;
+    int parts, per; // parts, blocks of 128 k in each
+};
+
+template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
+{
+    constexpr int NST = C::NST, MI = C::MI, NI = C::NI;
+    __shared__ __attribute__((aligned(16))) uint8_t L[NST * C::STAGE];
+    __shared__ uint16_t ss[C::SG][C::BN];
+    // an XCD takes a run of tiles, eight rows of them at a time
+    constexpr int GM = 8;
+    const int nt = (a.w.rows + C::BN - 1) / C::BN, mt = (a.x.T + C::BM - 1) / C::BM;
+    const int64_t total = (int64_t)nt * mt * a.parts, each = (total + NXCD - 1) / NXCD;
+    const int64_t at = blockIdx.x / NXCD, q0 = blockIdx.x % NXCD * each + at;
+    if (at >= each || q0 >= total)
+        return;
+    const int part = (int)(q0 / ((int64_t)nt * mt));
+    const int64_t q = q0 % ((int64_t)nt * mt), gsz = (int64_t)GM * nt;
+    const int grp = (int)(q / gsz), grows = min(GM, mt - grp * GM), gr = (int)(q % gsz);
+    const int m0 = (grp * GM + gr % grows) * C::BM, n0 = gr / grows * C::BN;
+    const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = lane >> 4;
+    const int wm = w / C::WGN, wn = w % C::WGN;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(ng::lds_u8 *)L;
+
+    // rows past an operand read its last row; their results are dropped
+    const uint8_t *srcx = a.x.data + (int64_t)m0 * a.x.pitch, *srcw = a.w.q + (int64_t)n0 * a.w.pitch;
+    uint32_t off[C::WB];
+#pragma unroll
+    for (int g = 0; g < C::WB; ++g) {
+        if (g < C::WBA) {
+            const int r = (w * C::WBA + g) * 8 + lane / 8;
+            off[g] = (uint32_t)min(r, a.x.T - 1 - m0) * (uint32_t)a.x.pitch +
+                     (((lane & 7) ^ (r >> 1 & 7)) << 4);
+        } else {
+            const int r = (w * C::WBB + g - C::WBA) * 32 + lane / 2;
+            off[g] = (uint32_t)min(r, a.w.rows - 1 - n0) * (uint32_t)a.w.pitch + ((lane & 1) << 4);
+        }
+    }
+    floatx4_t acc[NI][MI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < MI; ++j)
+            acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+
+    const uint8_t *Aw = L + (wm * C::WM + l16) * 128;
+    const uint8_t *Bw = L + C::ABYTES + (wn * C::WN + l16) * 32 + q4 * 8;
+    const int f0 = ((q4 * 2) ^ (l16 >> 1)) << 4, f1 = f0 ^ 16; // this lane's chunks of its row
+    auto fence = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+    };
+    const int b0 = part * a.per, b1 = min(a.w.nkb, b0 + a.per);
+    constexpr int CB = C::SG * G / FP4_BLK; // blocks of k whose scales are staged
+    for (int c0 = b0; c0 < b1; c0 += CB) {
+        const int nb = min(CB, b1 - c0), ks = 2 * nb, n = ks * a.x.planes;
+        // steps are 64 k of one of a token's rows, the smallest row first; the
+        // loads' own step: number, row, place among the row's steps
+        int ls = 0, lp = a.x.planes - 1, lk = 0;
+        auto load = [&](int g, int st) {
+            const uint32_t dst = lds0 + (uint32_t)(st * C::STAGE);
+            if (g < C::WBA)
+                ng::dma16(srcx + lp * a.x.plane + (int64_t)c0 * 256 + lk * 128, off[g],
+                          dst + (w * C::WBA + g) * 1024, ls, n);
+            else
+                ng::dma16(srcw + (int64_t)c0 * FP4_BYTES + lk * 32, off[g],
+                          dst + C::ABYTES + (w * C::WBB + g - C::WBA) * 1024, ls, n);
+        };
+        auto loaded = [&] {
+            ++ls;
+            if (++lk == ks)
+                lk = 0, --lp;
+        };
+        if (c0 > b0)
+            __syncthreads(); // the last scales and stages are used
+#pragma unroll
+        for (int s = 0; s < NST - 1; ++s) {
+#pragma unroll
+            for (int g = 0; g < C::WB; ++g)
+                load(g, s);
+            loaded();
+        }
+        for (int i = threadIdx.x; i < nb * (FP4_BLK / G) * C::BN; i += C::NT) {
+            const int g = i / C::BN, r = i % C::BN;
+            ss[g][r] = a.w.scale[((int64_t)c0 * (FP4_BLK / G) + g) * a.w.rows +
+                                 min(n0 + r, a.w.rows - 1)];
+        }
+        ng::wait_vm<0>();
+        __syncthreads();
+        bf16x8_t xf[MI][2];
+        uint2 raw;
+        float sc;
+        auto ldx = [&](int j, int st) {
+            const uint8_t *p = Aw + st * C::STAGE + j * 16 * 128;
+            xf[j][0] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + f0));
+            xf[j][1] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + f1));
+        };
+        auto ldw = [&](int i, int st, int k) { // fragment i of a row's step k: codes and scale
+            raw = *(const uint2 *)(Bw + st * C::STAGE + i * 16 * 32);
+            sc = bf16_to_f32(ss[(k * 64 + q4 * 16) / G][wn * C::WN + i * 16 + l16]);
+        };
+#pragma unroll
+        for (int j = 0; j < MI; ++j)
+            ldx(j, 0);
+        ldw(0, 0, 0);
+        bf16x8_t wf[2][2]; // fragments in turn
+        auto conv = [&](int b) {
+            wf[b][0] = scaled8(raw.x, sc), wf[b][1] = scaled8(raw.y, sc);
+        };
+        conv(0);
+        for (int s = 0, st = 0, k = 0; s < n; ++s) {
+            const int kn = k + 1 == ks ? 0 : k + 1;
+            const int free = st == 0 ? NST - 1 : st - 1, nxt = st == NST - 1 ? 0 : st + 1;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                if (i == NI - 1) {
+                    fence();
+                    if (s + NST - 1 < n)
+                        ng::wait_vm<(NST - 2) * C::WB>();
+                    else
+                        ng::wait_vm<0>();
+                    __builtin_amdgcn_s_waitcnt(0xC07F); // lgkmcnt(0)
+                    __builtin_amdgcn_s_barrier();
+                    fence();
+                }
+                // the next fragment's codes, converted beside this row's products
+                if (i < NI - 1)
+                    ldw(i + 1, st, k);
+                else
+                    ldw(0, nxt, kn);
+#pragma unroll
+                for (int j = 0; j < MI; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1][0], xf[j][0], acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1][1], xf[j][1], acc[i][j], 0, 0, 0);
+                    if (i == NI - 1)
+                        ldx(j, nxt);
+                    const int t = i * MI + j;
+                    if (t < C::WB)
+                        load(t, free);
+                }
+                conv(i + 1 & 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            loaded();
+            st = nxt, k = kn;
+        }
+    }
+    ng::wait_vm<0>();
+    __syncthreads(); // the stages are free
+    // ---- a lane's four results are one token's (j * 16 + l16), n i * 16 + q4 * 4:
+    // through the wave's own piece of LDS, 128 bytes of 16 tokens at a time
+    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN;
+    uint8_t *buf = L + w * 16 * C::OROW;
+    auto store = [&](auto type, void *out, int64_t ld) {
+        using T = decltype(type);
+        constexpr int ES = sizeof(T), WE = 128 / ES < C::WN ? 128 / ES : C::WN;
+        constexpr int VPL = 16 / ES, LPR = WE / VPL; // values a lane, lanes of a run
+        const int c8 = lane % LPR, rr = lane / LPR;
+#pragma unroll
+        for (int j = 0; j < MI; ++j)
+#pragma unroll
+            for (int h = 0; h < C::WN / WE; ++h) {
+#pragma unroll
+                for (int i = 0; i < WE / 16; ++i) {
+                    const floatx4_t v = acc[h * (WE / 16) + i][j];
+                    uint8_t *p = buf + l16 * C::OROW + (i * 16 + q4 * 4) * ES;
+                    if constexpr (ES == 4)
+                        *(floatx4_t *)p = v;
+                    else
+                        *(uint2 *)p = make_uint2(f32x2_to_bf16x2(v[0], v[1]),
+                                                 f32x2_to_bf16x2(v[2], v[3]));
+                }
+                const int c = nw + h * WE + c8 * VPL;
+#pragma unroll
+                for (int r0 = 0; r0 < 16; r0 += 64 / LPR) {
+                    const int m = mw + j * 16 + r0 + rr;
+                    const uint4 v = *(const uint4 *)(buf + (r0 + rr) * C::OROW + c8 * 16);
+                    T *row = (T *)out + m * ld;
+                    if (m < a.x.T && c + VPL <= a.w.rows) {
+                        stg16u_nt(row + c, v);
+                    } else if (m < a.x.T) {
+                        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < VPL; ++e)
+                            if (c + e < a.w.rows)
+                                row[c + e] = (T)(u[e * ES / 4] >> (8 * ES * e % 32));
+                    }
+                }
+            }
+    };
+    if (a.parts > 1)
+        store(uint32_t(), a.part + (int64_t)part * a.x.T * a.ldp, a.ldp);
+    else if (a.dto == TWELL_F32)
+        store(uint32_t(), a.out, a.ldo);
+    else
+        store(uint16_t(), a.out, a.ldo);
+}
+
+using T256 = TileCfg<256, 256, 2, 4, 3>; // waves of 128 tokens x 64 rows
+using T128 = TileCfg<128, 128, 2, 2, 3>; // waves of 64 x 64
+using T64 = TileCfg<64, 128, 1, 4, 3>;   // waves of 64 x 32
+
+template <int G, class C> void tile_one(const TileArgs &a, hipStream_t s)
+{
+    const int64_t tiles = (int64_t)((a.w.rows + C::BN - 1) / C::BN) *
+                          ((a.x.T + C::BM - 1) / C::BM) * a.parts;
+    const uint32_t grid = (uint32_t)((tiles + NXCD - 1) / NXCD * NXCD);
+    fp4_tile_kernel<G, C><<<grid, C::NT, 0, s>>>(a);
+}
+enum TileKind { TILE_64, TILE_128, TILE_256 };
+template <int G> void tile_group(const TileArgs &a, TileKind k, hipStream_t s)
+{
+    if (k == TILE_256)
+        tile_one<G, T256>(a, s);
+    else if (k == TILE_128)
+        tile_one<G, T128>(a, s);
+    else
+        tile_one<G, T64>(a, s);
+}
+
+// Which tiles, and in how many parts of the contraction.
+struct TilePlan {
+    TileKind k;
+    int parts, per;
+};
+TilePlan tile_plan(int T, int N, int nkb, int planes)
+{
+    TilePlan best = {TILE_64, 1, nkb};
+    double least = 1e300;
+    auto up = [](double a, double b) { return ceil(a / b); };
+    const struct {
+        TileKind k;
+        int bm, bn, occ;
+        double step, tile;
+    } tiles[] = {{TILE_64, 64, 128, 3, 0.6, 1.5}, {TILE_128, 128, 128, 2, 0.8, 2.0},
+                 {TILE_256, 256, 256, 1, 1.0, 4.0}};
+    for (const auto &c : tiles)
+        for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
+            const double wg = up(T, c.bm) * up(N, c.bn) * parts;
+            const double join = parts == 1 ? 0. : 3.0 + (double)parts * T * N * 8 / 4e6;
+            const double t = up(wg, 256 * c.occ) * (up(nkb, parts) * 2 * planes * c.step + c.tile) + join;
+            if (t < least)
+                least = t, best = {c.k, parts, (nkb + parts - 1) / parts};
+        }
+    if (const char *e = getenv("FP4K")) {
+        best.k = (TileKind)atoi(e);
+        best.parts = atoi(getenv("FP4P"));
+        best.per = (nkb + best.parts - 1) / best.parts;
+    }
+    best.parts = best.per ? (nkb + best.per - 1) / best.per : 1;
+    return best;
+}
+int64_t part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
+
 // ---------------------------------------------------------------- many tokens
 // The values as bfloat16 in the workspace, then a dense product on the shared
 // main loop, over a float32 token's three rows in turn.
@@ -495,7 +790,11 @@ size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
         return up256(pack) + (size_t)cols_parts(rows, fp4_blocks(cols), &per) * x->rows * planes *
                                  pitch * 4;
     }
-    return up256(pack) + (dx ? (size_t)fp4_blocks(rows) * FP4_BLK : rows) * pitch * 2;
+    if (!dx) {
+        const TilePlan p = tile_plan(x->rows, rows, fp4_blocks(cols), planes);
+        return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(rows) * 4;
+    }
+    return up256(pack) + (size_t)fp4_blocks(rows) * FP4_BLK * pitch * 2;
 }
 
 int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t *out, bool dx,
@@ -531,6 +830,24 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
         const int64_t threads = (int64_t)((w.cols + 3) / 4) * a.T;
         fp4_join_kernel<<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(j);
         tm.mark("fp4_join");
+    } else if (!dx) {
+        const TilePlan p = tile_plan(a.T, w.rows, w.nkb, a.planes);
+        const TileArgs t = {a, w, out->data, out->ld, (int)out->dtype, (float *)ws2,
+                            part_pitch(w.rows), p.parts, p.per};
+        if (w.group == 32)
+            tile_group<32>(t, p.k, s);
+        else if (w.group == 64)
+            tile_group<64>(t, p.k, s);
+        else
+            tile_group<128>(t, p.k, s);
+        tm.mark("fp4_tile");
+        if (p.parts > 1) {
+            const JoinArgs j = {t.part, p.parts, a.T, 1, w.rows, t.ldp, out->data, out->ld,
+                                (int)out->dtype};
+            const int64_t threads = (int64_t)((w.rows + 3) / 4) * a.T, wgs = (threads + 255) / 256;
+            fp4_join_kernel<<<(uint32_t)(wgs < 1 << 22 ? wgs : 1 << 22), 256, 0, s>>>(j);
+            tm.mark("fp4_join");
+        }
     } else {
         const int cols = w.nkb * FP4_BLK, rows = dx ? fp4_blocks(w.rows) * FP4_BLK : w.rows;
         fp4_dequant(w, ws2, cols, TWELL_BF16, rows, cols, s);

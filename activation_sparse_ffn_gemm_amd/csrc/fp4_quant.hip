@@ -237,8 +237,9 @@ __global__ __launch_bounds__(256) void fp4_pack_kernel(const void *x, int dt, in
 
 size_t fp4_pack_bytes(const twell_mat_t *x)
 {
-    const bool bf = x->dtype == TWELL_BF16;
-    if (bf && x->cols % FP4_BLK == 0 && (x->rows == 1 || x->ld % 8 == 0) &&
+    // (the tile kernels address 256 rows by 32-bit offsets)
+    const bool bf = x->dtype == TWELL_BF16, near = x->rows == 1 || x->ld < 1 << 23;
+    if (bf && near && x->cols % FP4_BLK == 0 && (x->rows == 1 || x->ld % 8 == 0) &&
         (uintptr_t)x->data % 16 == 0)
         return 0;
     return (size_t)x->rows * fp4_blocks(x->cols) * FP4_BLK * 2 * (bf ? 1 : 3);

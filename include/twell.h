@@ -456,6 +456,7 @@ size_t twell_fp8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K);
  * number, products of many tokens and dY W take it rounded to the nearest.
  */
 #define TWELL_FP4_BLOCK 128 /* columns that a row is padded to */
+#define TWELL_FP4_MAX_K (1 << 21) /* longest contraction of a product */
 typedef struct {
     int32_t rows, cols, group;
     uint8_t *q;
@@ -482,7 +483,7 @@ int twell_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing
  * out [T][w.rows], each float32 or bfloat16 with rows any stride apart. Every
  * product is exact (float32 activations are taken as three bfloat16 numbers
  * that add up to them), sums are float32, out is rounded once. out must not
- * overlap x. w.cols <= TWELL_MAX_K.
+ * overlap x. w.cols <= TWELL_FP4_MAX_K.
  *   workspace: twell_fp4_matmul_workspace_bytes(...) bytes are enough for any
  *   strides and alignment; a call that itself takes less asks for no more, 0
  *   (and workspace may be NULL) among others for few tokens of bfloat16, 16-byte
@@ -500,7 +501,7 @@ size_t twell_fp4_matmul_workspace_bytes(twell_dtype x_dtype, int32_t T, int32_t 
 /*
  * The product's gradient for x: dx[t][k] = sum over n of dy[t][n] w[n][k], dy
  * [T][w.rows], dx [T][w.cols]; otherwise as twell_fp4_matmul (w.rows <=
- * TWELL_MAX_K). The weights have none: they are frozen.
+ * TWELL_FP4_MAX_K). The weights have none: they are frozen.
  * Errors: NULL / SHAPE / DTYPE / ALIGN / WORKSPACE / HIP.
  */
 int twell_fp4_matmul_dx(const twell_mat_t *dy, const twell_fp4_t *w, const twell_mat_t *dx,
