@@ -5,11 +5,14 @@
 // are three of them (see Acts), so the bfloat16 matrix instruction forms every
 // product exactly; sums are float32.
 #include <cmath>
-#include <cstdlib>
 
 #include "fp4.hpp"
 
 namespace {
+
+struct __attribute__((packed, aligned(2), may_alias)) bytes8 {
+    uint32_t x, y;
+};
 
 // Eight codes times their scales, each rounded to bfloat16 (exact for scales of
 // six bits).
@@ -22,10 +25,41 @@ DEVI bf16x8_t scaled8(uint32_t q, const float *s)
                                                    f32x2_to_bf16x2(c[4] * s[4], c[5] * s[5]),
                                                    f32x2_to_bf16x2(c[6] * s[6], c[7] * s[7])));
 }
-DEVI bf16x8_t scaled8(uint32_t q, float s)
+// Two of them: those of byte h.
+DEVI uint32_t scaled2(uint32_t q, int h, float s)
 {
-    const float v[8] = {s, s, s, s, s, s, s, s};
-    return scaled8(q, v);
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    const f32x2_t c = h == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0)
+                      : h == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1)
+                      : h == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2)
+                               : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
+    return f32x2_to_bf16x2(c[0] * s, c[1] * s);
+}
+
+// Four results of a row, from column n, as far as N goes.
+DEVI void store4(void *out, int dto, int64_t ldo, int64_t row, int n, int N, floatx4_t v)
+{
+    if (dto == TWELL_BF16) {
+        uint16_t *p = (uint16_t *)out + row * ldo + n;
+        const uint2 u = make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+        if (n + 4 <= N) {
+            *(bytes8 *)p = bytes8{u.x, u.y};
+        } else {
+            for (int e = 0; e < 3; ++e)
+                if (n + e < N)
+                    p[e] = (uint16_t)((e < 2 ? u.x : u.y) >> (16 * (e & 1)));
+        }
+    } else {
+        float *p = (float *)out + row * ldo + n;
+        if (n + 4 <= N) {
+            stg16u(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                                 __float_as_uint(v[2]), __float_as_uint(v[3])));
+        } else {
+            for (int e = 0; e < 3; ++e)
+                if (n + e < N)
+                    p[e] = v[e];
+        }
+    }
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -45,9 +79,11 @@ struct RowsArgs {
     int64_t ldo;
     int dto, tile0; // first tile of rows of this launch
     int tiles;      // tiles of rows of this launch
+    Fp4Up up;       // the sparse layer's
 };
 
-template <int G, int NB, int XR, int WV, int NST>
+// UP: the results are the sparse layer's gates, and out its a (see Fp4Up).
+template <int G, int NB, int XR, int WV, int NST, bool UP>
 __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
 {
     constexpr int STG = NB * 1024 + XR * 256, NG = FP4_BLK / G, MF = G / 32, LPF = NB + XR / 4;
@@ -57,6 +93,7 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
     static_assert(XR % 4 == 0 && (NST - 1) * LPF < 64 && (NST & (NST - 1)) == 0, "stages");
     __shared__ __attribute__((aligned(16))) uint8_t L[BUF];
     __shared__ __attribute__((aligned(8))) uint16_t ss[SCB * NG][16 * NB];
+    __shared__ __attribute__((aligned(16))) float gate[UP ? 16 : 1][16 * NB];
     const int lane = threadIdx.x & 63, w = wave_id();
     const int l16 = lane & 15, q4 = lane >> 4;
     const int tile = (int)(blockIdx.x % (uint32_t)a.tiles), mt = (int)(blockIdx.x / (uint32_t)a.tiles);
@@ -107,9 +144,14 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
         for (int q = threadIdx.x; q < nk * NG * 4 * NB; q += 64 * WV) {
             const int g = q / (4 * NB), r = q % (4 * NB) * 4;
             const uint16_t *p = a.w.scale + ((int64_t)k0 * NG + g) * a.w.rows;
+            if (n0 + r + 4 <= a.w.rows) {
+                const bytes8 v = *(const bytes8 *)(p + n0 + r);
+                *(uint2 *)&ss[g][r] = make_uint2(v.x, v.y);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                ss[g][r + e] = p[min(n0 + r + e, a.w.rows - 1)];
+                for (int e = 0; e < 4; ++e)
+                    ss[g][r + e] = p[min(n0 + r + e, a.w.rows - 1)];
+            }
         }
         __syncthreads();
         for (int i = 0; i < n; ++i) {
@@ -183,22 +225,29 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
             m = m0 + l16 / 3;
             mine = l16 % 3 == 0 && l16 < 15;
         }
-        if (!mine || m >= a.T)
-            continue;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int n = n0 + b * 16 + q4 * 4 + e;
-            if (n < a.w.rows) {
-                if (a.dto == TWELL_BF16)
-                    ((uint16_t *)a.out)[m * a.ldo + n] = (uint16_t)f32x2_to_bf16x2(o[e], 0.f);
-                else
-                    ((float *)a.out)[m * a.ldo + n] = o[e];
-            }
+        if (UP)
+            *(floatx4_t *)&gate[l16][b * 16 + q4 * 4] = o;
+        else if (mine && m < a.T)
+            store4(a.out, a.dto, a.ldo, m, n0 + b * 16 + q4 * 4, a.w.rows, o);
+    }
+    if constexpr (UP) { // out is a: g u where g's gate is open, CLOSED elsewhere
+        __syncthreads();
+        constexpr int PER = 64 / (16 * NB) > 0 ? 64 / (16 * NB) : 1; // columns of a set of 64
+        static_assert(16 * NB * PER == 64 || NB == 4, "a wave's set");
+        for (int c = w * PER; c < tpt && m0 + c < a.T; c += WV * PER) {
+            // lane l: neuron l % (16 NB) of the token at column c + l / (16 NB)
+            const int tc = c + lane / (16 * NB), i = lane % (16 * NB);
+            const int t = m0 + tc, n = n0 + i;
+            const bool real = tc < tpt && t < a.T && n < a.w.rows;
+            const float g = real ? gate[a.planes == 3 ? 3 * tc : tc][i] : 0.f;
+            const float v = fp4_up(a.up, g, t, n);
+            if (real)
+                ((float *)a.out)[t * a.ldo + n] = v;
         }
     }
 }
 
-template <int G, int NB, int XR, int WV, int NST> void rows_one(RowsArgs a, hipStream_t s)
+template <int G, int NB, int XR, int NST, bool UP> void rows_one(RowsArgs a, hipStream_t s)
 {
     const int tiles = (int)(((int64_t)a.w.rows + 16 * NB - 1) / (16 * NB));
     const int tpt = a.planes == 3 ? 5 : 16;
@@ -206,16 +255,18 @@ template <int G, int NB, int XR, int WV, int NST> void rows_one(RowsArgs a, hipS
     const int most = (1 << 22) / (int)mt; // threads of a launch are numbered in 32 bits
     for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += a.tiles) {
         a.tiles = tiles - a.tile0 < most ? tiles - a.tile0 : most;
-        fp4_rows_kernel<G, NB, XR, WV, NST><<<mt * (uint32_t)a.tiles, 64 * WV, 0, s>>>(a);
+        fp4_rows_kernel<G, NB, XR, 8, NST, UP><<<mt * (uint32_t)a.tiles, 64 * 8, 0, s>>>(a);
     }
 }
-template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
+template <int G, bool UP> void rows_group(const RowsArgs &a, hipStream_t s)
 {
-    const int cols = a.R < 16 ? a.R : 16;
-    if (cols <= 4)
-        rows_one<G, 1, 4, 8, 4>(a, s);
+    const bool wide = a.w.rows >= 16384;
+    if (a.R <= 4)
+        wide ? rows_one<G, 2, 4, 4, UP>(a, s) : rows_one<G, 1, 4, 4, UP>(a, s);
+    else if (a.R <= 8)
+        wide ? rows_one<G, 4, 8, 2, UP>(a, s) : rows_one<G, 2, 8, 2, UP>(a, s);
     else
-        rows_one<G, 2, 16, 8, 2>(a, s);
+        wide ? rows_one<G, 4, 16, 2, UP>(a, s) : rows_one<G, 2, 16, 2, UP>(a, s);
 }
 
 // ---------------------------------------------------------------- dY W, few tokens
@@ -232,10 +283,13 @@ template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
 struct ColsArgs {
     const uint8_t *x;
     int64_t xrow;
-    int R, nkx; // columns of activations, blocks of 128 that they are padded to
+    int T, planes, nkx; // nkx: blocks of 128 that the activations are padded to
     Fp4 w;
-    float *part; // [parts][R][128 nkb]
+    float *part; // [parts][T][128 nkb]
     int parts, per; // rows of a part: a multiple of CN
+    void *out; // of one part
+    int64_t ldo;
+    int dto;
 };
 
 // Eight rows of eight codes to eight columns of eight codes: neighbouring rows'
@@ -263,11 +317,13 @@ DEVI void turn8(uint32_t *v)
     }
 }
 
-constexpr int CWV = 8, CN = 32 * CWV; // waves, rows staged at a time
-template <int TB> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(ColsArgs a)
+// TB: 16-column tiles of activations (five float32 tokens each); U: sets of 32
+// rows that a wave has in flight.
+constexpr int CWV = 8, CN = 32 * CWV;
+template <int TB, int U> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(ColsArgs a)
 {
-    constexpr int XB = 16 * TB * CN * 2, OROW = FP4_BLK + 4; // floats
-    constexpr int OB = CWV * 16 * OROW * 4;
+    constexpr int ROWS = CN * U, XROW = ROWS * 2, XB = 16 * TB * XROW;
+    constexpr int OROW = FP4_BLK + 4, OB = CWV * 16 * OROW * 4; // (OROW in floats)
     __shared__ __attribute__((aligned(16))) uint8_t L[XB > OB ? XB : OB];
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = lane >> 4;
     // an XCD takes a run of neighbouring blocks: two share W's 128-byte lines
@@ -277,6 +333,7 @@ template <int TB> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(Co
         return;
     const int part = id / a.w.nkb, kb = id % a.w.nkb;
     const int n_lo = part * a.per, n_hi = min(n_lo + a.per, a.w.rows);
+    const bool three = a.planes == 3;
     const uint8_t *wq = a.w.q + (int64_t)kb * FP4_BYTES + l16 * 4;
     const uint16_t *sc = a.w.scale + (int64_t)((kb * FP4_BLK + l16 * 8) / a.w.group) * a.w.rows;
     floatx4_t acc[8][TB];
@@ -285,45 +342,58 @@ template <int TB> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(Co
 #pragma unroll
         for (int t = 0; t < TB; ++t)
             acc[j][t] = floatx4_t{0.f, 0.f, 0.f, 0.f};
-    for (int n0 = n_lo; n0 < n_hi; n0 += CN) {
+    for (int n0 = n_lo; n0 < n_hi; n0 += ROWS) {
         // this wave's rows: past the matrix the last one, whose activations are zeros
-        const int n = n0 + w * 32 + q4 * 8;
-        uint32_t v[8];
+        uint32_t v[U][8];
+        uint4 s[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = *(const uint32_t *)(wq + (int64_t)min(n + i, a.w.rows - 1) * a.w.pitch);
-        float s[8];
-        if (n + 8 <= a.w.rows) {
-            elem<TWELL_BF16>::widen(ldg16u(sc + n), s);
-        } else {
+        for (int u = 0; u < U; ++u) {
+            const int n = n0 + u * CN + w * 32 + q4 * 8;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                s[i] = bf16_to_f32(sc[min(n + i, a.w.rows - 1)]);
+                v[u][i] = *(const uint32_t *)(wq + (int64_t)min(n + i, a.w.rows - 1) * a.w.pitch);
+            if (n + 8 <= a.w.rows) {
+                s[u] = ldg16u(sc + n);
+            } else {
+                uint32_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    h[i] = sc[min(n + i, a.w.rows - 1)];
+                s[u] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                                  h[6] | h[7] << 16);
+            }
         }
         if (n0 > n_lo)
             __syncthreads(); // the last rows' activations are used
-        constexpr int CH = CN / 8; // chunks of 16 bytes of a column
+        constexpr int CH = ROWS / 8; // chunks of 16 bytes of a column
 #pragma unroll
         for (int i = 0; i < 16 * TB * CH / (64 * CWV); ++i) {
-            const int q = i * 64 * CWV + threadIdx.x, c = q / CH, k = q % CH;
+            const int q = i * 64 * CWV + threadIdx.x, c = q / CH, k = q % CH, l = c & 15;
+            const int r = three ? (c >> 4) * 15 + l : c; // its row of activations
             uint4 u = make_uint4(0, 0, 0, 0);
-            if (c < a.R && n0 + k * 8 < a.nkx * FP4_BLK)
-                u = ldg16(a.x + c * a.xrow + (int64_t)(n0 + k * 8) * 2);
-            *(uint4 *)(L + c * CN * 2 + ((k ^ (c & 15)) << 4)) = u;
+            if (r < a.T * a.planes && n0 + k * 8 < a.nkx * FP4_BLK)
+                u = ldg16(a.x + r * a.xrow + (int64_t)(n0 + k * 8) * 2);
+            *(uint4 *)(L + c * XROW + ((k ^ l) << 4)) = u;
         }
         __syncthreads();
-        turn8(v);
-        bf16x8_t xf[TB];
 #pragma unroll
-        for (int t = 0; t < TB; ++t)
-            xf[t] = __builtin_bit_cast(
-                bf16x8_t, *(const uint4 *)(L + (t * 16 + l16) * CN * 2 + (((w * 4 + q4) ^ l16) << 4)));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const bf16x8_t f = scaled8(v[j], s);
+        for (int u = 0; u < U; ++u) {
+            turn8(v[u]);
+            float f[8];
+            elem<TWELL_BF16>::widen(s[u], f);
+            bf16x8_t xf[TB];
 #pragma unroll
             for (int t = 0; t < TB; ++t)
-                acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, xf[t], acc[j][t], 0, 0, 0);
+                xf[t] = __builtin_bit_cast(
+                    bf16x8_t, *(const uint4 *)(L + (t * 16 + l16) * XROW +
+                                               (((u * CWV + w) * 4 + q4 ^ l16) << 4)));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const bf16x8_t c = scaled8(v[u][j], f);
+#pragma unroll
+                for (int t = 0; t < TB; ++t)
+                    acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(c, xf[t], acc[j][t], 0, 0, 0);
+            }
         }
     }
     // the waves' sums meet in LDS, 16 columns of activations at a time
@@ -340,51 +410,78 @@ template <int TB> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(Co
         }
         __syncthreads();
         const int c = threadIdx.x / 32, k = threadIdx.x % 32 * 4;
-        floatx4_t o = *(const floatx4_t *)&O[0][c][k];
+        auto sum = [&](int col) {
+            floatx4_t o = *(const floatx4_t *)&O[0][col][k];
 #pragma unroll
-        for (int u = 1; u < CWV; ++u)
-            o += *(const floatx4_t *)&O[u][c][k];
-        if (t * 16 + c < a.R)
-            *(floatx4_t *)(a.part + ((int64_t)part * a.R + t * 16 + c) * a.w.nkb * FP4_BLK +
-                           kb * FP4_BLK + k) = o;
+            for (int u = 1; u < CWV; ++u)
+                o += *(const floatx4_t *)&O[u][col][k];
+            return o;
+        };
+        const int m = three ? t * 5 + c : t * 16 + c;
+        if (m < a.T && (!three || c < 5)) {
+            const floatx4_t o = three ? (sum(3 * c + 2) + sum(3 * c + 1)) + sum(3 * c) : sum(c);
+            if (a.parts == 1)
+                store4(a.out, a.dto, a.ldo, m, kb * FP4_BLK + k, a.w.cols, o);
+            else
+                *(floatx4_t *)(a.part + ((int64_t)part * a.T + m) * a.w.nkb * FP4_BLK +
+                               kb * FP4_BLK + k) = o;
+        }
     }
 }
 
-// out [T][N] = the sum of the parts, in order, of a token's `planes` rows; the
-// smaller planes first. Four columns a thread.
+// out [T][N] = the sum of the parts, in order. Four columns a thread.
 struct JoinArgs {
     const float *part;
-    int parts, T, planes, N;
-    int64_t pitch; // floats of a row of a part
+    int parts, T, N;
+    int64_t pitch; // floats of a row of a part, a multiple of four
     void *out;
     int64_t ldo;
     int dto;
 };
-__global__ __launch_bounds__(256) void fp4_join_kernel(JoinArgs a)
+__global__ __launch_bounds__(64) void fp4_join_kernel(JoinArgs a)
 {
-    const int64_t n4 = (a.N + 3) / 4, total = n4 * a.T;
-    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total;
-         q += (int64_t)gridDim.x * 256) {
+    const int64_t n4 = (a.N + 3) / 4, total = n4 * a.T, stride = (int64_t)a.T * a.pitch;
+    for (int64_t q = (int64_t)blockIdx.x * 64 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 64) {
         const int64_t t = q / n4;
         const int n = (int)(q % n4) * 4;
-        const int64_t stride = (int64_t)a.T * a.planes * a.pitch;
+        const float *src = a.part + t * a.pitch + n;
         floatx4_t sum = {0.f, 0.f, 0.f, 0.f};
-        for (int p = a.planes - 1; p >= 0; --p) {
-            const float *src = a.part + (t * a.planes + p) * a.pitch + n;
-            floatx4_t v = *(const floatx4_t *)src;
-            for (int i = 1; i < a.parts; ++i)
-                v += *(const floatx4_t *)(src + i * stride);
-            sum += v;
-        }
+        for (int p = 0; p < a.parts; p += 8) { // eight in flight
+            floatx4_t v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < a.N) {
-                if (a.dto == TWELL_BF16)
-                    ((uint16_t *)a.out)[t * a.ldo + n + e] = (uint16_t)f32x2_to_bf16x2(sum[e], 0.f);
-                else
-                    ((float *)a.out)[t * a.ldo + n + e] = sum[e];
-            }
+            for (int i = 0; i < 8; ++i)
+                v[i] = *(const floatx4_t *)(src + min(p + i, a.parts - 1) * stride);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (p + i < a.parts)
+                    sum += v[i];
+        }
+        store4(a.out, a.dto, a.ldo, t, n, a.N, sum);
     }
+}
+void join(const JoinArgs &a, hipStream_t s)
+{
+    const int64_t wgs = ((int64_t)((a.N + 3) / 4) * a.T + 63) / 64;
+    fp4_join_kernel<<<(uint32_t)(wgs < 1 << 24 ? wgs : 1 << 24), 64, 0, s>>>(a);
+}
+
+template <int TB> void cols_tb(const ColsArgs &a, hipStream_t s)
+{
+    const uint32_t grid = (uint32_t)((a.w.nkb * a.parts + NXCD - 1) / NXCD * NXCD);
+    if (a.per > CN)
+        fp4_cols_kernel<TB, 2><<<grid, 64 * CWV, 0, s>>>(a);
+    else
+        fp4_cols_kernel<TB, 1><<<grid, 64 * CWV, 0, s>>>(a);
+}
+void cols(const ColsArgs &a, hipStream_t s)
+{
+    const int tiles = (a.T + (a.planes == 3 ? 4 : 15)) / (a.planes == 3 ? 5 : 16);
+    if (tiles <= 1)
+        cols_tb<1>(a, s);
+    else if (tiles <= 2)
+        cols_tb<2>(a, s);
+    else
+        cols_tb<4>(a, s);
 }
 
 // Parts of the contraction: about a workgroup a CU, of at least CN rows each.
@@ -407,17 +504,25 @@ int cols_parts(int N, int nkb, int *per)
 // The step's one barrier stands before its last row of products: by then every
 // read of its stage is done and the next stage's loads are in, and the next
 // step's first fragments are read beside that row.
-template <int BM_, int BN_, int WGM_, int WGN_, int NST_> struct TileCfg {
-    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_;
+template <int BM_, int BN_, int WGM_, int WGN_, int NST_, int KS_, int SG_> struct TileCfg {
+    static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_, KS = KS_;
     static constexpr int NWV = WGM * WGN, NT = 64 * NWV;
     static constexpr int WM = BM / WGM, WN = BN / WGN, MI = WM / 16, NI = WN / 16;
-    static constexpr int ABYTES = BM * 128, STAGE = ABYTES + BN * 32;
-    static constexpr int WBA = BM / 8 / NWV, WBB = BN / 32 / NWV, WB = WBA + WBB;
-    static constexpr int SG = 64; // groups of scales staged at a time
+    // bytes of a token's and of W's row of a step, 16-byte chunks of them, matrix
+    // instructions of a step and tile
+    static constexpr int RA = KS * 2, RW = KS / 2, CA = RA / 16, CW = RW / 16, NF = KS / 32;
+    static constexpr int ABYTES = BM * RA, STAGE = ABYTES + BN * RW;
+    static constexpr int WBA = ABYTES / 1024 / NWV, WBB = BN * RW / 1024 / NWV, WB = WBA + WBB;
+    // what a row's chunks are XORed with, so that 16 rows lie on distinct banks
+    DEVI static int swa(int r) { return KS == 64 ? r >> 1 & 7 : r & 15; }
+    DEVI static int sww(int r) { return KS == 64 ? 0 : r >> 2 & 3; }
+    static constexpr int SG = SG_; // groups of scales staged at a time
     static constexpr int OROW = 128 + 16, OUTB = 16 * OROW * NWV; // the epilogue's rows
-    static_assert(BM % (8 * NWV) == 0 && BN % (32 * NWV) == 0, "whole loads");
-    static_assert(WN % 32 == 0 && MI * NI >= WB + MI, "loads go out before the last row");
-    static_assert(NST >= 3 && (NST - 2) * WB < 64, "loads in flight must fit vmcnt");
+    static_assert(ABYTES % (1024 * NWV) == 0 && BN * RW % (1024 * NWV) == 0, "whole loads");
+    static_assert(KS == 64 || KS == 128, "a lane's codes share a scale");
+    static constexpr int LPS = (WB + 2 * MI - 1) / (2 * MI); // loads beside a product after it
+    static_assert(WN % 32 == 0 && NI % 2 == 0, "fragments in turn, whole runs of results");
+    static_assert(NST >= 2 && (NST - 2) * WB < 64, "loads in flight must fit vmcnt");
     static_assert(OUTB <= NST * STAGE && NST * STAGE + SG * BN * 2 <= 160 * 1024, "LDS");
 };
 
@@ -432,14 +537,18 @@ struct TileArgs {
     int parts, per; // parts, blocks of 128 k in each
 };
 
-template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
+// PL: rows of a token's activations.
+template <int G, class C, int PL>
+__global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
 {
     constexpr int NST = C::NST, MI = C::MI, NI = C::NI;
     __shared__ __attribute__((aligned(16))) uint8_t L[NST * C::STAGE];
     __shared__ uint16_t ss[C::SG][C::BN];
     // an XCD takes a run of tiles, eight rows of them at a time
     constexpr int GM = 8;
-    const int nt = (a.w.rows + C::BN - 1) / C::BN, mt = (a.x.T + C::BM - 1) / C::BM;
+    constexpr bool three = PL == 3;
+    constexpr int tpt = three ? C::BM / 16 * 5 : C::BM; // tokens of a tile
+    const int nt = (a.w.rows + C::BN - 1) / C::BN, mt = (a.x.T + tpt - 1) / tpt;
     const int64_t total = (int64_t)nt * mt * a.parts, each = (total + NXCD - 1) / NXCD;
     const int64_t at = blockIdx.x / NXCD, q0 = blockIdx.x % NXCD * each + at;
     if (at >= each || q0 >= total)
@@ -447,23 +556,27 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
     const int part = (int)(q0 / ((int64_t)nt * mt));
     const int64_t q = q0 % ((int64_t)nt * mt), gsz = (int64_t)GM * nt;
     const int grp = (int)(q / gsz), grows = min(GM, mt - grp * GM), gr = (int)(q % gsz);
-    const int m0 = (grp * GM + gr % grows) * C::BM, n0 = gr / grows * C::BN;
+    const int m0 = (grp * GM + gr % grows) * tpt, n0 = gr / grows * C::BN;
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = lane >> 4;
     const int wm = w / C::WGN, wn = w % C::WGN;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(ng::lds_u8 *)L;
 
-    // rows past an operand read its last row; their results are dropped
+    // Rows past an operand read its last row; their results are dropped. Of
+    // float32 activations a fragment holds five tokens, three rows each.
+    const int64_t xrow = three ? a.x.plane : a.x.pitch;
     const uint8_t *srcx = a.x.data + (int64_t)m0 * a.x.pitch, *srcw = a.w.q + (int64_t)n0 * a.w.pitch;
     uint32_t off[C::WB];
 #pragma unroll
     for (int g = 0; g < C::WB; ++g) {
         if (g < C::WBA) {
-            const int r = (w * C::WBA + g) * 8 + lane / 8;
-            off[g] = (uint32_t)min(r, a.x.T - 1 - m0) * (uint32_t)a.x.pitch +
-                     (((lane & 7) ^ (r >> 1 & 7)) << 4);
+            const int r = (w * C::WBA + g) * (64 / C::CA) + lane / C::CA;
+            const int x = three ? (r >> 4) * 15 + (r & 15) : r; // this row's
+            const int last = (a.x.T - m0) * PL - 1;
+            off[g] = (uint32_t)min(x, last) * (uint32_t)xrow + (((lane % C::CA) ^ C::swa(r)) << 4);
         } else {
-            const int r = (w * C::WBB + g - C::WBA) * 32 + lane / 2;
-            off[g] = (uint32_t)min(r, a.w.rows - 1 - n0) * (uint32_t)a.w.pitch + ((lane & 1) << 4);
+            const int r = (w * C::WBB + g - C::WBA) * (64 / C::CW) + lane / C::CW;
+            off[g] = (uint32_t)min(r, a.w.rows - 1 - n0) * (uint32_t)a.w.pitch +
+                     (((lane % C::CW) ^ C::sww(r)) << 4);
         }
     }
     floatx4_t acc[NI][MI];
@@ -473,9 +586,15 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
         for (int j = 0; j < MI; ++j)
             acc[i][j] = floatx4_t{0.f, 0.f, 0.f, 0.f};
 
-    const uint8_t *Aw = L + (wm * C::WM + l16) * 128;
-    const uint8_t *Bw = L + C::ABYTES + (wn * C::WN + l16) * 32 + q4 * 8;
-    const int f0 = ((q4 * 2) ^ (l16 >> 1)) << 4, f1 = f0 ^ 16; // this lane's chunks of its row
+    // this lane's row of a fragment, its first chunk of tokens and its codes
+    constexpr int NF = C::NF;
+    const uint8_t *Aw = L + (wm * C::WM + l16) * C::RA;
+    const uint8_t *Bw = L + C::ABYTES + (wn * C::WN + l16) * C::RW +
+                        (C::KS == 64 ? q4 * 8 : (q4 ^ C::sww(l16)) << 4);
+    int f[NF];
+#pragma unroll
+    for (int e = 0; e < NF; ++e)
+        f[e] = ((q4 * NF + e) ^ C::swa(l16)) << 4;
     auto fence = [] {
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
@@ -483,32 +602,25 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
     const int b0 = part * a.per, b1 = min(a.w.nkb, b0 + a.per);
     constexpr int CB = C::SG * G / FP4_BLK; // blocks of k whose scales are staged
     for (int c0 = b0; c0 < b1; c0 += CB) {
-        const int nb = min(CB, b1 - c0), ks = 2 * nb, n = ks * a.x.planes;
-        // steps are 64 k of one of a token's rows, the smallest row first; the
-        // loads' own step: number, row, place among the row's steps
-        int ls = 0, lp = a.x.planes - 1, lk = 0;
+        const int nb = min(CB, b1 - c0), n = FP4_BLK / C::KS * nb; // steps
+        int ls = 0; // the loads' own step
         auto load = [&](int g, int st) {
             const uint32_t dst = lds0 + (uint32_t)(st * C::STAGE);
             if (g < C::WBA)
-                ng::dma16(srcx + lp * a.x.plane + (int64_t)c0 * 256 + lk * 128, off[g],
+                ng::dma16(srcx + (int64_t)c0 * 256 + ls * C::RA, off[g],
                           dst + (w * C::WBA + g) * 1024, ls, n);
             else
-                ng::dma16(srcw + (int64_t)c0 * FP4_BYTES + lk * 32, off[g],
+                ng::dma16(srcw + (int64_t)c0 * FP4_BYTES + ls * C::RW, off[g],
                           dst + C::ABYTES + (w * C::WBB + g - C::WBA) * 1024, ls, n);
-        };
-        auto loaded = [&] {
-            ++ls;
-            if (++lk == ks)
-                lk = 0, --lp;
         };
         if (c0 > b0)
             __syncthreads(); // the last scales and stages are used
 #pragma unroll
-        for (int s = 0; s < NST - 1; ++s) {
+        for (int s = 0; s < NST; ++s) {
 #pragma unroll
             for (int g = 0; g < C::WB; ++g)
                 load(g, s);
-            loaded();
+            ++ls;
         }
         for (int i = threadIdx.x; i < nb * (FP4_BLK / G) * C::BN; i += C::NT) {
             const int g = i / C::BN, r = i % C::BN;
@@ -517,33 +629,45 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
         }
         ng::wait_vm<0>();
         __syncthreads();
-        bf16x8_t xf[MI][2];
-        uint2 raw;
-        float sc;
+        bf16x8_t xf[MI][NF];
+        uint32_t wf[2][NF][4]; // fragments of W in turn
+        uint32_t raw[2][NF];   // their codes and scales, read a row of products earlier
+        float sc[2];
         auto ldx = [&](int j, int st) {
-            const uint8_t *p = Aw + st * C::STAGE + j * 16 * 128;
-            xf[j][0] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + f0));
-            xf[j][1] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(p + f1));
+#pragma unroll
+            for (int e = 0; e < NF; ++e)
+                xf[j][e] = __builtin_bit_cast(
+                    bf16x8_t, *(const uint4 *)(Aw + st * C::STAGE + j * 16 * C::RA + f[e]));
         };
-        auto ldw = [&](int i, int st, int k) { // fragment i of a row's step k: codes and scale
-            raw = *(const uint2 *)(Bw + st * C::STAGE + i * 16 * 32);
-            sc = bf16_to_f32(ss[(k * 64 + q4 * 16) / G][wn * C::WN + i * 16 + l16]);
+        auto ldw = [&](int i, int st, int k) { // fragment i of step k
+            const uint8_t *p = Bw + st * C::STAGE + i * 16 * C::RW;
+            uint32_t *q = raw[i & 1];
+            if constexpr (NF == 2) {
+                const uint2 u = *(const uint2 *)p;
+                q[0] = u.x, q[1] = u.y;
+            } else {
+                const uint4 u = *(const uint4 *)p;
+                q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
+            }
+            sc[i & 1] = bf16_to_f32(
+                ss[(k * C::KS + q4 * (C::KS / 4)) / G][wn * C::WN + i * 16 + l16]);
+        };
+        auto conv = [&](int i, int p) { // dword p of fragment i
+            wf[i & 1][p / 4][p % 4] = scaled2(raw[i & 1][p / 4], p % 4, sc[i & 1]);
         };
 #pragma unroll
         for (int j = 0; j < MI; ++j)
             ldx(j, 0);
         ldw(0, 0, 0);
-        bf16x8_t wf[2][2]; // fragments in turn
-        auto conv = [&](int b) {
-            wf[b][0] = scaled8(raw.x, sc), wf[b][1] = scaled8(raw.y, sc);
-        };
-        conv(0);
-        for (int s = 0, st = 0, k = 0; s < n; ++s) {
-            const int kn = k + 1 == ks ? 0 : k + 1;
-            const int free = st == 0 ? NST - 1 : st - 1, nxt = st == NST - 1 ? 0 : st + 1;
+        ldw(1, 0, 0);
+#pragma unroll
+        for (int p = 0; p < 4 * NF; ++p)
+            conv(0, p);
+        for (int s = 0, st = 0; s < n; ++s) {
+            const int nxt = st == NST - 1 ? 0 : st + 1, sn = s + 1 < n ? s + 1 : 0;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                if (i == NI - 1) {
+                if (i == NI - 2) {
                     fence();
                     if (s + NST - 1 < n)
                         ng::wait_vm<(NST - 2) * C::WB>();
@@ -553,33 +677,41 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
                     __builtin_amdgcn_s_barrier();
                     fence();
                 }
-                // the next fragment's codes, converted beside this row's products
-                if (i < NI - 1)
-                    ldw(i + 1, st, k);
+                if (i < NI - 2)
+                    ldw(i + 2, st, s);
                 else
-                    ldw(0, nxt, kn);
+                    ldw(i + 2 - NI, nxt, sn);
 #pragma unroll
                 for (int j = 0; j < MI; ++j) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1][0], xf[j][0], acc[i][j], 0, 0, 0);
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[i & 1][1], xf[j][1], acc[i][j], 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < NF; ++e)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            __builtin_bit_cast(bf16x8_t, *(const uint4 *)wf[i & 1][e]), xf[j][e],
+                            acc[i][j], 0, 0, 0);
                     if (i == NI - 1)
                         ldx(j, nxt);
-                    const int t = i * MI + j;
-                    if (t < C::WB)
-                        load(t, free);
+                    // the next fragment, piece by piece beside this row's products
+#pragma unroll
+                    for (int p = j * 4 * NF / MI; p < (j + 1) * 4 * NF / MI; ++p)
+                        conv(i < NI - 1 ? i + 1 : 0, p);
+                    // past the barrier the stage is free: all of its step is in registers
+                    const int t = (i - (NI - 2)) * MI + j;
+#pragma unroll
+                    for (int g = t * C::LPS; g < (t + 1) * C::LPS && g < C::WB; ++g)
+                        if (t >= 0)
+                            load(g, st);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                conv(i + 1 & 1);
-                __builtin_amdgcn_sched_barrier(0);
             }
-            loaded();
-            st = nxt, k = kn;
+            ++ls;
+            st = nxt;
         }
     }
     ng::wait_vm<0>();
     __syncthreads(); // the stages are free
     // ---- a lane's four results are one token's (j * 16 + l16), n i * 16 + q4 * 4:
     // through the wave's own piece of LDS, 128 bytes of 16 tokens at a time
-    const int mw = m0 + wm * C::WM, nw = n0 + wn * C::WN;
+    const int mw = m0 + (three ? wm * C::WM / 16 * 5 : wm * C::WM), nw = n0 + wn * C::WN;
     uint8_t *buf = L + w * 16 * C::OROW;
     auto store = [&](auto type, void *out, int64_t ld) {
         using T = decltype(type);
@@ -592,8 +724,17 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
             for (int h = 0; h < C::WN / WE; ++h) {
 #pragma unroll
                 for (int i = 0; i < WE / 16; ++i) {
-                    const floatx4_t v = acc[h * (WE / 16) + i][j];
-                    uint8_t *p = buf + l16 * C::OROW + (i * 16 + q4 * 4) * ES;
+                    floatx4_t v = acc[h * (WE / 16) + i][j];
+                    int row = l16;
+                    if constexpr (three) { // a token's three rows, the smallest two first
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float mid = __shfl(v[e], lane + 1, 64), lo = __shfl(v[e], lane + 2, 64);
+                            v[e] += mid + lo;
+                        }
+                        row = l16 % 3 == 0 && l16 < 15 ? l16 / 3 : 15;
+                    }
+                    uint8_t *p = buf + row * C::OROW + (i * 16 + q4 * 4) * ES;
                     if constexpr (ES == 4)
                         *(floatx4_t *)p = v;
                     else
@@ -603,7 +744,9 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
                 const int c = nw + h * WE + c8 * VPL;
 #pragma unroll
                 for (int r0 = 0; r0 < 16; r0 += 64 / LPR) {
-                    const int m = mw + j * 16 + r0 + rr;
+                    if (three && r0 + rr >= 5)
+                        continue;
+                    const int m = mw + j * (three ? 5 : 16) + r0 + rr;
                     const uint4 v = *(const uint4 *)(buf + (r0 + rr) * C::OROW + c8 * 16);
                     T *row = (T *)out + m * ld;
                     if (m < a.x.T && c + VPL <= a.w.rows) {
@@ -626,16 +769,20 @@ template <int G, class C> __global__ __launch_bounds__(C::NT, C::NWV / 4) void f
         store(uint16_t(), a.out, a.ldo);
 }
 
-using T256 = TileCfg<256, 256, 2, 4, 3>; // waves of 128 tokens x 64 rows
-using T128 = TileCfg<128, 128, 2, 2, 3>; // waves of 64 x 64
-using T64 = TileCfg<64, 128, 1, 4, 3>;   // waves of 64 x 32
+using T64 = TileCfg<64, 128, 1, 4, 2, 128, 64>;  // waves of 64 tokens x 32 rows
+using T128 = TileCfg<128, 128, 1, 4, 2, 64, 64>; // waves of 128 x 32
+using T256 = TileCfg<256, 256, 2, 4, 3, 64, 64>; // waves of 128 x 64
 
 template <int G, class C> void tile_one(const TileArgs &a, hipStream_t s)
 {
-    const int64_t tiles = (int64_t)((a.w.rows + C::BN - 1) / C::BN) *
-                          ((a.x.T + C::BM - 1) / C::BM) * a.parts;
+    const int tpt = a.x.planes == 3 ? C::BM / 16 * 5 : C::BM;
+    const int64_t tiles = (int64_t)((a.w.rows + C::BN - 1) / C::BN) * ((a.x.T + tpt - 1) / tpt) *
+                          a.parts;
     const uint32_t grid = (uint32_t)((tiles + NXCD - 1) / NXCD * NXCD);
-    fp4_tile_kernel<G, C><<<grid, C::NT, 0, s>>>(a);
+    if (a.x.planes == 3)
+        fp4_tile_kernel<G, C, 3><<<grid, C::NT, 0, s>>>(a);
+    else
+        fp4_tile_kernel<G, C, 1><<<grid, C::NT, 0, s>>>(a);
 }
 enum TileKind { TILE_64, TILE_128, TILE_256 };
 template <int G> void tile_group(const TileArgs &a, TileKind k, hipStream_t s)
@@ -647,8 +794,21 @@ template <int G> void tile_group(const TileArgs &a, TileKind k, hipStream_t s)
     else
         tile_one<G, T64>(a, s);
 }
+void tiles(const TileArgs &a, TileKind k, hipStream_t s)
+{
+    if (a.w.group == 32)
+        tile_group<32>(a, k, s);
+    else if (a.w.group == 64)
+        tile_group<64>(a, k, s);
+    else
+        tile_group<128>(a, k, s);
+}
 
-// Which tiles, and in how many parts of the contraction.
+// Which tiles, and in how many parts of the contraction: the least of the times
+// that these measured figures give (us; they order the choices, no more). A
+// step of 128 k takes `step` alone on its CU and `pair` beside another
+// workgroup (both of them), a tile `ends` more for its beginning and end; parts
+// add a launch and the partial sums' way through memory.
 struct TilePlan {
     TileKind k;
     int parts, per;
@@ -660,42 +820,40 @@ TilePlan tile_plan(int T, int N, int nkb, int planes)
     auto up = [](double a, double b) { return ceil(a / b); };
     const struct {
         TileKind k;
-        int bm, bn, occ;
-        double step, tile;
-    } tiles[] = {{TILE_64, 64, 128, 3, 0.6, 1.5}, {TILE_128, 128, 128, 2, 0.8, 2.0},
-                 {TILE_256, 256, 256, 1, 1.0, 4.0}};
-    for (const auto &c : tiles)
+        int bm, bn;
+        double step, pair, ends;
+    } kinds[] = {{TILE_64, 64, 128, 0.75, 1.1, 2.5}, {TILE_128, 128, 128, 1.1, 1.95, 3.0},
+                 {TILE_256, 256, 256, 2.7, 5.4, 5.0}};
+    for (const auto &c : kinds)
         for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
-            const double wg = up(T, c.bm) * up(N, c.bn) * parts;
-            const double join = parts == 1 ? 0. : 3.0 + (double)parts * T * N * 8 / 4e6;
-            const double t = up(wg, 256 * c.occ) * (up(nkb, parts) * 2 * planes * c.step + c.tile) + join;
+            const double wg = up(T, planes == 3 ? c.bm / 16 * 5 : c.bm) * up(N, c.bn) * parts;
+            const double n = up(wg, 256), k = up(nkb, parts);
+            const double t = floor(n / 2) * (k * c.pair + c.ends) +
+                             (n - 2 * floor(n / 2)) * (k * c.step + c.ends) +
+                             (parts == 1 ? 0. : 3.0 + (double)parts * T * N * 8 / 4e6);
             if (t < least)
                 least = t, best = {c.k, parts, (nkb + parts - 1) / parts};
         }
-    if (const char *e = getenv("FP4K")) {
-        best.k = (TileKind)atoi(e);
-        best.parts = atoi(getenv("FP4P"));
-        best.per = (nkb + best.parts - 1) / best.parts;
-    }
     best.parts = best.per ? (nkb + best.per - 1) / best.per : 1;
     return best;
 }
 int64_t part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
 
-// ---------------------------------------------------------------- many tokens
+// ---------------------------------------------------------------- dY W, many tokens
 // The values as bfloat16 in the workspace, then a dense product on the shared
-// main loop, over a float32 token's three rows in turn.
+// main loop, W's rows along the contraction; a float32 token's three rows in turn,
+// the smallest first.
 struct GemmArgs {
     Acts x;
-    const uint8_t *w; // [n][k] (X W^T) or [k][n] (dY W), zeros past the contraction
+    const uint8_t *w; // [n][k], zeros past the contraction
     int64_t wpitch;
-    int N, NW; // columns of the result, rows (X W^T) or columns (dY W) of w
+    int N, NW; // columns of the result, of w
     void *out;
     int64_t ldo;
     int dto;
 };
 
-template <class C, int LB> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(GemmArgs a)
+template <class C> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(GemmArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t L[C::LDS];
     constexpr int KS = C::ROWB / 2;
@@ -705,23 +863,17 @@ template <class C, int LB> __global__ __launch_bounds__(C::NT) void fp4_gemm_ker
     for (int64_t q = blockIdx.x; q < (int64_t)nt * mt; q += gridDim.x) {
         const int m0 = (int)(q % mt) * C::BM, n0 = (int)(q / mt) * C::BN;
         auto rowa = [&](int r) { return a.x.data + (int64_t)min(m0 + r, a.x.T - 1) * a.x.pitch; };
-        auto rowb = [&](int r) {
-            return LB == ng::KC ? a.w + (int64_t)min(n0 + r, a.NW - 1) * a.wpitch
-                                : a.w + (int64_t)r * a.wpitch + (int64_t)n0 * 2;
-        };
+        auto rowb = [&](int r) { return a.w + (int64_t)r * a.wpitch + (int64_t)n0 * 2; };
         auto off = [&](int kt) {
             const int p = kt / steps, k = kt % steps;
-            return ng::StepOff{(size_t)(p * a.x.plane + (int64_t)k * C::ROWB),
-                               (size_t)(LB == ng::KC ? (int64_t)k * C::ROWB
-                                                     : (int64_t)k * KS * a.wpitch)};
+            return ng::StepOff{
+                (size_t)((a.x.planes - 1 - p) * a.x.plane + (int64_t)k * C::ROWB),
+                (size_t)((int64_t)k * KS * a.wpitch)};
         };
         ng::Acc<C> acc;
-        if constexpr (LB == ng::KC)
-            ng::mainloop<C, TWELL_BF16>(L, rowa, rowb, off, 0, steps * a.x.planes, acc);
-        else
-            ng::mainloop_mixed<C, TWELL_BF16, ng::KC, ng::KM>(L, rowa, rowb, off, 0,
-                                                             steps * a.x.planes, acc, 1 << 30,
-                                                             a.NW - n0);
+        ng::mainloop_mixed<C, TWELL_BF16, ng::KC, ng::KM>(L, rowa, rowb, off, 0,
+                                                         steps * a.x.planes, acc, 1 << 30,
+                                                         a.NW - n0);
 #pragma unroll
         for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
@@ -744,57 +896,53 @@ template <class C, int LB> __global__ __launch_bounds__(C::NT) void fp4_gemm_ker
 using C64 = ng::Cfg<64, 128, 2, 4, 4, 64>;
 using C256 = ng::Cfg<256, 256, 2, 4, 2, 128>;
 
-template <class C, int LB> void gemm_one(const GemmArgs &a, hipStream_t s)
+template <class C> void gemm_one(const GemmArgs &a, hipStream_t s)
 {
     const int64_t tiles = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.x.T + C::BM - 1) / C::BM);
-    const uint32_t grid = (uint32_t)(tiles < 1 << 20 ? tiles : 1 << 20);
-    fp4_gemm_kernel<C, LB><<<grid, C::NT, 0, s>>>(a);
+    fp4_gemm_kernel<C><<<(uint32_t)(tiles < 1 << 20 ? tiles : 1 << 20), C::NT, 0, s>>>(a);
 }
-template <int LB> void gemm(const GemmArgs &a, hipStream_t s)
+void gemm(const GemmArgs &a, hipStream_t s)
 {
-    const int64_t big = (int64_t)((a.N + 255) / 256) * ((a.x.T + 255) / 256);
-    if (big >= 128)
-        gemm_one<C256, LB>(a, s);
+    if ((int64_t)((a.N + 255) / 256) * ((a.x.T + 255) / 256) >= 128)
+        gemm_one<C256>(a, s);
     else
-        gemm_one<C64, LB>(a, s);
+        gemm_one<C64>(a, s);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-bool few(int T, int planes) { return T * (int64_t)planes <= 64; }
+// the few-token kernels: of X W^T for one 16-column tile, of dY W for four
+bool few(int T, int planes, bool dx) { return T <= (planes == 3 ? 5 : 16) * (dx ? 4 : 1); }
+int planes_of(const twell_mat_t *x) { return x->dtype == TWELL_BF16 ? 1 : 3; }
 
 } // namespace
 
 void fp4_dequant(const Fp4 &w, void *out, int64_t ld, int dt, int rows, int cols, hipStream_t s);
 
-void fp4_rows(const Acts &x, const Fp4 &w, void *out, int64_t ldo, int dto, hipStream_t s)
+void fp4_rows(const Acts &x, const Fp4 &w, void *out, int64_t ldo, int dto, const Fp4Up *up,
+              hipStream_t s)
 {
     const RowsArgs a = {x.data, x.planes == 3 ? x.plane : x.pitch, x.T, x.planes, x.T * x.planes,
-                        w, out, ldo, dto, 0, 0};
+                        w, out, ldo, dto, 0, 0, up ? *up : Fp4Up{}};
     if (w.group == 32)
-        rows_group<32>(a, s);
+        up ? rows_group<32, true>(a, s) : rows_group<32, false>(a, s);
     else if (w.group == 64)
-        rows_group<64>(a, s);
+        up ? rows_group<64, true>(a, s) : rows_group<64, false>(a, s);
     else
-        rows_group<128>(a, s);
+        up ? rows_group<128, true>(a, s) : rows_group<128, false>(a, s);
 }
 
 // Workspace: the packed activations, then the parts' sums or the weights' values.
 size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
 {
     const size_t pack = fp4_pack_bytes(x), pitch = (size_t)fp4_blocks(cols) * FP4_BLK;
-    const int planes = x->dtype == TWELL_BF16 ? 1 : 3;
-    if (few(x->rows, planes)) {
-        if (!dx)
-            return pack;
-        int per;
-        return up256(pack) + (size_t)cols_parts(rows, fp4_blocks(cols), &per) * x->rows * planes *
-                                 pitch * 4;
+    if (few(x->rows, planes_of(x), dx)) {
+        int per, parts = dx ? cols_parts(rows, fp4_blocks(cols), &per) : 1;
+        return parts == 1 ? pack : up256(pack) + (size_t)parts * x->rows * pitch * 4;
     }
-    if (!dx) {
-        const TilePlan p = tile_plan(x->rows, rows, fp4_blocks(cols), planes);
-        return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(rows) * 4;
-    }
-    return up256(pack) + (size_t)fp4_blocks(rows) * FP4_BLK * pitch * 2;
+    if (dx)
+        return up256(pack) + (size_t)fp4_blocks(rows) * FP4_BLK * pitch * 2;
+    const TilePlan p = tile_plan(x->rows, rows, fp4_blocks(cols), planes_of(x));
+    return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(rows) * 4;
 }
 
 int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t *out, bool dx,
@@ -810,52 +958,50 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
     if (packed)
         tm.mark("fp4_pack");
     uint8_t *ws2 = (uint8_t *)ws + up256(fp4_pack_bytes(x));
-    if (few(a.T, a.planes) && !dx) {
-        fp4_rows(a, w, out->data, out->ld, out->dtype, s);
+    const int dto = out->dtype;
+    const bool little = few(a.T, planes_of(x), dx);
+    if (!dx && little) {
+        fp4_rows(a, w, out->data, out->ld, dto, nullptr, s);
         tm.mark("fp4_rows");
-    } else if (few(a.T, a.planes)) {
-        ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T * a.planes, a.nkb, w,
-                      (float *)ws2, 0, 0};
-        c.parts = cols_parts(w.rows, w.nkb, &c.per);
-        const uint32_t grid = (uint32_t)((w.nkb * c.parts + NXCD - 1) / NXCD * NXCD);
-        if (c.R <= 16)
-            fp4_cols_kernel<1><<<grid, 64 * CWV, 0, s>>>(c);
-        else if (c.R <= 32)
-            fp4_cols_kernel<2><<<grid, 64 * CWV, 0, s>>>(c);
-        else
-            fp4_cols_kernel<4><<<grid, 64 * CWV, 0, s>>>(c);
-        tm.mark("fp4_cols");
-        const JoinArgs j = {c.part, c.parts, a.T, a.planes, w.cols, (int64_t)w.nkb * FP4_BLK,
-                            out->data, out->ld, (int)out->dtype};
-        const int64_t threads = (int64_t)((w.cols + 3) / 4) * a.T;
-        fp4_join_kernel<<<(uint32_t)((threads + 255) / 256), 256, 0, s>>>(j);
-        tm.mark("fp4_join");
     } else if (!dx) {
-        const TilePlan p = tile_plan(a.T, w.rows, w.nkb, a.planes);
-        const TileArgs t = {a, w, out->data, out->ld, (int)out->dtype, (float *)ws2,
-                            part_pitch(w.rows), p.parts, p.per};
-        if (w.group == 32)
-            tile_group<32>(t, p.k, s);
-        else if (w.group == 64)
-            tile_group<64>(t, p.k, s);
-        else
-            tile_group<128>(t, p.k, s);
+        const TilePlan p = tile_plan(a.T, w.rows, w.nkb, planes_of(x));
+        const TileArgs t = {a, w, out->data, out->ld, dto, (float *)ws2, part_pitch(w.rows),
+                            p.parts, p.per};
+        tiles(t, p.k, s);
         tm.mark("fp4_tile");
         if (p.parts > 1) {
-            const JoinArgs j = {t.part, p.parts, a.T, 1, w.rows, t.ldp, out->data, out->ld,
-                                (int)out->dtype};
-            const int64_t threads = (int64_t)((w.rows + 3) / 4) * a.T, wgs = (threads + 255) / 256;
-            fp4_join_kernel<<<(uint32_t)(wgs < 1 << 22 ? wgs : 1 << 22), 256, 0, s>>>(j);
+            join({t.part, p.parts, a.T, w.rows, t.ldp, out->data, out->ld, dto}, s);
+            tm.mark("fp4_join");
+        }
+    } else if (little) {
+        ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T, a.planes, a.nkb, w,
+                      (float *)ws2, 0, 0, out->data, out->ld, dto};
+        c.parts = cols_parts(w.rows, w.nkb, &c.per);
+        cols(c, s);
+        tm.mark("fp4_cols");
+        if (c.parts > 1) {
+            join({c.part, c.parts, a.T, w.cols, (int64_t)w.nkb * FP4_BLK, out->data, out->ld, dto}, s);
             tm.mark("fp4_join");
         }
     } else {
-        const int cols = w.nkb * FP4_BLK, rows = dx ? fp4_blocks(w.rows) * FP4_BLK : w.rows;
-        fp4_dequant(w, ws2, cols, TWELL_BF16, rows, cols, s);
+        const int wc = w.nkb * FP4_BLK, rows = fp4_blocks(w.rows) * FP4_BLK;
+        fp4_dequant(w, ws2, wc, TWELL_BF16, rows, wc, s);
         tm.mark("fp4_dequant");
-        const GemmArgs g = {a, ws2, (int64_t)cols * 2, dx ? w.cols : w.rows, dx ? cols : rows,
-                            out->data, out->ld, (int)out->dtype};
-        dx ? gemm<ng::KM>(g, s) : gemm<ng::KC>(g, s);
+        gemm({a, ws2, (int64_t)wc * 2, w.cols, wc, out->data, out->ld, dto}, s);
         tm.mark("fp4_gemm");
     }
     return hipGetLastError() == hipSuccess ? TWELL_OK : TWELL_E_HIP;
+}
+
+int fp4_gate_parts(const twell_mat_t *x, int d_ff)
+{
+    const int planes = planes_of(x);
+    return few(x->rows, planes, false)
+               ? 0 : tile_plan(x->rows, d_ff, fp4_blocks(x->cols), planes).parts;
+}
+
+void fp4_gate(const Acts &x, const Fp4 &w, float *parts, hipStream_t s)
+{
+    const TilePlan p = tile_plan(x.T, w.rows, w.nkb, x.planes);
+    tiles({x, w, parts, w.rows, TWELL_F32, parts, w.rows, p.parts, p.per}, p.k, s);
 }
