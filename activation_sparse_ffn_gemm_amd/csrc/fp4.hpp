@@ -93,73 +93,19 @@ struct Acts {
 size_t fp4_pack_bytes(const twell_mat_t *x); // 0: taken where it is
 Acts fp4_pack(const twell_mat_t *x, void *ws, hipStream_t s, bool *packed);
 
-// The sparse layer's up product, beside its gates: a = g u of the open gates.
-struct Fp4Up {
-    const void *x;
-    int64_t ldx;
-    int dt, d;
-    Fp4 w;
-};
-// a of a closed gate: the one float that an open gate's a, a sum with +0, is not
+// The sparse layer's a = g u of an open gate (NaN opens too). A closed gate's is
+// the one float that a sum with +0 is not.
 constexpr uint32_t FP4_CLOSED = 0x80000000u;
-
-// a of (token t, neuron n) with gate g in every lane (0 where there is none): the
-// wave goes through its open gates, two at a time, all lanes on a row of W.
-DEVI float fp4_up(const Fp4Up &p, float g, int t, int n)
+DEVI float fp4_act(float g, float u)
 {
-    constexpr int PAIR = 2;
-    uint64_t open = __ballot(!(g <= 0.f));
-    float a = __uint_as_float(FP4_CLOSED);
-    const int lane = threadIdx.x & 63;
-    while (open) {
-        int at[PAIR];
-        const void *x[PAIR];
-        const uint8_t *row[PAIR];
-        const uint16_t *sc[PAIR];
-        float u[PAIR];
-#pragma unroll
-        for (int i = 0; i < PAIR; ++i) {
-            at[i] = open ? __builtin_ctzll(open) : at[0];
-            open &= open - 1;
-            const int ni = bcast(n, at[i]);
-            x[i] = row_ptr(p.x, p.dt, p.ldx, bcast(t, at[i]));
-            row[i] = p.w.q + (int64_t)ni * p.w.pitch;
-            sc[i] = p.w.scale + ni;
-            u[i] = 0.f;
-        }
-        for (int j = 8 * lane; j < p.d; j += 512) {
-            uint32_t q[PAIR];
-            float s[PAIR], xv[PAIR][8], c[8];
-#pragma unroll
-            for (int i = 0; i < PAIR; ++i) {
-                q[i] = *(const uint32_t *)(row[i] + j / 2);
-                s[i] = bf16_to_f32(sc[i][(int64_t)(j / p.w.group) * p.w.rows]);
-                load8(x[i], p.dt, j, p.d, xv[i]);
-            }
-#pragma unroll
-            for (int i = 0; i < PAIR; ++i) {
-                fp4x8_to_f32(q[i], c);
-                float v = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v = fmaf(c[e], xv[i][e], v);
-                u[i] = fmaf(v, s[i], u[i]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < PAIR; ++i) {
-            const float v = wave_sum(u[i]);
-            if (lane == at[i])
-                a = g * v + 0.f;
-        }
-    }
-    return a;
+    return !(g <= 0.f) ? g * u + 0.f : __uint_as_float(FP4_CLOSED);
 }
 
-// out [T][w.rows] = x w^T for few tokens (any number is right), or, with up, a.
-void fp4_rows(const Acts &x, const Fp4 &w, void *out, int64_t ldo, int dto, const Fp4Up *up,
+// out [T][w.rows] = x w^T for few tokens (any number is right); with up, of w's
+// sizes, out is a of w's gates.
+void fp4_rows(const Acts &x, const Fp4 &w, const Fp4 *up, void *out, int64_t ldo, int dto,
               hipStream_t s);
-// The sparse layer's gates of more tokens: [parts][T][w.rows], parts 0 where
-// fp4_rows takes the tokens.
-int fp4_gate_parts(const twell_mat_t *x, int d_ff);
-void fp4_gate(const Acts &x, const Fp4 &w, float *parts, hipStream_t s);
+// Gates and up products of more tokens: [parts][T][2 wg.rows], parts 0 where
+// fp4_rows takes the tokens. wg.rows is a multiple of 128.
+int fp4_gates_parts(const twell_mat_t *x, int d_ff);
+void fp4_gates(const Acts &x, const Fp4 &wg, const Fp4 &wu, float *parts, hipStream_t s);

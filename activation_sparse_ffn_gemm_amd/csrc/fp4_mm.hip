@@ -79,11 +79,13 @@ struct RowsArgs {
     int64_t ldo;
     int dto, tile0; // first tile of rows of this launch
     int tiles;      // tiles of rows of this launch
-    Fp4Up up;       // the sparse layer's
+    const uint8_t *q2; // BOTH: the up weights, of w's sizes
+    const uint16_t *scale2;
 };
 
-// UP: the results are the sparse layer's gates, and out its a (see Fp4Up).
-template <int G, int NB, int XR, int WV, int NST, bool UP>
+// BOTH: of the NB sets of 16 rows every other one is of the sparse layer's up
+// weights, the same neurons as the gates before it, and out is its a.
+template <int G, int NB, int XR, int WV, int NST, bool BOTH>
 __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
 {
     constexpr int STG = NB * 1024 + XR * 256, NG = FP4_BLK / G, MF = G / 32, LPF = NB + XR / 4;
@@ -93,21 +95,22 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
     static_assert(XR % 4 == 0 && (NST - 1) * LPF < 64 && (NST & (NST - 1)) == 0, "stages");
     __shared__ __attribute__((aligned(16))) uint8_t L[BUF];
     __shared__ __attribute__((aligned(8))) uint16_t ss[SCB * NG][16 * NB];
-    __shared__ __attribute__((aligned(16))) float gate[UP ? 16 : 1][16 * NB];
     const int lane = threadIdx.x & 63, w = wave_id();
     const int l16 = lane & 15, q4 = lane >> 4;
     const int tile = (int)(blockIdx.x % (uint32_t)a.tiles), mt = (int)(blockIdx.x / (uint32_t)a.tiles);
-    const int n0 = (a.tile0 + tile) * (16 * NB);
+    constexpr int SETS = BOTH ? NB / 2 : NB; // of 16 neurons
+    const int n0 = (a.tile0 + tile) * (16 * SETS);
     const int tpt = a.planes == 3 ? 5 : 16; // tokens of a tile
     const int m0 = mt * tpt, c0 = m0 * a.planes;
     // W: lane l loads chunk l % 4 of row l / 4, as the swizzle places it; x: chunk
     // l % 16 of row 4 j + l / 16. Rows past an operand read its last row.
     const uint8_t *srcw = a.w.q + (int64_t)n0 * a.w.pitch, *srcx = a.x + (int64_t)c0 * a.xrow;
+    const uint8_t *srcu = BOTH ? a.q2 + (int64_t)n0 * a.w.pitch : nullptr;
     uint32_t off[LPF];
 #pragma unroll
     for (int i = 0; i < LPF; ++i) {
         if (i < NB) {
-            const int r = i * 16 + lane / 4;
+            const int r = (BOTH ? i / 2 : i) * 16 + lane / 4;
             off[i] = (uint32_t)min(r, a.w.rows - 1 - n0) * (uint32_t)a.w.pitch +
                      (((lane & 3) ^ (r >> 2 & 3)) << 4);
         } else {
@@ -120,7 +123,8 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
     auto fetch = [&](int kb, int st) {
 #pragma unroll
         for (int i = 0; i < LPF; ++i)
-            ng::dma16(i < NB ? srcw + (int64_t)kb * FP4_BYTES : srcx + (int64_t)kb * FP4_BLK * 2,
+            ng::dma16(i < NB ? (BOTH && (i & 1) ? srcu : srcw) + (int64_t)kb * FP4_BYTES
+                             : srcx + (int64_t)kb * FP4_BLK * 2,
                       off[i], lds0 + (uint32_t)(st * STG + i * 1024), kb, a.w.nkb);
     };
     floatx4_t acc[NB];
@@ -143,14 +147,16 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
             __syncthreads(); // the last scales are used
         for (int q = threadIdx.x; q < nk * NG * 4 * NB; q += 64 * WV) {
             const int g = q / (4 * NB), r = q % (4 * NB) * 4;
-            const uint16_t *p = a.w.scale + ((int64_t)k0 * NG + g) * a.w.rows;
-            if (n0 + r + 4 <= a.w.rows) {
-                const bytes8 v = *(const bytes8 *)(p + n0 + r);
+            const int i = r / 16, n = n0 + (BOTH ? i / 2 * 16 + r % 16 : r); // set, neuron
+            const uint16_t *p = (BOTH && (i & 1) ? a.scale2 : a.w.scale) +
+                                ((int64_t)k0 * NG + g) * a.w.rows;
+            if (n + 4 <= a.w.rows) {
+                const bytes8 v = *(const bytes8 *)(p + n);
                 *(uint2 *)&ss[g][r] = make_uint2(v.x, v.y);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    ss[g][r + e] = p[min(n0 + r + e, a.w.rows - 1)];
+                    ss[g][r + e] = p[min(n + e, a.w.rows - 1)];
             }
         }
         __syncthreads();
@@ -160,9 +166,12 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
             ng::wait_vm_steps<LPF, NST - 1>(min(n - 1 - i, NST - 1));
             asm volatile("" ::: "memory");
             const uint8_t *S = Lw + (i & (NST - 1)) * STG, *X = S + NB * 1024 + xr * 256;
+            // all of the block's reads, then its products
+            uint32_t wq[NB][4];
+            bf16x8_t xf[4];
+            uint2 sc[NB][NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                uint32_t wq[NB][MF];
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const int o = g * (G / 2) + q4 * (G / 8);
@@ -173,31 +182,38 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
                         wq[b][0] = u.x, wq[b][1] = u.y, wq[b][2] = u.z, wq[b][3] = u.w;
                     } else if constexpr (MF == 2) {
                         const uint2 u = *(const uint2 *)p;
-                        wq[b][0] = u.x, wq[b][1] = u.y;
+                        wq[b][2 * g] = u.x, wq[b][2 * g + 1] = u.y;
                     } else {
-                        wq[b][0] = *(const uint32_t *)p;
+                        wq[b][g] = *(const uint32_t *)p;
                     }
+                    sc[b][g] = *(const uint2 *)&ss[kc * NG + g][b * 16 + q4 * 4];
                 }
-                bf16x8_t xf[MF];
 #pragma unroll
                 for (int i = 0; i < MF; ++i) {
                     const int c = g * (G / 8) + q4 * MF + i;
-                    xf[i] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(X + ((c ^ xr) << 4)));
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    floatx4_t d = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < MF; ++i)
-                        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8_to_bf16(wq[b][i]), xf[i],
-                                                                    d, 0, 0, 0);
-                    const uint2 s = *(const uint2 *)&ss[kc * NG + g][b * 16 + q4 * 4];
-                    acc[b][0] = fmaf(d[0], bf16_lo(s.x), acc[b][0]);
-                    acc[b][1] = fmaf(d[1], bf16_hi(s.x), acc[b][1]);
-                    acc[b][2] = fmaf(d[2], bf16_lo(s.y), acc[b][2]);
-                    acc[b][3] = fmaf(d[3], bf16_hi(s.y), acc[b][3]);
+                    xf[g * MF + i] = __builtin_bit_cast(bf16x8_t, *(const uint4 *)(X + ((c ^ xr) << 4)));
                 }
             }
+            floatx4_t d[NB][NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    d[b][g] = floatx4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = g * MF; i < (g + 1) * MF; ++i)
+                        d[b][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4x8_to_bf16(wq[b][i]),
+                                                                          xf[i], d[b][g], 0, 0, 0);
+                }
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    acc[b][0] = fmaf(d[b][g][0], bf16_lo(sc[b][g].x), acc[b][0]);
+                    acc[b][1] = fmaf(d[b][g][1], bf16_hi(sc[b][g].x), acc[b][1]);
+                    acc[b][2] = fmaf(d[b][g][2], bf16_lo(sc[b][g].y), acc[b][2]);
+                    acc[b][3] = fmaf(d[b][g][3], bf16_hi(sc[b][g].y), acc[b][3]);
+                }
             // the reads are done before the piece is loaded again
             __builtin_amdgcn_s_waitcnt(0xC07F);
             asm volatile("" ::: "memory");
@@ -209,64 +225,79 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
     for (int b = 0; b < NB; ++b)
         part[w][b][lane] = acc[b];
     __syncthreads();
-    for (int b = w; b < NB; b += WV) { // joined in wave order
+    // joined in wave order
+    const bool three = a.planes == 3;
+    auto sum = [&](int b) {
         floatx4_t o = part[0][b][lane];
 #pragma unroll
         for (int u = 1; u < WV; ++u)
             o += part[u][b][lane];
-        int m = m0 + l16;
-        bool mine = l16 < 16;
-        if (a.planes == 3) { // a token's three columns: the smallest two first
+        if (three) // a token's three columns: the smallest two first
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float mid = __shfl(o[e], lane + 1, 64), lo = __shfl(o[e], lane + 2, 64);
                 o[e] += mid + lo;
             }
-            m = m0 + l16 / 3;
-            mine = l16 % 3 == 0 && l16 < 15;
+        return o;
+    };
+    const int m = m0 + (three ? l16 / 3 : l16);
+    const bool mine = (!three || (l16 % 3 == 0 && l16 < 15)) && m < a.T;
+    for (int b = w; b < SETS; b += WV) {
+        floatx4_t o = sum(BOTH ? 2 * b : b);
+        if constexpr (BOTH) {
+            const floatx4_t u = sum(2 * b + 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = fp4_act(o[e], u[e]);
         }
-        if (UP)
-            *(floatx4_t *)&gate[l16][b * 16 + q4 * 4] = o;
-        else if (mine && m < a.T)
+        if (mine)
             store4(a.out, a.dto, a.ldo, m, n0 + b * 16 + q4 * 4, a.w.rows, o);
-    }
-    if constexpr (UP) { // out is a: g u where g's gate is open, CLOSED elsewhere
-        __syncthreads();
-        constexpr int PER = 64 / (16 * NB) > 0 ? 64 / (16 * NB) : 1; // columns of a set of 64
-        static_assert(16 * NB * PER == 64 || NB == 4, "a wave's set");
-        for (int c = w * PER; c < tpt && m0 + c < a.T; c += WV * PER) {
-            // lane l: neuron l % (16 NB) of the token at column c + l / (16 NB)
-            const int tc = c + lane / (16 * NB), i = lane % (16 * NB);
-            const int t = m0 + tc, n = n0 + i;
-            const bool real = tc < tpt && t < a.T && n < a.w.rows;
-            const float g = real ? gate[a.planes == 3 ? 3 * tc : tc][i] : 0.f;
-            const float v = fp4_up(a.up, g, t, n);
-            if (real)
-                ((float *)a.out)[t * a.ldo + n] = v;
-        }
     }
 }
 
-template <int G, int NB, int XR, int NST, bool UP> void rows_one(RowsArgs a, hipStream_t s)
+template <int G, int NB, int XR, int WV, int NST, bool BOTH> void rows_one(RowsArgs a, hipStream_t s)
 {
-    const int tiles = (int)(((int64_t)a.w.rows + 16 * NB - 1) / (16 * NB));
+    constexpr int NR = 16 * (BOTH ? NB / 2 : NB);
+    const int tiles = (int)(((int64_t)a.w.rows + NR - 1) / NR);
     const int tpt = a.planes == 3 ? 5 : 16;
     const uint32_t mt = (uint32_t)((a.T + tpt - 1) / tpt);
     const int most = (1 << 22) / (int)mt; // threads of a launch are numbered in 32 bits
     for (a.tile0 = 0; a.tile0 < tiles; a.tile0 += a.tiles) {
         a.tiles = tiles - a.tile0 < most ? tiles - a.tile0 : most;
-        fp4_rows_kernel<G, NB, XR, 8, NST, UP><<<mt * (uint32_t)a.tiles, 64 * 8, 0, s>>>(a);
+        fp4_rows_kernel<G, NB, XR, WV, NST, BOTH><<<mt * (uint32_t)a.tiles, 64 * WV, 0, s>>>(a);
     }
 }
-template <int G, bool UP> void rows_group(const RowsArgs &a, hipStream_t s)
+// Sets of 16 rows and waves of a workgroup. One set and eight waves, which share
+// the contraction, while that gives no more than a workgroup a CU; two sets past
+// that (1 x 6144 over 2304: 4.2 against 4.6 us; 1 x 4096 over 4096: 5.0 against 4.2),
+// and with two workgroups a CU of these, four waves, so that one begins while
+// another ends (1 x 32768 over 4096: 13.8 against 14.3). Sixteen columns of
+// activations take four times the loads of a set: four sets share them there
+// (16 x 32768 over 4096: 14.9 against 16.0; one set 28.8).
+template <int G, int XR> void rows_x(const RowsArgs &a, hipStream_t s)
 {
     const bool wide = a.w.rows >= 16384;
+    if (a.q2) {
+        if (XR == 16 && wide)
+            rows_one<G, 4, XR, 4, 2, true>(a, s);
+        else
+            rows_one<G, 2, XR, 4, 2, true>(a, s);
+    } else if (wide) {
+        rows_one<G, XR == 16 ? 4 : 2, XR, 4, 2, false>(a, s);
+    } else if (a.w.rows > 16 * 256) {
+        rows_one<G, 2, XR, 8, 2, false>(a, s);
+    } else {
+        rows_one<G, 1, XR, 8, 2, false>(a, s);
+    }
+}
+template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
+{
     if (a.R <= 4)
-        wide ? rows_one<G, 2, 4, 4, UP>(a, s) : rows_one<G, 1, 4, 4, UP>(a, s);
+        rows_x<G, 4>(a, s);
     else if (a.R <= 8)
-        wide ? rows_one<G, 4, 8, 2, UP>(a, s) : rows_one<G, 2, 8, 2, UP>(a, s);
+        rows_x<G, 8>(a, s);
     else
-        wide ? rows_one<G, 4, 16, 2, UP>(a, s) : rows_one<G, 2, 16, 2, UP>(a, s);
+        rows_x<G, 16>(a, s);
 }
 
 // ---------------------------------------------------------------- dY W, few tokens
@@ -535,6 +566,9 @@ struct TileArgs {
     float *part; // split contraction: [parts][T][ldo of a part]
     int64_t ldp;
     int parts, per; // parts, blocks of 128 k in each
+    // a second matrix of w's sizes, its rows after w's (whole tiles), or NULL
+    const uint8_t *q2;
+    const uint16_t *scale2;
 };
 
 // PL: rows of a token's activations.
@@ -548,7 +582,8 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
     constexpr int GM = 8;
     constexpr bool three = PL == 3;
     constexpr int tpt = three ? C::BM / 16 * 5 : C::BM; // tokens of a tile
-    const int nt = (a.w.rows + C::BN - 1) / C::BN, mt = (a.x.T + tpt - 1) / tpt;
+    const int N = a.q2 ? 2 * a.w.rows : a.w.rows;
+    const int nt = (N + C::BN - 1) / C::BN, mt = (a.x.T + tpt - 1) / tpt;
     const int64_t total = (int64_t)nt * mt * a.parts, each = (total + NXCD - 1) / NXCD;
     const int64_t at = blockIdx.x / NXCD, q0 = blockIdx.x % NXCD * each + at;
     if (at >= each || q0 >= total)
@@ -564,7 +599,11 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
     // Rows past an operand read its last row; their results are dropped. Of
     // float32 activations a fragment holds five tokens, three rows each.
     const int64_t xrow = three ? a.x.plane : a.x.pitch;
-    const uint8_t *srcx = a.x.data + (int64_t)m0 * a.x.pitch, *srcw = a.w.q + (int64_t)n0 * a.w.pitch;
+    const uint8_t *srcx = a.x.data + (int64_t)m0 * a.x.pitch, *srcw;
+    const bool second = n0 >= a.w.rows;
+    const int nw0 = second ? n0 - a.w.rows : n0; // row of its matrix
+    const uint16_t *scale = second ? a.scale2 : a.w.scale;
+    srcw = (second ? a.q2 : a.w.q) + (int64_t)nw0 * a.w.pitch;
     uint32_t off[C::WB];
 #pragma unroll
     for (int g = 0; g < C::WB; ++g) {
@@ -575,7 +614,7 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
             off[g] = (uint32_t)min(x, last) * (uint32_t)xrow + (((lane % C::CA) ^ C::swa(r)) << 4);
         } else {
             const int r = (w * C::WBB + g - C::WBA) * (64 / C::CW) + lane / C::CW;
-            off[g] = (uint32_t)min(r, a.w.rows - 1 - n0) * (uint32_t)a.w.pitch +
+            off[g] = (uint32_t)min(r, a.w.rows - 1 - nw0) * (uint32_t)a.w.pitch +
                      (((lane % C::CW) ^ C::sww(r)) << 4);
         }
     }
@@ -624,8 +663,8 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
         }
         for (int i = threadIdx.x; i < nb * (FP4_BLK / G) * C::BN; i += C::NT) {
             const int g = i / C::BN, r = i % C::BN;
-            ss[g][r] = a.w.scale[((int64_t)c0 * (FP4_BLK / G) + g) * a.w.rows +
-                                 min(n0 + r, a.w.rows - 1)];
+            ss[g][r] = scale[((int64_t)c0 * (FP4_BLK / G) + g) * a.w.rows +
+                             min(nw0 + r, a.w.rows - 1)];
         }
         ng::wait_vm<0>();
         __syncthreads();
@@ -749,13 +788,13 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                     const int m = mw + j * (three ? 5 : 16) + r0 + rr;
                     const uint4 v = *(const uint4 *)(buf + (r0 + rr) * C::OROW + c8 * 16);
                     T *row = (T *)out + m * ld;
-                    if (m < a.x.T && c + VPL <= a.w.rows) {
+                    if (m < a.x.T && c + VPL <= N) {
                         stg16u_nt(row + c, v);
                     } else if (m < a.x.T) {
                         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int e = 0; e < VPL; ++e)
-                            if (c + e < a.w.rows)
+                            if (c + e < N)
                                 row[c + e] = (T)(u[e * ES / 4] >> (8 * ES * e % 32));
                     }
                 }
@@ -776,7 +815,8 @@ using T256 = TileCfg<256, 256, 2, 4, 3, 64, 64>; // waves of 128 x 64
 template <int G, class C> void tile_one(const TileArgs &a, hipStream_t s)
 {
     const int tpt = a.x.planes == 3 ? C::BM / 16 * 5 : C::BM;
-    const int64_t tiles = (int64_t)((a.w.rows + C::BN - 1) / C::BN) * ((a.x.T + tpt - 1) / tpt) *
+    const int64_t N = (int64_t)a.w.rows * (a.q2 ? 2 : 1);
+    const int64_t tiles = (N + C::BN - 1) / C::BN * ((a.x.T + tpt - 1) / tpt) *
                           a.parts;
     const uint32_t grid = (uint32_t)((tiles + NXCD - 1) / NXCD * NXCD);
     if (a.x.planes == 3)
@@ -813,7 +853,7 @@ struct TilePlan {
     TileKind k;
     int parts, per;
 };
-TilePlan tile_plan(int T, int N, int nkb, int planes)
+TilePlan tile_plan(int T, int N, int nkb, int planes, int widest = 256) // rows of a tile
 {
     TilePlan best = {TILE_64, 1, nkb};
     double least = 1e300;
@@ -825,7 +865,7 @@ TilePlan tile_plan(int T, int N, int nkb, int planes)
     } kinds[] = {{TILE_64, 64, 128, 0.75, 1.1, 2.5}, {TILE_128, 128, 128, 1.1, 1.95, 3.0},
                  {TILE_256, 256, 256, 2.7, 5.4, 5.0}};
     for (const auto &c : kinds)
-        for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
+        for (int parts = 1; c.bn <= widest && parts <= 32 && parts <= nkb; parts *= 2) {
             const double wg = up(T, planes == 3 ? c.bm / 16 * 5 : c.bm) * up(N, c.bn) * parts;
             const double n = up(wg, 256), k = up(nkb, parts);
             const double t = floor(n / 2) * (k * c.pair + c.ends) +
@@ -918,17 +958,17 @@ int planes_of(const twell_mat_t *x) { return x->dtype == TWELL_BF16 ? 1 : 3; }
 
 void fp4_dequant(const Fp4 &w, void *out, int64_t ld, int dt, int rows, int cols, hipStream_t s);
 
-void fp4_rows(const Acts &x, const Fp4 &w, void *out, int64_t ldo, int dto, const Fp4Up *up,
+void fp4_rows(const Acts &x, const Fp4 &w, const Fp4 *up, void *out, int64_t ldo, int dto,
               hipStream_t s)
 {
     const RowsArgs a = {x.data, x.planes == 3 ? x.plane : x.pitch, x.T, x.planes, x.T * x.planes,
-                        w, out, ldo, dto, 0, 0, up ? *up : Fp4Up{}};
+                        w, out, ldo, dto, 0, 0, up ? up->q : nullptr, up ? up->scale : nullptr};
     if (w.group == 32)
-        up ? rows_group<32, true>(a, s) : rows_group<32, false>(a, s);
+        rows_group<32>(a, s);
     else if (w.group == 64)
-        up ? rows_group<64, true>(a, s) : rows_group<64, false>(a, s);
+        rows_group<64>(a, s);
     else
-        up ? rows_group<128, true>(a, s) : rows_group<128, false>(a, s);
+        rows_group<128>(a, s);
 }
 
 // Workspace: the packed activations, then the parts' sums or the weights' values.
@@ -961,12 +1001,12 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
     const int dto = out->dtype;
     const bool little = few(a.T, planes_of(x), dx);
     if (!dx && little) {
-        fp4_rows(a, w, out->data, out->ld, dto, nullptr, s);
+        fp4_rows(a, w, nullptr, out->data, out->ld, dto, s);
         tm.mark("fp4_rows");
     } else if (!dx) {
         const TilePlan p = tile_plan(a.T, w.rows, w.nkb, planes_of(x));
         const TileArgs t = {a, w, out->data, out->ld, dto, (float *)ws2, part_pitch(w.rows),
-                            p.parts, p.per};
+                            p.parts, p.per, nullptr, nullptr};
         tiles(t, p.k, s);
         tm.mark("fp4_tile");
         if (p.parts > 1) {
@@ -993,15 +1033,16 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
     return hipGetLastError() == hipSuccess ? TWELL_OK : TWELL_E_HIP;
 }
 
-int fp4_gate_parts(const twell_mat_t *x, int d_ff)
+int fp4_gates_parts(const twell_mat_t *x, int d_ff)
 {
     const int planes = planes_of(x);
     return few(x->rows, planes, false)
-               ? 0 : tile_plan(x->rows, d_ff, fp4_blocks(x->cols), planes).parts;
+               ? 0 : tile_plan(x->rows, 2 * d_ff, fp4_blocks(x->cols), planes, 128).parts;
 }
 
-void fp4_gate(const Acts &x, const Fp4 &w, float *parts, hipStream_t s)
+void fp4_gates(const Acts &x, const Fp4 &wg, const Fp4 &wu, float *parts, hipStream_t s)
 {
-    const TilePlan p = tile_plan(x.T, w.rows, w.nkb, x.planes);
-    tiles({x, w, parts, w.rows, TWELL_F32, parts, w.rows, p.parts, p.per}, p.k, s);
+    const TilePlan p = tile_plan(x.T, 2 * wg.rows, wg.nkb, x.planes, 128);
+    const int64_t ld = 2 * (int64_t)wg.rows;
+    tiles({x, wg, parts, ld, TWELL_F32, parts, ld, p.parts, p.per, wu.q, wu.scale}, p.k, s);
 }

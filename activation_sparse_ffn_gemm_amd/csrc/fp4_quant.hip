@@ -88,7 +88,7 @@ inline uint32_t groups(int64_t tiles) { return (uint32_t)(tiles < 1 << 22 ? tile
 // A workgroup takes QR rows by QB blocks of columns; 16 lanes hold a block of a
 // row, eight elements each. The scales of the QR rows, which are neighbours in
 // memory, meet in LDS and are written as runs.
-constexpr int QR = 32, QB = 4;
+constexpr int QR = 8, QB = 4;
 template <int G> __global__ __launch_bounds__(256) void fp4_quant_kernel(QuantArgs a)
 {
     constexpr int NG = FP4_BLK / G; // groups of a block
@@ -100,19 +100,22 @@ template <int G> __global__ __launch_bounds__(256) void fp4_quant_kernel(QuantAr
         const int b0 = (int)(tile % nbt) * QB, b = b0 + cb, j = b * FP4_BLK + l16 * 8;
         const int64_t r0 = tile / nbt * QR;
         if (b < a.nkb) {
+            float v[QR / STEP][8]; // (rows past the matrix read its last one)
+#pragma unroll
+            for (int i = 0; i < QR / STEP; ++i)
+                load8(row_ptr(a.x, a.dt, a.ld, min(r0 + i * STEP + rr, (int64_t)a.R - 1)), a.dt, j,
+                      a.C, v[i]);
 #pragma unroll
             for (int i = 0; i < QR / STEP; ++i) {
                 const int64_t r = r0 + i * STEP + rr;
-                if (r >= a.R)
-                    break;
-                float v[8];
-                load8(row_ptr(a.x, a.dt, a.ld, r), a.dt, j, a.C, v);
                 uint32_t m = 0;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+                    m = max(m, __float_as_uint(v[i][e]) & 0x7fffffffu);
                 const GroupScale g = fp4_scale(lanes_umax<G / 8>(m));
-                *(uint32_t *)(a.q + r * a.pitch + b * FP4_BYTES + l16 * 4) = quant8_fp4(v, g);
+                if (r >= a.R)
+                    continue;
+                *(uint32_t *)(a.q + r * a.pitch + b * FP4_BYTES + l16 * 4) = quant8_fp4(v[i], g);
                 if (l16 % (G / 8) == 0)
                     ss[cb * NG + l16 / (G / 8)][i * STEP + rr] = g.held;
             }
@@ -133,60 +136,61 @@ struct DequantArgs {
     Fp4 w;
     void *out;
     int64_t ld;
-    int dt, rows, cols;
+    int rows, cols;
     int64_t tiles;
 };
-// One thread takes eight columns of DR rows.
-constexpr int DR = 4;
-__global__ __launch_bounds__(256) void fp4_dequant_kernel(DequantArgs a)
+// One thread takes 16 bytes of results of each of DR rows: eight bfloat16 or four
+// float32 columns.
+constexpr int DR = 8;
+template <class T> __global__ __launch_bounds__(256) void fp4_dequant_kernel(DequantArgs a)
 {
-    const int c8 = (a.cols + 7) / 8, nct = (c8 + 255) / 256;
+    constexpr int N = 16 / sizeof(T);
+    const int cn = (a.cols + N - 1) / N, nct = (cn + 255) / 256;
+    const int shift = 31 - __builtin_clz(a.w.group);
     for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        const int c = (int)(tile % nct) * 256 + threadIdx.x;
+        const int j = ((int)(tile % nct) * 256 + threadIdx.x) * N;
         const int64_t r0 = tile / nct * DR;
-        if (c >= c8)
+        if (j >= a.cols)
             continue;
-        const int j = c * 8;
-        const uint16_t *sc = a.w.scale + (int64_t)(j / a.w.group) * a.w.rows;
+        const bool in = j / 2 < a.w.pitch;
+        const uint16_t *sc = a.w.scale + (int64_t)(in ? j >> shift : 0) * a.w.rows;
+        const uint8_t *q = a.w.q + (in ? j / 2 : 0);
+        uint32_t code[DR];
+        uint16_t s[DR];
+#pragma unroll
+        for (int i = 0; i < DR; ++i) {
+            const int64_t r = min(r0 + i, (int64_t)a.w.rows - 1);
+            code[i] = N == 8 ? *(const uint32_t *)(q + r * a.w.pitch)
+                             : *(const uint16_t *)(q + r * a.w.pitch);
+            s[i] = sc[r];
+        }
 #pragma unroll
         for (int i = 0; i < DR; ++i) {
             const int64_t r = r0 + i;
             if (r >= a.rows)
                 break;
-            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (r < a.w.rows && c * 4 < a.w.pitch) {
-                fp4x8_to_f32(*(const uint32_t *)(a.w.q + r * a.w.pitch + c * 4), v);
-                const float s = bf16_to_f32(sc[r]);
+            float v[8];
+            fp4x8_to_f32(code[i], v);
+            const bool real = in && r < a.w.rows;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] *= s;
-            }
-            if (a.dt == TWELL_BF16) {
-                uint16_t *p = (uint16_t *)a.out + r * a.ld + j;
-                const uint4 u = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
-                                           f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
-                if (j + 8 <= a.cols) {
-                    stg16u(p, u);
-                } else {
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (j + e < a.cols)
-                            p[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-                }
+            for (int e = 0; e < N; ++e)
+                v[e] = real ? v[e] * bf16_to_f32(s[i]) : 0.f;
+            uint4 u;
+            if constexpr (N == 8)
+                u = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
+                               f32x2_to_bf16x2(v[4], v[5]), f32x2_to_bf16x2(v[6], v[7]));
+            else
+                u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
+                               __float_as_uint(v[2]), __float_as_uint(v[3]));
+            T *p = (T *)a.out + r * a.ld + j;
+            if (j + N <= a.cols) {
+                stg16u_nt(p, u);
             } else {
-                float *p = (float *)a.out + r * a.ld + j;
-                if (j + 8 <= a.cols) {
-                    stg16u(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
-                                         __float_as_uint(v[2]), __float_as_uint(v[3])));
-                    stg16u(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]),
-                                             __float_as_uint(v[6]), __float_as_uint(v[7])));
-                } else {
+                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (j + e < a.cols)
-                            p[e] = v[e];
-                }
+                for (int e = 0; e < N - 1; ++e)
+                    if (j + e < a.cols)
+                        p[e] = (T)(w[e * sizeof(T) / 4] >> (8 * sizeof(T) * e % 32));
             }
         }
     }
@@ -265,24 +269,27 @@ hipError_t launch_fp4_quant(const twell_mat_t *x, const twell_fp4_t *o, twell_ti
     QuantArgs a = {x->data, x->ld, x->dtype, x->rows, x->cols, fp4_blocks(x->cols),
                    o->q, o->scale, fp4_pitch(x->cols), 0};
     a.tiles = (int64_t)((a.nkb + QB - 1) / QB) * ((a.R + QR - 1) / QR);
-    const dim3 grid(groups(a.tiles));
     if (o->group == 32)
-        fp4_quant_kernel<32><<<grid, 256, 0, s>>>(a);
+        fp4_quant_kernel<32><<<groups(a.tiles), 256, 0, s>>>(a);
     else if (o->group == 64)
-        fp4_quant_kernel<64><<<grid, 256, 0, s>>>(a);
+        fp4_quant_kernel<64><<<groups(a.tiles), 256, 0, s>>>(a);
     else
-        fp4_quant_kernel<128><<<grid, 256, 0, s>>>(a);
+        fp4_quant_kernel<128><<<groups(a.tiles), 256, 0, s>>>(a);
     tm.mark("fp4_quant");
     return hipGetLastError();
 }
 
 void fp4_dequant(const Fp4 &w, void *out, int64_t ld, int dt, int rows, int cols, hipStream_t s)
 {
-    const int64_t tiles = (int64_t)(((cols + 7) / 8 + 255) / 256) * ((rows + DR - 1) / DR);
+    const int n = dt == TWELL_BF16 ? 8 : 4;
+    const int64_t tiles = (int64_t)(((cols + n - 1) / n + 255) / 256) * ((rows + DR - 1) / DR);
     if (tiles == 0)
         return;
-    const DequantArgs a = {w, out, ld, dt, rows, cols, tiles};
-    fp4_dequant_kernel<<<groups(tiles), 256, 0, s>>>(a);
+    const DequantArgs a = {w, out, ld, rows, cols, tiles};
+    if (dt == TWELL_BF16)
+        fp4_dequant_kernel<uint16_t><<<groups(tiles), 256, 0, s>>>(a);
+    else
+        fp4_dequant_kernel<uint32_t><<<groups(tiles), 256, 0, s>>>(a);
 }
 
 hipError_t launch_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing_t *timing,
