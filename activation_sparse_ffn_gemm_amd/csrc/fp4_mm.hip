@@ -524,6 +524,40 @@ int cols_parts(int N, int nkb, int *per)
     return *per ? (N + *per - 1) / *per : 1;
 }
 
+// Which tiles, and in how many parts of the contraction: the least of the times
+// that measured figures give (us; they order the choices, no more). A step of
+// 128 takes `step` alone on its CU and `pair` beside another workgroup (both of
+// them), a tile `ends` more for its beginning and end; parts add a launch and
+// the partial sums' way through memory.
+enum TileKind { TILE_64, TILE_128, TILE_256 };
+struct TileTime {
+    int bm, bn; // by TileKind
+    double step, pair, ends;
+};
+struct TilePlan {
+    TileKind k;
+    int parts, per;
+};
+TilePlan tile_plan(const TileTime *kinds, int n_kinds, double T, double N, int nkb, int rounds)
+{
+    TilePlan best = {TILE_64, 1, nkb};
+    double least = 1e300;
+    auto up = [](double a, double b) { return ceil(a / b); };
+    for (int i = 0; i < n_kinds; ++i)
+        for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
+            const TileTime &c = kinds[i];
+            const double n = up(up(T, c.bm) * up(N, c.bn) * parts, 256), pairs = floor(n / 2);
+            const double k = up(nkb, parts) * rounds;
+            const double t = pairs * (k * c.pair + c.ends) + (n - 2 * pairs) * (k * c.step + c.ends) +
+                             (parts == 1 ? 0. : 3.0 + parts * T * N * 8 / 4e6);
+            if (t < least)
+                least = t, best = {(TileKind)i, parts, (nkb + parts - 1) / parts};
+        }
+    best.parts = best.per ? (nkb + best.per - 1) / best.per : 1;
+    return best;
+}
+int64_t part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
+
 // ---------------------------------------------------------------- X W^T, many tokens
 // A workgroup computes BM tokens x BN rows of W. A step is 64 k: the tokens' 128
 // bytes and W's 32 go straight from global memory to LDS, NST steps resident,
@@ -824,7 +858,6 @@ template <int G, class C> void tile_one(const TileArgs &a, hipStream_t s)
     else
         fp4_tile_kernel<G, C, 1><<<grid, C::NT, 0, s>>>(a);
 }
-enum TileKind { TILE_64, TILE_128, TILE_256 };
 template <int G> void tile_group(const TileArgs &a, TileKind k, hipStream_t s)
 {
     if (k == TILE_256)
@@ -844,40 +877,14 @@ void tiles(const TileArgs &a, TileKind k, hipStream_t s)
         tile_group<128>(a, k, s);
 }
 
-// Which tiles, and in how many parts of the contraction: the least of the times
-// that these measured figures give (us; they order the choices, no more). A
-// step of 128 k takes `step` alone on its CU and `pair` beside another
-// workgroup (both of them), a tile `ends` more for its beginning and end; parts
-// add a launch and the partial sums' way through memory.
-struct TilePlan {
-    TileKind k;
-    int parts, per;
-};
-TilePlan tile_plan(int T, int N, int nkb, int planes, int widest = 256) // rows of a tile
+// Tiles of X W^T. A float32 token takes 3.2 rows of a tile.
+TilePlan fwd_plan(int T, int N, int nkb, int planes, bool both = false)
 {
-    TilePlan best = {TILE_64, 1, nkb};
-    double least = 1e300;
-    auto up = [](double a, double b) { return ceil(a / b); };
-    const struct {
-        TileKind k;
-        int bm, bn;
-        double step, pair, ends;
-    } kinds[] = {{TILE_64, 64, 128, 0.75, 1.1, 2.5}, {TILE_128, 128, 128, 1.1, 1.95, 3.0},
-                 {TILE_256, 256, 256, 2.7, 5.4, 5.0}};
-    for (const auto &c : kinds)
-        for (int parts = 1; c.bn <= widest && parts <= 32 && parts <= nkb; parts *= 2) {
-            const double wg = up(T, planes == 3 ? c.bm / 16 * 5 : c.bm) * up(N, c.bn) * parts;
-            const double n = up(wg, 256), k = up(nkb, parts);
-            const double t = floor(n / 2) * (k * c.pair + c.ends) +
-                             (n - 2 * floor(n / 2)) * (k * c.step + c.ends) +
-                             (parts == 1 ? 0. : 3.0 + (double)parts * T * N * 8 / 4e6);
-            if (t < least)
-                least = t, best = {c.k, parts, (nkb + parts - 1) / parts};
-        }
-    best.parts = best.per ? (nkb + best.per - 1) / best.per : 1;
-    return best;
+    static const TileTime kinds[] = {{64, 128, 0.75, 1.1, 2.5}, {128, 128, 1.1, 1.95, 3.0},
+                                     {256, 256, 2.7, 5.4, 5.0}};
+    // (of two matrices one after the other 256 rows may be of both)
+    return tile_plan(kinds, both ? 2 : 3, planes == 3 ? T * 3.2 : T, N, nkb, 1);
 }
-int64_t part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
 
 // ---------------------------------------------------------------- dY W, many tokens
 // The values as bfloat16 in the workspace, then a dense product on the shared
@@ -891,6 +898,9 @@ struct GemmArgs {
     void *out;
     int64_t ldo;
     int dto;
+    float *part; // split contraction: [parts][T][ldp]
+    int64_t ldp;
+    int parts, per; // parts, blocks of 128 rows of w in each
 };
 
 template <class C> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(GemmArgs a)
@@ -898,14 +908,17 @@ template <class C> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(Gemm
     __shared__ __attribute__((aligned(16))) uint8_t L[C::LDS];
     constexpr int KS = C::ROWB / 2;
     const int nt = (a.N + C::BN - 1) / C::BN, mt = (a.x.T + C::BM - 1) / C::BM;
-    const int steps = a.x.nkb * (FP4_BLK / KS);
     const int lane = threadIdx.x & 63, wm = ng::wave_m<C>(), wn = ng::wave_n<C>();
-    for (int64_t q = blockIdx.x; q < (int64_t)nt * mt; q += gridDim.x) {
-        const int m0 = (int)(q % mt) * C::BM, n0 = (int)(q / mt) * C::BN;
+    for (int64_t q = blockIdx.x; q < (int64_t)nt * mt * a.parts; q += gridDim.x) {
+        const int part = (int)(q / ((int64_t)nt * mt));
+        const int64_t tile = q % ((int64_t)nt * mt);
+        const int m0 = (int)(tile % mt) * C::BM, n0 = (int)(tile / mt) * C::BN;
+        const int b0 = part * a.per, steps = (min(a.x.nkb, b0 + a.per) - b0) * (FP4_BLK / KS);
+        const int k0 = b0 * (FP4_BLK / KS);
         auto rowa = [&](int r) { return a.x.data + (int64_t)min(m0 + r, a.x.T - 1) * a.x.pitch; };
         auto rowb = [&](int r) { return a.w + (int64_t)r * a.wpitch + (int64_t)n0 * 2; };
         auto off = [&](int kt) {
-            const int p = kt / steps, k = kt % steps;
+            const int p = kt / steps, k = k0 + kt % steps;
             return ng::StepOff{
                 (size_t)((a.x.planes - 1 - p) * a.x.plane + (int64_t)k * C::ROWB),
                 (size_t)((int64_t)k * KS * a.wpitch)};
@@ -924,7 +937,9 @@ template <class C> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(Gemm
                     const int n = n0 + ng::acc_col<C>(wn, ni, lane);
                     if (m < a.x.T && n < a.N) {
                         const float v = acc.v[mi][ni][e];
-                        if (a.dto == TWELL_BF16)
+                        if (a.parts > 1)
+                            a.part[((int64_t)part * a.x.T + m) * a.ldp + n] = v;
+                        else if (a.dto == TWELL_BF16)
                             ((uint16_t *)a.out)[m * a.ldo + n] = (uint16_t)f32x2_to_bf16x2(v, 0.f);
                         else
                             ((float *)a.out)[m * a.ldo + n] = v;
@@ -933,18 +948,27 @@ template <class C> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(Gemm
     }
 }
 
-using C64 = ng::Cfg<64, 128, 2, 4, 4, 64>;
+using C64 = ng::Cfg<64, 128, 1, 4, 3, 128>;
+using C128 = ng::Cfg<128, 128, 2, 4, 2, 128>;
 using C256 = ng::Cfg<256, 256, 2, 4, 2, 128>;
 
+TilePlan dx_plan(int T, int N, int nkb, int planes)
+{
+    static const TileTime kinds[] = {{64, 128, 1.2, 2.2, 3.0}, {128, 128, 1.95, 2.5, 3.0},
+                                     {256, 256, 3.3, 6.6, 5.0}};
+    return tile_plan(kinds, 3, T, N, nkb, planes);
+}
 template <class C> void gemm_one(const GemmArgs &a, hipStream_t s)
 {
-    const int64_t tiles = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.x.T + C::BM - 1) / C::BM);
+    const int64_t tiles = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.x.T + C::BM - 1) / C::BM) * a.parts;
     fp4_gemm_kernel<C><<<(uint32_t)(tiles < 1 << 20 ? tiles : 1 << 20), C::NT, 0, s>>>(a);
 }
-void gemm(const GemmArgs &a, hipStream_t s)
+void gemm(const GemmArgs &a, TileKind k, hipStream_t s)
 {
-    if ((int64_t)((a.N + 255) / 256) * ((a.x.T + 255) / 256) >= 128)
+    if (k == TILE_256)
         gemm_one<C256>(a, s);
+    else if (k == TILE_128)
+        gemm_one<C128>(a, s);
     else
         gemm_one<C64>(a, s);
 }
@@ -979,9 +1003,12 @@ size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
         int per, parts = dx ? cols_parts(rows, fp4_blocks(cols), &per) : 1;
         return parts == 1 ? pack : up256(pack) + (size_t)parts * x->rows * pitch * 4;
     }
-    if (dx)
-        return up256(pack) + (size_t)fp4_blocks(rows) * FP4_BLK * pitch * 2;
-    const TilePlan p = tile_plan(x->rows, rows, fp4_blocks(cols), planes_of(x));
+    if (dx) {
+        const int parts = dx_plan(x->rows, cols, fp4_blocks(rows), planes_of(x)).parts;
+        return up256(pack) + (size_t)fp4_blocks(rows) * FP4_BLK * pitch * 2 +
+               (parts > 1 ? (size_t)parts * x->rows * part_pitch(cols) * 4 : 0);
+    }
+    const TilePlan p = fwd_plan(x->rows, rows, fp4_blocks(cols), planes_of(x));
     return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(rows) * 4;
 }
 
@@ -1004,7 +1031,7 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
         fp4_rows(a, w, nullptr, out->data, out->ld, dto, s);
         tm.mark("fp4_rows");
     } else if (!dx) {
-        const TilePlan p = tile_plan(a.T, w.rows, w.nkb, planes_of(x));
+        const TilePlan p = fwd_plan(a.T, w.rows, w.nkb, planes_of(x));
         const TileArgs t = {a, w, out->data, out->ld, dto, (float *)ws2, part_pitch(w.rows),
                             p.parts, p.per, nullptr, nullptr};
         tiles(t, p.k, s);
@@ -1027,8 +1054,15 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
         const int wc = w.nkb * FP4_BLK, rows = fp4_blocks(w.rows) * FP4_BLK;
         fp4_dequant(w, ws2, wc, TWELL_BF16, rows, wc, s);
         tm.mark("fp4_dequant");
-        gemm({a, ws2, (int64_t)wc * 2, w.cols, wc, out->data, out->ld, dto}, s);
+        const TilePlan p = dx_plan(a.T, w.cols, a.nkb, planes_of(x));
+        const GemmArgs g = {a, ws2, (int64_t)wc * 2, w.cols, wc, out->data, out->ld, dto,
+                            (float *)(ws2 + (size_t)rows * wc * 2), part_pitch(w.cols), p.parts, p.per};
+        gemm(g, p.k, s);
         tm.mark("fp4_gemm");
+        if (g.parts > 1) {
+            join({g.part, g.parts, a.T, w.cols, g.ldp, out->data, out->ld, dto}, s);
+            tm.mark("fp4_join");
+        }
     }
     return hipGetLastError() == hipSuccess ? TWELL_OK : TWELL_E_HIP;
 }
@@ -1037,12 +1071,12 @@ int fp4_gates_parts(const twell_mat_t *x, int d_ff)
 {
     const int planes = planes_of(x);
     return few(x->rows, planes, false)
-               ? 0 : tile_plan(x->rows, 2 * d_ff, fp4_blocks(x->cols), planes, 128).parts;
+               ? 0 : fwd_plan(x->rows, 2 * d_ff, fp4_blocks(x->cols), planes, true).parts;
 }
 
 void fp4_gates(const Acts &x, const Fp4 &wg, const Fp4 &wu, float *parts, hipStream_t s)
 {
-    const TilePlan p = tile_plan(x.T, 2 * wg.rows, wg.nkb, x.planes, 128);
+    const TilePlan p = fwd_plan(x.T, 2 * wg.rows, wg.nkb, x.planes, true);
     const int64_t ld = 2 * (int64_t)wg.rows;
     tiles({x, wg, parts, ld, TWELL_F32, parts, ld, p.parts, p.per, wu.q, wu.scale}, p.k, s);
 }
