@@ -175,7 +175,8 @@ bool tiles_ok(int64_t rows, int64_t cols, int64_t tr, int64_t tc)
 bool fp4_sizes_ok(int32_t T, int32_t N, int32_t K, bool dx)
 {
     return T >= 0 && T <= TWELL_MAX_ROWS && N >= 0 && N <= TWELL_MAX_ROWS && K >= 0 &&
-           K <= TWELL_MAX_ROWS && (dx ? N : K) <= TWELL_FP4_MAX_K && tiles_ok(T, dx ? K : N, 16, 16);
+           K <= TWELL_MAX_ROWS && (dx ? N : K) <= TWELL_FP4_MAX_K &&
+           ((int64_t)T + 15) / 16 * (((int64_t)(dx ? K : N) + 127) / 128) <= 1 << 23;
 }
 
 // a matrix whose rows take the most workspace that any strides make them take

@@ -546,7 +546,10 @@ TilePlan tile_plan(const TileTime *kinds, int n_kinds, double T, double N, int n
     for (int i = 0; i < n_kinds; ++i)
         for (int parts = 1; parts <= 32 && parts <= nkb; parts *= 2) {
             const TileTime &c = kinds[i];
-            const double n = up(up(T, c.bm) * up(N, c.bn) * parts, 256), pairs = floor(n / 2);
+            const double tiles = up(T, c.bm) * up(N, c.bn);
+            if (parts > 1 && tiles >= 512)
+                break; // the chip is full
+            const double n = up(tiles * parts, 256), pairs = floor(n / 2);
             const double k = up(nkb, parts) * rounds;
             const double t = pairs * (k * c.pair + c.ends) + (n - 2 * pairs) * (k * c.step + c.ends) +
                              (parts == 1 ? 0. : 3.0 + parts * T * N * 8 / 4e6);

@@ -482,8 +482,9 @@ int twell_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing
  * out[t][n] = sum over k of x[t][k] w[n][k] for w in 4 bits: x [T][w.cols],
  * out [T][w.rows], each float32 or bfloat16 with rows any stride apart. Every
  * product is exact (float32 activations are taken as three bfloat16 numbers
- * that add up to them), sums are float32, out is rounded once. out must not
- * overlap x. w.cols <= TWELL_FP4_MAX_K.
+ * that add up to them; values up to 2^110 in size), sums are float32, out is
+ * rounded once. out must not overlap x. w.cols <= TWELL_FP4_MAX_K, and at most
+ * 2^23 pieces of 16 tokens by 128 results.
  *   workspace: twell_fp4_matmul_workspace_bytes(...) bytes are enough for any
  *   strides and alignment; a call that itself takes less asks for no more, 0
  *   (and workspace may be NULL) among others for few tokens of bfloat16, 16-byte
@@ -517,8 +518,8 @@ size_t twell_fp4_matmul_dx_workspace_bytes(twell_dtype dy_dtype, int32_t T, int3
  *   g = x wg_t^T,  u = x wu_t^T,  y = sum over neurons i with g_i > 0 of
  *   g_i u_i wd[i]
  * in float32 throughout (g and u are not rounded to a storage type; a NaN of g
- * counts as positive). wu_t's and wd's rows are read only where some gate is
- * open.
+ * counts as positive). wd's rows are read only where a gate is open; u is formed
+ * of every neuron unless few tokens meet more than 2^26 weights a matrix.
  *   x [T][d_model] float32 or bfloat16, 0 <= T <= TWELL_DECODE_T, rows any
  *   stride apart; wg_t, wu_t, wd [d_ff][d_model] of one group, d_model and d_ff
  *   within the layer's limits (d_model <= 4096); y [T][d_model] float32.
