@@ -614,7 +614,7 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
 {
     constexpr int NST = C::NST, MI = C::MI, NI = C::NI;
     __shared__ __attribute__((aligned(16))) uint8_t L[NST * C::STAGE];
-    __shared__ uint16_t ss[C::SG][C::BN];
+    __shared__ __attribute__((aligned(8))) uint16_t ss[C::SG][C::BN];
     // an XCD takes a run of tiles, eight rows of them at a time
     constexpr int GM = 8;
     constexpr bool three = PL == 3;
@@ -698,10 +698,30 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                 load(g, s);
             ++ls;
         }
-        for (int i = threadIdx.x; i < nb * (FP4_BLK / G) * C::BN; i += C::NT) {
-            const int g = i / C::BN, r = i % C::BN;
-            ss[g][r] = scale[((int64_t)c0 * (FP4_BLK / G) + g) * a.w.rows +
-                             min(nw0 + r, a.w.rows - 1)];
+        // scales, four rows a load, SL loads in flight
+        constexpr int PR = C::BN / 4, SL = 4;
+        const int pieces = nb * (FP4_BLK / G) * PR;
+        for (int i = threadIdx.x; i < pieces; i += SL * C::NT) {
+            bytes8 v[SL];
+#pragma unroll
+            for (int u = 0; u < SL; ++u) {
+                const int q = min(i + u * C::NT, pieces - 1), r = q % PR * 4;
+                const uint16_t *p = scale + ((int64_t)c0 * (FP4_BLK / G) + q / PR) * a.w.rows;
+                if (nw0 + r + 4 <= a.w.rows) {
+                    v[u] = *(const bytes8 *)(p + nw0 + r);
+                } else {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        h[e] = p[min(nw0 + r + e, a.w.rows - 1)];
+                    v[u] = bytes8{h[0] | h[1] << 16, h[2] | h[3] << 16};
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < SL; ++u) {
+                const int q = min(i + u * C::NT, pieces - 1);
+                *(uint2 *)&ss[q / PR][q % PR * 4] = make_uint2(v[u].x, v[u].y);
+            }
         }
         ng::wait_vm<0>();
         __syncthreads();
