@@ -5,6 +5,8 @@
 // are three of them (see Acts), so the bfloat16 matrix instruction forms every
 // product exactly; sums are float32.
 #include <cmath>
+#include <cstdlib>
+#include <type_traits>
 
 #include "fp4.hpp"
 
@@ -26,14 +28,14 @@ DEVI bf16x8_t scaled8(uint32_t q, const float *s)
                                                    f32x2_to_bf16x2(c[6] * s[6], c[7] * s[7])));
 }
 // Two of them: those of byte h.
-DEVI uint32_t scaled2(uint32_t q, int h, float s)
+DEVI uint32_t scaled2(uint32_t q, int h, float lo, float hi)
 {
     typedef float f32x2_t __attribute__((ext_vector_type(2)));
     const f32x2_t c = h == 0   ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 0)
                       : h == 1 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 1)
                       : h == 2 ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 2)
                                : __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, 1.f, 3);
-    return f32x2_to_bf16x2(c[0] * s, c[1] * s);
+    return f32x2_to_bf16x2(c[0] * lo, c[1] * hi);
 }
 
 // Four results of a row, from column n, as far as N goes.
@@ -538,7 +540,7 @@ struct TilePlan {
     TileKind k;
     int parts, per;
 };
-TilePlan tile_plan(const TileTime *kinds, int n_kinds, double T, double N, int nkb, int rounds)
+TilePlan tile_plan(const TileTime *kinds, int n_kinds, double T, double N, int nkb)
 {
     TilePlan best = {TILE_64, 1, nkb};
     double least = 1e300;
@@ -550,7 +552,7 @@ TilePlan tile_plan(const TileTime *kinds, int n_kinds, double T, double N, int n
             if (parts > 1 && tiles >= 512)
                 break; // the chip is full
             const double n = up(tiles * parts, 256), pairs = floor(n / 2);
-            const double k = up(nkb, parts) * rounds;
+            const double k = up(nkb, parts);
             const double t = pairs * (k * c.pair + c.ends) + (n - 2 * pairs) * (k * c.step + c.ends) +
                              (parts == 1 ? 0. : 3.0 + parts * T * N * 8 / 4e6);
             if (t < least)
@@ -583,6 +585,9 @@ template <int BM_, int BN_, int WGM_, int WGN_, int NST_, int KS_, int SG_> stru
     static constexpr int WBA = ABYTES / 1024 / NWV, WBB = BN * RW / 1024 / NWV, WB = WBA + WBB;
     // what a row's chunks are XORed with, so that 16 rows lie on distinct banks
     DEVI static int swa(int r) { return KS == 64 ? r >> 1 & 7 : r & 15; }
+    // DX: 16-byte chunks of a row of W's columns, and what they are XORed with
+    static constexpr int CD = BN / 32;
+    DEVI static int swd(int r) { return CD == 8 ? r >> 1 & 7 : r >> 2 & 3; }
     DEVI static int sww(int r) { return KS == 64 ? 0 : r >> 2 & 3; }
     static constexpr int SG = SG_; // groups of scales staged at a time
     static constexpr int OROW = 128 + 16, OUTB = 16 * OROW * NWV; // the epilogue's rows
@@ -608,18 +613,18 @@ struct TileArgs {
     const uint16_t *scale2;
 };
 
-// PL: rows of a token's activations.
-template <int G, class C, int PL>
+// PL: rows of a token's activations. DX: of dY W, see above.
+template <int G, class C, int PL, bool DX>
 __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
 {
     constexpr int NST = C::NST, MI = C::MI, NI = C::NI;
     __shared__ __attribute__((aligned(16))) uint8_t L[NST * C::STAGE];
-    __shared__ __attribute__((aligned(8))) uint16_t ss[C::SG][C::BN];
+    __shared__ __attribute__((aligned(16))) uint16_t ss[C::SG * C::BN];
     // an XCD takes a run of tiles, eight rows of them at a time
     constexpr int GM = 8;
     constexpr bool three = PL == 3;
     constexpr int tpt = three ? C::BM / 16 * 5 : C::BM; // tokens of a tile
-    const int N = a.q2 ? 2 * a.w.rows : a.w.rows;
+    const int N = DX ? a.w.cols : a.q2 ? 2 * a.w.rows : a.w.rows;
     const int nt = (N + C::BN - 1) / C::BN, mt = (a.x.T + tpt - 1) / tpt;
     const int64_t total = (int64_t)nt * mt * a.parts, each = (total + NXCD - 1) / NXCD;
     const int64_t at = blockIdx.x / NXCD, q0 = blockIdx.x % NXCD * each + at;
@@ -637,10 +642,10 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
     // float32 activations a fragment holds five tokens, three rows each.
     const int64_t xrow = three ? a.x.plane : a.x.pitch;
     const uint8_t *srcx = a.x.data + (int64_t)m0 * a.x.pitch, *srcw;
-    const bool second = n0 >= a.w.rows;
+    const bool second = !DX && n0 >= a.w.rows;
     const int nw0 = second ? n0 - a.w.rows : n0; // row of its matrix
     const uint16_t *scale = second ? a.scale2 : a.w.scale;
-    srcw = (second ? a.q2 : a.w.q) + (int64_t)nw0 * a.w.pitch;
+    srcw = DX ? a.w.q : (second ? a.q2 : a.w.q) + (int64_t)nw0 * a.w.pitch;
     uint32_t off[C::WB];
 #pragma unroll
     for (int g = 0; g < C::WB; ++g) {
@@ -649,6 +654,10 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
             const int x = three ? (r >> 4) * 15 + (r & 15) : r; // this row's
             const int last = (a.x.T - m0) * PL - 1;
             off[g] = (uint32_t)min(x, last) * (uint32_t)xrow + (((lane % C::CA) ^ C::swa(r)) << 4);
+        } else if (DX) { // row of the step, and the chunk of columns (past the last: the first)
+            const int r = (w * C::WBB + g - C::WBA) * (64 / C::CD) + lane / C::CD;
+            const uint32_t c = (uint32_t)n0 / 2 + (((lane % C::CD) ^ C::swd(r)) << 4);
+            off[g] = c < (uint32_t)a.w.pitch ? c : 0;
         } else {
             const int r = (w * C::WBB + g - C::WBA) * (64 / C::CW) + lane / C::CW;
             off[g] = (uint32_t)min(r, a.w.rows - 1 - nw0) * (uint32_t)a.w.pitch +
@@ -665,8 +674,10 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
     // this lane's row of a fragment, its first chunk of tokens and its codes
     constexpr int NF = C::NF;
     const uint8_t *Aw = L + (wm * C::WM + l16) * C::RA;
-    const uint8_t *Bw = L + C::ABYTES + (wn * C::WN + l16) * C::RW +
-                        (C::KS == 64 ? q4 * 8 : (q4 ^ C::sww(l16)) << 4);
+    // (DX: row 16 q4 + l16 of the step, whose 16 codes of a tile the read turns)
+    const uint8_t *Bw = L + C::ABYTES + (DX ? (q4 * 16 + l16) * (C::BN / 2)
+                                            : (wn * C::WN + l16) * C::RW +
+                                                  (C::KS == 64 ? q4 * 8 : (q4 ^ C::sww(l16)) << 4));
     int f[NF];
 #pragma unroll
     for (int e = 0; e < NF; ++e)
@@ -675,19 +686,25 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
         __builtin_amdgcn_sched_barrier(0);
         asm volatile("" ::: "memory");
     };
-    const int b0 = part * a.per, b1 = min(a.w.nkb, b0 + a.per);
+    const int b0 = part * a.per, b1 = min(DX ? a.x.nkb : a.w.nkb, b0 + a.per);
     constexpr int CB = C::SG * G / FP4_BLK; // blocks of k whose scales are staged
     for (int c0 = b0; c0 < b1; c0 += CB) {
-        const int nb = min(CB, b1 - c0), n = FP4_BLK / C::KS * nb; // steps
+        const int nb = min(CB, b1 - c0), n_steps = FP4_BLK / C::KS * nb;
         int ls = 0; // the loads' own step
         auto load = [&](int g, int st) {
             const uint32_t dst = lds0 + (uint32_t)(st * C::STAGE);
             if (g < C::WBA)
                 ng::dma16(srcx + (int64_t)c0 * 256 + ls * C::RA, off[g],
-                          dst + (w * C::WBA + g) * 1024, ls, n);
-            else
+                          dst + (w * C::WBA + g) * 1024, ls, n_steps);
+            else if (DX) {
+                const int r = (w * C::WBB + g - C::WBA) * (64 / C::CD) + lane / C::CD;
+                const int64_t n = min((int64_t)c0 * FP4_BLK + ls * C::KS + r, (int64_t)a.w.rows - 1);
+                if (ls < n_steps)
+                    ng::lds_dma16(srcw + n * a.w.pitch + off[g],
+                                  dst + C::ABYTES + (w * C::WBB + g - C::WBA) * 1024);
+            } else
                 ng::dma16(srcw + (int64_t)c0 * FP4_BYTES + ls * C::RW, off[g],
-                          dst + C::ABYTES + (w * C::WBB + g - C::WBA) * 1024, ls, n);
+                          dst + C::ABYTES + (w * C::WBB + g - C::WBA) * 1024, ls, n_steps);
         };
         if (c0 > b0)
             __syncthreads(); // the last scales and stages are used
@@ -698,29 +715,34 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                 load(g, s);
             ++ls;
         }
-        // scales, four rows a load, SL loads in flight
-        constexpr int PR = C::BN / 4, SL = 4;
-        const int pieces = nb * (FP4_BLK / G) * PR;
+        // Scales, four rows a load, SL loads in flight: [group][row of the tile], or
+        // (DX) [group of the tile][row].
+        constexpr int SL = 4, NC = CB * FP4_BLK;
+        const int per = DX ? nb * (FP4_BLK / 4) : C::BN / 4; // pieces of a group
+        const int pieces = per * (DX ? C::BN / G : nb * (FP4_BLK / G));
+        const int g0 = DX ? n0 / G : c0 * (FP4_BLK / G), r0 = DX ? c0 * FP4_BLK : nw0;
         for (int i = threadIdx.x; i < pieces; i += SL * C::NT) {
             bytes8 v[SL];
 #pragma unroll
             for (int u = 0; u < SL; ++u) {
-                const int q = min(i + u * C::NT, pieces - 1), r = q % PR * 4;
-                const uint16_t *p = scale + ((int64_t)c0 * (FP4_BLK / G) + q / PR) * a.w.rows;
-                if (nw0 + r + 4 <= a.w.rows) {
-                    v[u] = *(const bytes8 *)(p + nw0 + r);
+                const int q = min(i + u * C::NT, pieces - 1), r = r0 + q % per * 4;
+                const int g = min(g0 + q / per, a.w.nkb * (FP4_BLK / G) - 1);
+                const uint16_t *p = scale + (int64_t)g * a.w.rows;
+                if (r + 4 <= a.w.rows) {
+                    v[u] = *(const bytes8 *)(p + r);
                 } else {
                     uint32_t h[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        h[e] = p[min(nw0 + r + e, a.w.rows - 1)];
+                        h[e] = p[min(r + e, a.w.rows - 1)];
                     v[u] = bytes8{h[0] | h[1] << 16, h[2] | h[3] << 16};
                 }
             }
 #pragma unroll
             for (int u = 0; u < SL; ++u) {
                 const int q = min(i + u * C::NT, pieces - 1);
-                *(uint2 *)&ss[q / PR][q % PR * 4] = make_uint2(v[u].x, v[u].y);
+                *(uint2 *)&ss[q / per * (DX ? NC : C::BN) + q % per * 4] =
+                    make_uint2(v[u].x, v[u].y);
             }
         }
         ng::wait_vm<0>();
@@ -729,6 +751,7 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
         uint32_t wf[2][NF][4]; // fragments of W in turn
         uint32_t raw[2][NF];   // their codes and scales, read a row of products earlier
         float sc[2];
+        uint32_t sp[4 * NF]; // DX: the scales of the lane's rows of a step
         auto ldx = [&](int j, int st) {
 #pragma unroll
             for (int e = 0; e < NF; ++e)
@@ -736,8 +759,17 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                     bf16x8_t, *(const uint4 *)(Aw + st * C::STAGE + j * 16 * C::RA + f[e]));
         };
         auto ldw = [&](int i, int st, int k) { // fragment i of step k
-            const uint8_t *p = Bw + st * C::STAGE + i * 16 * C::RW;
             uint32_t *q = raw[i & 1];
+            if constexpr (DX) {
+                typedef int intx2_t __attribute__((ext_vector_type(2)));
+                typedef __attribute__((address_space(3))) intx2_t lds_i2;
+                const int c = (wn * C::WN + i * 16) / 2; // byte of the row
+                const uint8_t *p = Bw + st * C::STAGE + (((c >> 4) ^ C::swd(q4 * 16 + l16)) << 4) + (c & 15);
+                const intx2_t u = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i2 *)(uintptr_t)(ng::lds_u8 *)p);
+                q[0] = (uint32_t)u[0], q[1] = (uint32_t)u[1];
+                return;
+            }
+            const uint8_t *p = Bw + st * C::STAGE + i * 16 * C::RW;
             if constexpr (NF == 2) {
                 const uint2 u = *(const uint2 *)p;
                 q[0] = u.x, q[1] = u.y;
@@ -746,26 +778,35 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                 q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
             }
             sc[i & 1] = bf16_to_f32(
-                ss[(k * C::KS + q4 * (C::KS / 4)) / G][wn * C::WN + i * 16 + l16]);
+                ss[(k * C::KS + q4 * (C::KS / 4)) / G * C::BN + wn * C::WN + i * 16 + l16]);
+        };
+        auto lds = [&](int i, int k) { // scales of fragment i of step k
+            const uint4 *p = (const uint4 *)&ss[(wn * C::WN + i * 16) / G * NC + k * C::KS + q4 * 16];
+            const uint4 u = p[0], v = p[1];
+            sp[0] = u.x, sp[1] = u.y, sp[2] = u.z, sp[3] = u.w;
+            sp[4] = v.x, sp[5] = v.y, sp[6] = v.z, sp[7] = v.w;
         };
         auto conv = [&](int i, int p) { // dword p of fragment i
-            wf[i & 1][p / 4][p % 4] = scaled2(raw[i & 1][p / 4], p % 4, sc[i & 1]);
+            const float lo = DX ? bf16_lo(sp[p]) : sc[i & 1], hi = DX ? bf16_hi(sp[p]) : sc[i & 1];
+            wf[i & 1][p / 4][p % 4] = scaled2(raw[i & 1][p / 4], p % 4, lo, hi);
         };
 #pragma unroll
         for (int j = 0; j < MI; ++j)
             ldx(j, 0);
         ldw(0, 0, 0);
         ldw(1, 0, 0);
+        if (DX)
+            lds(0, 0);
 #pragma unroll
         for (int p = 0; p < 4 * NF; ++p)
             conv(0, p);
-        for (int s = 0, st = 0; s < n; ++s) {
-            const int nxt = st == NST - 1 ? 0 : st + 1, sn = s + 1 < n ? s + 1 : 0;
+        for (int s = 0, st = 0; s < n_steps; ++s) {
+            const int nxt = st == NST - 1 ? 0 : st + 1, sn = s + 1 < n_steps ? s + 1 : 0;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 if (i == NI - 2) {
                     fence();
-                    if (s + NST - 1 < n)
+                    if (s + NST - 1 < n_steps)
                         ng::wait_vm<(NST - 2) * C::WB>();
                     else
                         ng::wait_vm<0>();
@@ -777,6 +818,13 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                     ldw(i + 2, st, s);
                 else
                     ldw(i + 2 - NI, nxt, sn);
+                // DX: a fragment of other scales than the last, converted from the row's
+                // middle on
+                const int next = i < NI - 1 ? i + 1 : 0;
+                const bool fresh = DX && (next == 0 || (C::WN > G && next * 16 % G == 0));
+                if (fresh)
+                    lds(next, next == 0 ? sn : s);
+                const int from = fresh ? MI / 2 : 0;
 #pragma unroll
                 for (int j = 0; j < MI; ++j) {
 #pragma unroll
@@ -788,8 +836,10 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
                         ldx(j, nxt);
                     // the next fragment, piece by piece beside this row's products
 #pragma unroll
-                    for (int p = j * 4 * NF / MI; p < (j + 1) * 4 * NF / MI; ++p)
-                        conv(i < NI - 1 ? i + 1 : 0, p);
+                    for (int p = (j - from) * 4 * NF / (MI - from);
+                         p < (j + 1 - from) * 4 * NF / (MI - from); ++p)
+                        if (p >= 0)
+                            conv(next, p);
                     // past the barrier the stage is free: all of its step is in registers
                     const int t = (i - (NI - 2)) * MI + j;
 #pragma unroll
@@ -866,38 +916,38 @@ __global__ __launch_bounds__(C::NT, C::NWV / 4) void fp4_tile_kernel(TileArgs a)
 }
 
 using T64 = TileCfg<64, 128, 1, 4, 2, 128, 64>;  // waves of 64 tokens x 32 rows
+using T64DX = TileCfg<64, 128, 1, 4, 3, 64, 64>;  // (dY W takes steps of 64)
 using T128 = TileCfg<128, 128, 1, 4, 2, 64, 64>; // waves of 128 x 32
 using T256 = TileCfg<256, 256, 2, 4, 3, 64, 64>; // waves of 128 x 64
 
-template <int G, class C> void tile_one(const TileArgs &a, hipStream_t s)
+template <int G, class C, bool DX> void tile_one(const TileArgs &a, hipStream_t s)
 {
     const int tpt = a.x.planes == 3 ? C::BM / 16 * 5 : C::BM;
-    const int64_t N = (int64_t)a.w.rows * (a.q2 ? 2 : 1);
-    const int64_t tiles = (N + C::BN - 1) / C::BN * ((a.x.T + tpt - 1) / tpt) *
-                          a.parts;
+    const int64_t N = DX ? a.w.cols : (int64_t)a.w.rows * (a.q2 ? 2 : 1);
+    const int64_t tiles = (N + C::BN - 1) / C::BN * ((a.x.T + tpt - 1) / tpt) * a.parts;
     const uint32_t grid = (uint32_t)((tiles + NXCD - 1) / NXCD * NXCD);
     if (a.x.planes == 3)
-        fp4_tile_kernel<G, C, 3><<<grid, C::NT, 0, s>>>(a);
+        fp4_tile_kernel<G, C, 3, DX><<<grid, C::NT, 0, s>>>(a);
     else
-        fp4_tile_kernel<G, C, 1><<<grid, C::NT, 0, s>>>(a);
+        fp4_tile_kernel<G, C, 1, DX><<<grid, C::NT, 0, s>>>(a);
 }
-template <int G> void tile_group(const TileArgs &a, TileKind k, hipStream_t s)
+template <int G, bool DX> void tile_group(const TileArgs &a, TileKind k, hipStream_t s)
 {
     if (k == TILE_256)
-        tile_one<G, T256>(a, s);
+        tile_one<G, T256, DX>(a, s);
     else if (k == TILE_128)
-        tile_one<G, T128>(a, s);
+        tile_one<G, T128, DX>(a, s);
     else
-        tile_one<G, T64>(a, s);
+        tile_one<G, std::conditional_t<DX, T64DX, T64>, DX>(a, s);
 }
-void tiles(const TileArgs &a, TileKind k, hipStream_t s)
+template <bool DX> void tiles(const TileArgs &a, TileKind k, hipStream_t s)
 {
     if (a.w.group == 32)
-        tile_group<32>(a, k, s);
+        tile_group<32, DX>(a, k, s);
     else if (a.w.group == 64)
-        tile_group<64>(a, k, s);
+        tile_group<64, DX>(a, k, s);
     else
-        tile_group<128>(a, k, s);
+        tile_group<128, DX>(a, k, s);
 }
 
 // Tiles of X W^T. A float32 token takes 3.2 rows of a tile.
@@ -906,94 +956,19 @@ TilePlan fwd_plan(int T, int N, int nkb, int planes, bool both = false)
     static const TileTime kinds[] = {{64, 128, 0.75, 1.1, 2.5}, {128, 128, 1.1, 1.95, 3.0},
                                      {256, 256, 2.7, 5.4, 5.0}};
     // (of two matrices one after the other 256 rows may be of both)
-    return tile_plan(kinds, both ? 2 : 3, planes == 3 ? T * 3.2 : T, N, nkb, 1);
+    return tile_plan(kinds, both ? 2 : 3, planes == 3 ? T * 3.2 : T, N, nkb);
 }
-
-// ---------------------------------------------------------------- dY W, many tokens
-// The values as bfloat16 in the workspace, then a dense product on the shared
-// main loop, W's rows along the contraction; a float32 token's three rows in turn,
-// the smallest first.
-struct GemmArgs {
-    Acts x;
-    const uint8_t *w; // [n][k], zeros past the contraction
-    int64_t wpitch;
-    int N, NW; // columns of the result, of w
-    void *out;
-    int64_t ldo;
-    int dto;
-    float *part; // split contraction: [parts][T][ldp]
-    int64_t ldp;
-    int parts, per; // parts, blocks of 128 rows of w in each
-};
-
-template <class C> __global__ __launch_bounds__(C::NT) void fp4_gemm_kernel(GemmArgs a)
+// Tiles of dY W.
+TilePlan dx_plan(int T, int K, int nkb, int planes)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t L[C::LDS];
-    constexpr int KS = C::ROWB / 2;
-    const int nt = (a.N + C::BN - 1) / C::BN, mt = (a.x.T + C::BM - 1) / C::BM;
-    const int lane = threadIdx.x & 63, wm = ng::wave_m<C>(), wn = ng::wave_n<C>();
-    for (int64_t q = blockIdx.x; q < (int64_t)nt * mt * a.parts; q += gridDim.x) {
-        const int part = (int)(q / ((int64_t)nt * mt));
-        const int64_t tile = q % ((int64_t)nt * mt);
-        const int m0 = (int)(tile % mt) * C::BM, n0 = (int)(tile / mt) * C::BN;
-        const int b0 = part * a.per, steps = (min(a.x.nkb, b0 + a.per) - b0) * (FP4_BLK / KS);
-        const int k0 = b0 * (FP4_BLK / KS);
-        auto rowa = [&](int r) { return a.x.data + (int64_t)min(m0 + r, a.x.T - 1) * a.x.pitch; };
-        auto rowb = [&](int r) { return a.w + (int64_t)r * a.wpitch + (int64_t)n0 * 2; };
-        auto off = [&](int kt) {
-            const int p = kt / steps, k = k0 + kt % steps;
-            return ng::StepOff{
-                (size_t)((a.x.planes - 1 - p) * a.x.plane + (int64_t)k * C::ROWB),
-                (size_t)((int64_t)k * KS * a.wpitch)};
-        };
-        ng::Acc<C> acc;
-        ng::mainloop_mixed<C, TWELL_BF16, ng::KC, ng::KM>(L, rowa, rowb, off, 0,
-                                                         steps * a.x.planes, acc, 1 << 30,
-                                                         a.NW - n0);
-#pragma unroll
-        for (int mi = 0; mi < C::MI; ++mi)
-#pragma unroll
-            for (int ni = 0; ni < C::NI; ++ni)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int m = m0 + ng::acc_row<C>(wm, mi, e, lane);
-                    const int n = n0 + ng::acc_col<C>(wn, ni, lane);
-                    if (m < a.x.T && n < a.N) {
-                        const float v = acc.v[mi][ni][e];
-                        if (a.parts > 1)
-                            a.part[((int64_t)part * a.x.T + m) * a.ldp + n] = v;
-                        else if (a.dto == TWELL_BF16)
-                            ((uint16_t *)a.out)[m * a.ldo + n] = (uint16_t)f32x2_to_bf16x2(v, 0.f);
-                        else
-                            ((float *)a.out)[m * a.ldo + n] = v;
-                    }
-                }
+    static const TileTime kinds[] = {{64, 128, 0.9, 1.3, 2.5}, {128, 128, 1.3, 2.2, 3.0},
+                                     {256, 256, 3.0, 6.0, 5.0}};
+    TilePlan p = tile_plan(kinds, 3, planes == 3 ? T * 3.2 : T, K, nkb);
+    if (getenv("FP4K")) {
+        p.k = (TileKind)atoi(getenv("FP4K")), p.parts = atoi(getenv("FP4P"));
+        p.per = (nkb + p.parts - 1) / p.parts, p.parts = p.per ? (nkb + p.per - 1) / p.per : 1;
     }
-}
-
-using C64 = ng::Cfg<64, 128, 1, 4, 3, 128>;
-using C128 = ng::Cfg<128, 128, 2, 4, 2, 128>;
-using C256 = ng::Cfg<256, 256, 2, 4, 2, 128>;
-
-TilePlan dx_plan(int T, int N, int nkb, int planes)
-{
-    static const TileTime kinds[] = {{64, 128, 1.2, 2.2, 3.0}, {128, 128, 1.95, 2.5, 3.0},
-                                     {256, 256, 3.3, 6.6, 5.0}};
-    return tile_plan(kinds, 3, T, N, nkb, planes);
-}
-template <class C> void gemm_one(const GemmArgs &a, hipStream_t s)
-{
-    const int64_t tiles = (int64_t)((a.N + C::BN - 1) / C::BN) * ((a.x.T + C::BM - 1) / C::BM) * a.parts;
-    fp4_gemm_kernel<C><<<(uint32_t)(tiles < 1 << 20 ? tiles : 1 << 20), C::NT, 0, s>>>(a);
-}
-void gemm(const GemmArgs &a, TileKind k, hipStream_t s)
-{
-    if (k == TILE_256)
-        gemm_one<C256>(a, s);
-    else if (k == TILE_128)
-        gemm_one<C128>(a, s);
-    else
-        gemm_one<C64>(a, s);
+    return p;
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1002,8 +977,6 @@ bool few(int T, int planes, bool dx) { return T <= (planes == 3 ? 5 : 16) * (dx 
 int planes_of(const twell_mat_t *x) { return x->dtype == TWELL_BF16 ? 1 : 3; }
 
 } // namespace
-
-void fp4_dequant(const Fp4 &w, void *out, int64_t ld, int dt, int rows, int cols, hipStream_t s);
 
 void fp4_rows(const Acts &x, const Fp4 &w, const Fp4 *up, void *out, int64_t ldo, int dto,
               hipStream_t s)
@@ -1026,13 +999,9 @@ size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
         int per, parts = dx ? cols_parts(rows, fp4_blocks(cols), &per) : 1;
         return parts == 1 ? pack : up256(pack) + (size_t)parts * x->rows * pitch * 4;
     }
-    if (dx) {
-        const int parts = dx_plan(x->rows, cols, fp4_blocks(rows), planes_of(x)).parts;
-        return up256(pack) + (size_t)fp4_blocks(rows) * FP4_BLK * pitch * 2 +
-               (parts > 1 ? (size_t)parts * x->rows * part_pitch(cols) * 4 : 0);
-    }
-    const TilePlan p = fwd_plan(x->rows, rows, fp4_blocks(cols), planes_of(x));
-    return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(rows) * 4;
+    const int n = dx ? cols : rows, nkb = fp4_blocks(dx ? rows : cols);
+    const TilePlan p = dx ? dx_plan(x->rows, n, nkb, planes_of(x)) : fwd_plan(x->rows, n, nkb, planes_of(x));
+    return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(n) * 4;
 }
 
 int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t *out, bool dx,
@@ -1050,42 +1019,28 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
     uint8_t *ws2 = (uint8_t *)ws + up256(fp4_pack_bytes(x));
     const int dto = out->dtype;
     const bool little = few(a.T, planes_of(x), dx);
+    JoinArgs j = {(float *)ws2, 1, a.T, dx ? w.cols : w.rows, 0, out->data, out->ld, dto};
     if (!dx && little) {
         fp4_rows(a, w, nullptr, out->data, out->ld, dto, s);
         tm.mark("fp4_rows");
-    } else if (!dx) {
-        const TilePlan p = fwd_plan(a.T, w.rows, w.nkb, planes_of(x));
-        const TileArgs t = {a, w, out->data, out->ld, dto, (float *)ws2, part_pitch(w.rows),
-                            p.parts, p.per, nullptr, nullptr};
-        tiles(t, p.k, s);
-        tm.mark("fp4_tile");
-        if (p.parts > 1) {
-            join({t.part, p.parts, a.T, w.rows, t.ldp, out->data, out->ld, dto}, s);
-            tm.mark("fp4_join");
-        }
     } else if (little) {
         ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T, a.planes, a.nkb, w,
                       (float *)ws2, 0, 0, out->data, out->ld, dto};
-        c.parts = cols_parts(w.rows, w.nkb, &c.per);
+        c.parts = j.parts = cols_parts(w.rows, w.nkb, &c.per);
+        j.pitch = (int64_t)w.nkb * FP4_BLK;
         cols(c, s);
         tm.mark("fp4_cols");
-        if (c.parts > 1) {
-            join({c.part, c.parts, a.T, w.cols, (int64_t)w.nkb * FP4_BLK, out->data, out->ld, dto}, s);
-            tm.mark("fp4_join");
-        }
     } else {
-        const int wc = w.nkb * FP4_BLK, rows = fp4_blocks(w.rows) * FP4_BLK;
-        fp4_dequant(w, ws2, wc, TWELL_BF16, rows, wc, s);
-        tm.mark("fp4_dequant");
-        const TilePlan p = dx_plan(a.T, w.cols, a.nkb, planes_of(x));
-        const GemmArgs g = {a, ws2, (int64_t)wc * 2, w.cols, wc, out->data, out->ld, dto,
-                            (float *)(ws2 + (size_t)rows * wc * 2), part_pitch(w.cols), p.parts, p.per};
-        gemm(g, p.k, s);
-        tm.mark("fp4_gemm");
-        if (g.parts > 1) {
-            join({g.part, g.parts, a.T, w.cols, g.ldp, out->data, out->ld, dto}, s);
-            tm.mark("fp4_join");
-        }
+        const TilePlan p = dx ? dx_plan(a.T, j.N, a.nkb, planes_of(x)) : fwd_plan(a.T, j.N, a.nkb, planes_of(x));
+        j.parts = p.parts, j.pitch = part_pitch(j.N);
+        const TileArgs t = {a, w, out->data, out->ld, dto, (float *)ws2, j.pitch, p.parts, p.per,
+                            nullptr, nullptr};
+        dx ? tiles<true>(t, p.k, s) : tiles<false>(t, p.k, s);
+        tm.mark("fp4_tile");
+    }
+    if (j.parts > 1) {
+        join(j, s);
+        tm.mark("fp4_join");
     }
     return hipGetLastError() == hipSuccess ? TWELL_OK : TWELL_E_HIP;
 }
@@ -1101,5 +1056,5 @@ void fp4_gates(const Acts &x, const Fp4 &wg, const Fp4 &wu, float *parts, hipStr
 {
     const TilePlan p = fwd_plan(x.T, 2 * wg.rows, wg.nkb, x.planes, true);
     const int64_t ld = 2 * (int64_t)wg.rows;
-    tiles({x, wg, parts, ld, TWELL_F32, parts, ld, p.parts, p.per, wu.q, wu.scale}, p.k, s);
+    tiles<false>({x, wg, parts, ld, TWELL_F32, parts, ld, p.parts, p.per, wu.q, wu.scale}, p.k, s);
 }
