@@ -5,7 +5,6 @@
 // are three of them (see Acts), so the bfloat16 matrix instruction forms every
 // product exactly; sums are float32.
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 #include "fp4.hpp"
@@ -508,13 +507,10 @@ template <int TB> void cols_tb(const ColsArgs &a, hipStream_t s)
 }
 void cols(const ColsArgs &a, hipStream_t s)
 {
-    const int tiles = (a.T + (a.planes == 3 ? 4 : 15)) / (a.planes == 3 ? 5 : 16);
-    if (tiles <= 1)
+    if (a.T <= (a.planes == 3 ? 5 : 16))
         cols_tb<1>(a, s);
-    else if (tiles <= 2)
-        cols_tb<2>(a, s);
     else
-        cols_tb<4>(a, s);
+        cols_tb<2>(a, s);
 }
 
 // Parts of the contraction: about a workgroup a CU, of at least CN rows each.
@@ -963,17 +959,23 @@ TilePlan dx_plan(int T, int K, int nkb, int planes)
 {
     static const TileTime kinds[] = {{64, 128, 0.9, 1.3, 2.5}, {128, 128, 1.3, 2.2, 3.0},
                                      {256, 256, 3.0, 6.0, 5.0}};
-    TilePlan p = tile_plan(kinds, 3, planes == 3 ? T * 3.2 : T, K, nkb);
-    if (getenv("FP4K")) {
-        p.k = (TileKind)atoi(getenv("FP4K")), p.parts = atoi(getenv("FP4P"));
-        p.per = (nkb + p.parts - 1) / p.parts, p.parts = p.per ? (nkb + p.per - 1) / p.per : 1;
-    }
-    return p;
+    return tile_plan(kinds, 3, planes == 3 ? T * 3.2 : T, K, nkb);
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-// the few-token kernels: of X W^T for one 16-column tile, of dY W for four
-bool few(int T, int planes, bool dx) { return T <= (planes == 3 ? 5 : 16) * (dx ? 4 : 1); }
+// Whether the few-token kernels take a product: of X W^T over N rows of nkb blocks
+// up to two 16-column tiles of activations (24 tokens over 6144 x 2304: 8.1 against
+// 11.4 us), or while all tiles together are little work (64 tokens over 1024 x 1024:
+// 3.7 against 8.3, over 6144 x 2304 11.8 against 13.2, over 4096 x 4096 16.0 against
+// 14.4); of dY W up to two tiles (24 tokens over 6144 x 2304: 10.8 against 12.9, 48:
+// 15.3 against 13.6).
+int token_tiles(int T, int planes) { return (T + (planes == 3 ? 4 : 15)) / (planes == 3 ? 5 : 16); }
+bool few_fwd(int T, int planes, int64_t N, int nkb)
+{
+    const int64_t mt = token_tiles(T, planes);
+    return mt <= 2 || mt * ((N + 15) / 16) * nkb <= 22000;
+}
+bool few_dx(int T, int planes) { return token_tiles(T, planes) <= 2; }
 int planes_of(const twell_mat_t *x) { return x->dtype == TWELL_BF16 ? 1 : 3; }
 
 } // namespace
@@ -995,12 +997,15 @@ void fp4_rows(const Acts &x, const Fp4 &w, const Fp4 *up, void *out, int64_t ldo
 size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
 {
     const size_t pack = fp4_pack_bytes(x), pitch = (size_t)fp4_blocks(cols) * FP4_BLK;
-    if (few(x->rows, planes_of(x), dx)) {
-        int per, parts = dx ? cols_parts(rows, fp4_blocks(cols), &per) : 1;
+    const int planes = planes_of(x);
+    if (!dx && few_fwd(x->rows, planes, rows, fp4_blocks(cols)))
+        return pack;
+    if (dx && few_dx(x->rows, planes)) {
+        int per, parts = cols_parts(rows, fp4_blocks(cols), &per);
         return parts == 1 ? pack : up256(pack) + (size_t)parts * x->rows * pitch * 4;
     }
     const int n = dx ? cols : rows, nkb = fp4_blocks(dx ? rows : cols);
-    const TilePlan p = dx ? dx_plan(x->rows, n, nkb, planes_of(x)) : fwd_plan(x->rows, n, nkb, planes_of(x));
+    const TilePlan p = dx ? dx_plan(x->rows, n, nkb, planes) : fwd_plan(x->rows, n, nkb, planes);
     return p.parts == 1 ? pack : up256(pack) + (size_t)p.parts * x->rows * part_pitch(n) * 4;
 }
 
@@ -1017,13 +1022,12 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
     if (packed)
         tm.mark("fp4_pack");
     uint8_t *ws2 = (uint8_t *)ws + up256(fp4_pack_bytes(x));
-    const int dto = out->dtype;
-    const bool little = few(a.T, planes_of(x), dx);
+    const int dto = out->dtype, planes = planes_of(x);
     JoinArgs j = {(float *)ws2, 1, a.T, dx ? w.cols : w.rows, 0, out->data, out->ld, dto};
-    if (!dx && little) {
+    if (!dx && few_fwd(a.T, planes, w.rows, w.nkb)) {
         fp4_rows(a, w, nullptr, out->data, out->ld, dto, s);
         tm.mark("fp4_rows");
-    } else if (little) {
+    } else if (dx && few_dx(a.T, planes)) {
         ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T, a.planes, a.nkb, w,
                       (float *)ws2, 0, 0, out->data, out->ld, dto};
         c.parts = j.parts = cols_parts(w.rows, w.nkb, &c.per);
@@ -1031,12 +1035,13 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
         cols(c, s);
         tm.mark("fp4_cols");
     } else {
-        const TilePlan p = dx ? dx_plan(a.T, j.N, a.nkb, planes_of(x)) : fwd_plan(a.T, j.N, a.nkb, planes_of(x));
+        const TilePlan p = dx ? dx_plan(a.T, j.N, a.nkb, planes) : fwd_plan(a.T, j.N, a.nkb, planes);
         j.parts = p.parts, j.pitch = part_pitch(j.N);
         const TileArgs t = {a, w, out->data, out->ld, dto, (float *)ws2, j.pitch, p.parts, p.per,
                             nullptr, nullptr};
         dx ? tiles<true>(t, p.k, s) : tiles<false>(t, p.k, s);
-        tm.mark("fp4_tile");
+        static const char *const names[] = {"fp4_tile64", "fp4_tile128", "fp4_tile256"};
+        tm.mark(names[p.k]);
     }
     if (j.parts > 1) {
         join(j, s);
@@ -1048,7 +1053,7 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
 int fp4_gates_parts(const twell_mat_t *x, int d_ff)
 {
     const int planes = planes_of(x);
-    return few(x->rows, planes, false)
+    return few_fwd(x->rows, planes, 2 * d_ff, fp4_blocks(x->cols))
                ? 0 : fwd_plan(x->rows, 2 * d_ff, fp4_blocks(x->cols), planes, true).parts;
 }
 

@@ -17,40 +17,93 @@ def acts(T, K, seed, dtype=BF):
     return torch.randn(T, K, generator=gen(seed)).to(dtype)
 
 
+def coded(N, K, group, seed, spread=4):
+    """A matrix of any codes, scales of powers of two: (Fp4, its float64 values), on
+    the GPU."""
+    g = torch.Generator(DEV).manual_seed(seed)
+    kp = -(-K // 128) * 128
+    q = torch.randint(0, 256, (N, kp // 2), generator=g, device=DEV, dtype=torch.uint8)
+    if K < kp:
+        q[:, (K + 1) // 2:] = 0
+        if K % 2:
+            q[:, K // 2] &= 15
+    e = torch.randint(-spread, spread + 1, (kp // group, N), generator=g, device=DEV)
+    w4 = tw.Fp4(q, torch.exp2(e.float()).to(BF), K, group)
+    return w4, w4.float().double()
+
+
+def check(call, x, w4, w, T, n, K):
+    """call(x, w4) against x w^T (w given with the contraction last), 64 bits on the GPU."""
+    t = tw.KernelTimer()
+    got = call(x, w4, out_dtype=F32, timing=t)
+    x = x.double()
+    want, mag = x @ w.t().contiguous(), x.abs() @ w.t().abs().contiguous()
+    assert got.shape == (T, n)
+    d = (got.double() - want).abs() - ref.terms(K) * ref.U32 * mag
+    assert bool((d <= 0).all()), f"off by {float(d.max()):.3e} past the tolerance"
+    return [name for name, _ in t.collect()]
+
+
 # ---------------------------------------------------------------- kernels and sizes
-# few tokens over rows of each width class and contractions longer than the
-# scales staged at once; tiles of 64, 128 and 256, their contraction in parts, and
-# longer than the scales staged at once; a last round of tiles that is cut
-FWD = [(1, 4097, 256, 32), (3, 16400, 128, 64), (16, 16385, 130, 32), (2, 40, 9000, 32),
-       (16, 24, 17000, 128), (12, 4200, 640, 64), (40, 200, 4500, 32), (70, 300, 9000, 32),
-       (300, 1000, 1000, 128), (1030, 700, 260, 64), (2100, 4360, 384, 128), (4200, 2050, 136, 32)]
+# few tokens: rows of each width class, contractions longer than the scales staged
+# at once, several tiles of tokens
+ROWS = [(1, 4097, 256, 32), (3, 16400, 128, 64), (16, 16385, 130, 32), (2, 40, 9000, 32),
+        (16, 24, 17000, 128), (12, 4200, 640, 64), (40, 200, 4500, 32), (70, 300, 900, 32),
+        (32, 4300, 520, 128)]
+# many: tiles of each size, the contraction in parts, and longer than the scales
+# staged at once, edges cut; with how many tokens
+TILES = [(100, 2811, 2304, 32), (60, 33000, 2200, 32), (500, 5632, 2200, 32), (333, 2811, 1090, 64),
+         (2048, 4096, 520, 64), (640, 4090, 2048, 128), (1030, 4101, 1000, 128), (4200, 4100, 2200, 32), (8200, 2050, 136, 128)]
 
 
-@pytest.mark.parametrize("T,N,K,group", FWD)
-def test_matmul_sizes(T, N, K, group):
+@pytest.mark.parametrize("T,N,K,group", ROWS)
+def test_matmul_few_tokens(T, N, K, group):
     print("[case] fp4_matmul", T, N, K, group, flush=True)
-    w4, w = quantised(N, K, group, N)
+    w4, w = coded(N, K, group, N)
     for dtype in (BF, F32):
-        x = acts(T, K, 5, dtype)
-        got = tw.fp4_matmul(x.to(DEV), w4, out_dtype=F32)
-        want, mag = ref.matmul(x, w)
-        within(got, want, ref.bound(mag, want, K, F32))
+        check(tw.fp4_matmul, acts(T, K, 5, dtype).to(DEV), w4, w, T, N, K)
 
 
-DX = [(1, 5000, 130, 32), (17, 600, 2000, 64), (33, 7000, 300, 128), (64, 300, 40000, 32),
-      (20, 513, 384, 64), (70, 5000, 300, 32), (300, 1000, 1000, 128), (1030, 260, 700, 64),
-      (2100, 384, 4360, 128)]
+@pytest.mark.parametrize("dtype", (BF, F32))
+def test_matmul_tiles(dtype):
+    seen = set()
+    for T, N, K, group in TILES:
+        print("[case] fp4_matmul", T, N, K, group, dtype, flush=True)
+        w4, w = coded(N, K, group, N)
+        seen |= set(check(tw.fp4_matmul, acts(T, K, 5, dtype).to(DEV), w4, w, T, N, K))
+    assert {"fp4_tile64", "fp4_tile128", "fp4_tile256", "fp4_join"} <= seen
 
 
-@pytest.mark.parametrize("T,N,K,group", DX)
-def test_matmul_dx_sizes(T, N, K, group):
-    print("[case] fp4_matmul_dx", T, N, K, group, flush=True)
-    w4, w = quantised(N, K, group, N)
-    for dtype in (BF, F32):
-        dy = acts(T, N, 5, dtype)
-        got = tw.fp4_matmul_dx(dy.to(DEV), w4, out_dtype=F32)
-        want, mag = ref.matmul(dy, w.t())
-        within(got, want, ref.bound(mag, want, N, F32))
+@pytest.mark.parametrize("dtype", (BF, F32))
+def test_matmul_dx_kernels(dtype):
+    seen = set()
+    for T, K, N, group in TILES + [(1, 5000, 130, 32), (17, 600, 2000, 64), (33, 300, 7000, 128),
+                                   (30, 40000, 300, 64), (20, 384, 513, 64), (5, 70, 600, 32)]:
+        print("[case] fp4_matmul_dx", T, N, K, group, dtype, flush=True)
+        w4, w = coded(N, K, group, N)
+        seen |= set(check(tw.fp4_matmul_dx, acts(T, N, 5, dtype).to(DEV), w4, w.t(), T, K, N))
+    assert {"fp4_cols", "fp4_tile64", "fp4_tile128", "fp4_tile256", "fp4_join"} <= seen
+
+
+@pytest.mark.parametrize("T,d,f,group", [(64, 2304, 6144, 32), (40, 1024, 16384, 128), (34, 4096, 4224, 64)])
+@pytest.mark.parametrize("dtype", (BF, F32))
+def test_layer_of_many_tokens(T, d, f, group, dtype):
+    """The gates and up products as tiles, their contraction in parts."""
+    x = acts(T, d, 1)
+    x[:, 0] = 1
+    ms = []
+    for i in range(3):
+        m = torch.randn(f, d, generator=gen(10 + i)) / (f if i == 2 else d) ** 0.5
+        if i == 0:
+            m[:, 0] = -2
+        w4 = tw.fp4_quant(m.to(DEV), group=group)
+        ms.append((w4, w4.float().double().cpu()))
+    x = x.to(dtype)
+    t = tw.KernelTimer()
+    y = tw.fp4_decode_fwd(x.to(DEV), *(m for m, _ in ms), timing=t)
+    want, tol = ref.layer(x, *(v for _, v in ms))
+    within(y, want, tol)
+    assert [n for n, _ in t.collect()][-3:] == ["fp4_gates", "fp4_act", "fp4_down"]
 
 
 @pytest.mark.parametrize("T", (1, 3, 5, 17))
@@ -333,22 +386,20 @@ def test_nothing_to_do():
     assert tw.fp4_dequant(none).shape == (0, 200)
 
 
-def test_kernel_names_are_timed():
-    w4, _ = quantised(300, 520, 64, 1)
-    ms = [quantised(256, 192, 32, i, 0.1)[0] for i in range(3)]
-    t = tw.KernelTimer()
-    seen = {}
-    for T in (1, 40, 200):
-        for call in (lambda: tw.fp4_matmul(acts(T, 520, 1).to(DEV), w4, timing=t),
-                     lambda: tw.fp4_matmul_dx(acts(T, 300, 1, F32).to(DEV), w4, timing=t),
-                     lambda: tw.fp4_decode_fwd(acts(min(T, 64), 192, 1).to(DEV), *ms, timing=t),
-                     lambda: tw.fp4_quant(weights(9, 99, 1).to(DEV), timing=t),
-                     lambda: tw.fp4_dequant(w4, timing=t)):
-            call()
-            torch.cuda.synchronize()
-            t.add(seen)
-    assert {"fp4_pack", "fp4_rows", "fp4_tile", "fp4_cols", "fp4_dequant", "fp4_quant",
-            "fp4_gate_up", "fp4_gates", "fp4_act", "fp4_down"} <= set(seen)
+def test_kernels_are_timed():
+    t, seen = tw.KernelTimer(), {}
+    w4, ms = coded(300, 520, 64, 1)[0], [coded(256, 192, 32, i)[0] for i in range(3)]
+    x = acts(40, 520, 1, F32).to(DEV)
+    for call in (lambda: tw.fp4_matmul(x, w4, timing=t),
+                 lambda: tw.fp4_matmul_dx(x[:2, :300], w4, timing=t),
+                 lambda: tw.fp4_decode_fwd(x[:2, :192], *ms, timing=t),
+                 lambda: tw.fp4_quant(x, timing=t), lambda: tw.fp4_dequant(w4, timing=t)):
+        call()
+        torch.cuda.synchronize()
+        t.add(seen)
+    assert {"fp4_pack", "fp4_rows", "fp4_cols", "fp4_dequant", "fp4_quant", "fp4_gate_up",
+            "fp4_down"} <= set(seen)
+    assert all(0 < ms < 10 for ms in seen.values())
 
 
 # ---------------------------------------------------------------- together
