@@ -117,8 +117,8 @@ __global__ __launch_bounds__(64 * LW) void fp4_up_kernel(UpArgs p)
 }
 
 // LPR: lanes of a row, eight columns each (a slice is 8 LPR columns)
-constexpr int UB = 8; // sets of 64 neurons that a wave lists at a time
-template <int LPR, int LW> __global__ __launch_bounds__(64 * LW) void fp4_down_kernel(LayerArgs p)
+constexpr int UB = 16; // sets of 64 neurons that a wave lists at a time
+template <int LPR> __global__ __launch_bounds__(64 * LW) void fp4_down_kernel(LayerArgs p)
 {
     constexpr int RPW = 64 / LPR, COLS = 8 * LPR, DEEP = 8; // rows of a load, loads in flight
     __shared__ int li[LW][64 * UB];
@@ -230,16 +230,13 @@ hipError_t launch_fp4_layer(const twell_mat_t *x, const twell_fp4_t *wg, const t
         tm.mark("fp4_up");
     }
     const LayerArgs p = {T, d, f, fp4_arg(wd), a, y};
-    // A slice of 512 columns reads the gates' list least often, one of 128 fills the
-    // chip for few tokens; its sixteen waves are through a long list sooner (one
-    // token by 6144 neurons: 10.7 against 11.6 us of the layer; by 2816: 7.4 against 6.9)
+    // a slice of 512 columns reads the gates' list least often, one of 128 fills the
+    // chip for few tokens
     const int64_t wide = T * ((d + 511) / 512), slices = T * ((d + 127) / 128);
     if (wide >= 256)
-        fp4_down_kernel<64, 8><<<(uint32_t)wide, 64 * 8, 0, s>>>(p);
-    else if (slices <= 128 && f > 64 * UB * 8)
-        fp4_down_kernel<16, 16><<<(uint32_t)slices, 64 * 16, 0, s>>>(p);
+        fp4_down_kernel<64><<<(uint32_t)wide, 64 * LW, 0, s>>>(p);
     else
-        fp4_down_kernel<16, 8><<<(uint32_t)slices, 64 * 8, 0, s>>>(p);
+        fp4_down_kernel<16><<<(uint32_t)slices, 64 * LW, 0, s>>>(p);
     tm.mark("fp4_down");
     return hipGetLastError();
 }
