@@ -131,30 +131,32 @@ template <int G> __global__ __launch_bounds__(256) void fp4_quant_kernel(QuantAr
     }
 }
 
-// The values: out [w.rows up to `rows`][`cols`], zeros outside the matrix.
+// Row i / n of piece i, n pieces a row: in 32 bits where they do.
+DEVI int64_t row_of(int64_t i, int n)
+{
+    return i >> 32 ? i / n : (int64_t)((uint32_t)i / (uint32_t)n);
+}
+
 struct DequantArgs {
     Fp4 w;
     void *out;
     int64_t ld;
-    int rows, cols;
-    int64_t tiles;
+    int cn; // pieces of a row
+    int64_t pieces;
 };
 // One thread takes 16 bytes of results of each of DR rows: eight bfloat16 or four
 // float32 columns.
-constexpr int DR = 8;
+constexpr int DR = 4;
 template <class T> __global__ __launch_bounds__(256) void fp4_dequant_kernel(DequantArgs a)
 {
     constexpr int N = 16 / sizeof(T);
-    const int cn = (a.cols + N - 1) / N, nct = (cn + 255) / 256;
     const int shift = 31 - __builtin_clz(a.w.group);
-    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-        const int j = ((int)(tile % nct) * 256 + threadIdx.x) * N;
-        const int64_t r0 = tile / nct * DR;
-        if (j >= a.cols)
-            continue;
-        const bool in = j / 2 < a.w.pitch;
-        const uint16_t *sc = a.w.scale + (int64_t)(in ? j >> shift : 0) * a.w.rows;
-        const uint8_t *q = a.w.q + (in ? j / 2 : 0);
+    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < a.pieces; i0 += (int64_t)gridDim.x * 256) {
+        const int64_t rg = row_of(i0, a.cn);
+        const int j = (int)(i0 - rg * a.cn) * N;
+        const int64_t r0 = rg * DR;
+        const uint16_t *sc = a.w.scale + (int64_t)(j >> shift) * a.w.rows;
+        const uint8_t *q = a.w.q + j / 2;
         uint32_t code[DR];
         uint16_t s[DR];
 #pragma unroll
@@ -167,14 +169,13 @@ template <class T> __global__ __launch_bounds__(256) void fp4_dequant_kernel(Deq
 #pragma unroll
         for (int i = 0; i < DR; ++i) {
             const int64_t r = r0 + i;
-            if (r >= a.rows)
+            if (r >= a.w.rows)
                 break;
             float v[8];
             fp4x8_to_f32(code[i], v);
-            const bool real = in && r < a.w.rows;
 #pragma unroll
             for (int e = 0; e < N; ++e)
-                v[e] = real ? v[e] * bf16_to_f32(s[i]) : 0.f;
+                v[e] *= bf16_to_f32(s[i]);
             uint4 u;
             if constexpr (N == 8)
                 u = make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]),
@@ -183,13 +184,13 @@ template <class T> __global__ __launch_bounds__(256) void fp4_dequant_kernel(Deq
                 u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]),
                                __float_as_uint(v[2]), __float_as_uint(v[3]));
             T *p = (T *)a.out + r * a.ld + j;
-            if (j + N <= a.cols) {
+            if (j + N <= a.w.cols) {
                 stg16u_nt(p, u);
             } else {
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int e = 0; e < N - 1; ++e)
-                    if (j + e < a.cols)
+                    if (j + e < a.w.cols)
                         p[e] = (T)(w[e * sizeof(T) / 4] >> (8 * sizeof(T) * e % 32));
             }
         }
@@ -227,13 +228,12 @@ DEVI void pack8(const void *x, int dt, int64_t ld, int64_t t, int c, int C, int 
 
 // Rows of bfloat16 padded to whole blocks, three rows a float32 row (see Acts).
 __global__ __launch_bounds__(256) void fp4_pack_kernel(const void *x, int dt, int64_t ld, int C,
-                                                       int nkb, int64_t tiles, uint8_t *out)
+                                                       int nkb, int64_t pieces, uint8_t *out)
 {
-    const int c8 = nkb * (FP4_BLK / 8), nct = (c8 + 255) / 256;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int c = (int)(tile % nct) * 256 + threadIdx.x;
-        if (c < c8)
-            pack8(x, dt, ld, tile / nct, c, C, nkb, out);
+    const int n = nkb * (FP4_BLK / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = row_of(i, n);
+        pack8(x, dt, ld, t, (int)(i - t * n), C, nkb, out);
     }
 }
 
@@ -256,9 +256,9 @@ Acts fp4_pack(const twell_mat_t *x, void *ws, hipStream_t s, bool *packed)
     *packed = fp4_pack_bytes(x) != 0;
     if (!*packed)
         return {(const uint8_t *)x->data, x->ld * 2, x->rows, 1, nkb, 0};
-    const int64_t tiles = (int64_t)((nkb * (FP4_BLK / 8) + 255) / 256) * x->rows;
-    fp4_pack_kernel<<<groups(tiles), 256, 0, s>>>(x->data, x->dtype, x->ld, x->cols, nkb, tiles,
-                                                  (uint8_t *)ws);
+    const int64_t pieces = (int64_t)nkb * (FP4_BLK / 8) * x->rows;
+    fp4_pack_kernel<<<groups((pieces + 255) / 256), 256, 0, s>>>(x->data, x->dtype, x->ld, x->cols,
+                                                                 nkb, pieces, (uint8_t *)ws);
     return {(const uint8_t *)ws, row * planes, x->rows, planes, nkb, row};
 }
 
@@ -279,24 +279,17 @@ hipError_t launch_fp4_quant(const twell_mat_t *x, const twell_fp4_t *o, twell_ti
     return hipGetLastError();
 }
 
-void fp4_dequant(const Fp4 &w, void *out, int64_t ld, int dt, int rows, int cols, hipStream_t s)
-{
-    const int n = dt == TWELL_BF16 ? 8 : 4;
-    const int64_t tiles = (int64_t)(((cols + n - 1) / n + 255) / 256) * ((rows + DR - 1) / DR);
-    if (tiles == 0)
-        return;
-    const DequantArgs a = {w, out, ld, rows, cols, tiles};
-    if (dt == TWELL_BF16)
-        fp4_dequant_kernel<uint16_t><<<groups(tiles), 256, 0, s>>>(a);
-    else
-        fp4_dequant_kernel<uint32_t><<<groups(tiles), 256, 0, s>>>(a);
-}
-
 hipError_t launch_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing_t *timing,
                               hipStream_t s)
 {
     Timer tm(timing, s);
-    fp4_dequant(fp4_arg(w), out->data, out->ld, out->dtype, out->rows, out->cols, s);
+    const int n = out->dtype == TWELL_BF16 ? 8 : 4, cn = (int)(((int64_t)w->cols + n - 1) / n);
+    const int64_t pieces = (int64_t)cn * ((w->rows + DR - 1) / DR);
+    const DequantArgs a = {fp4_arg(w), out->data, out->ld, cn, pieces};
+    if (out->dtype == TWELL_BF16)
+        fp4_dequant_kernel<uint16_t><<<groups((pieces + 255) / 256), 256, 0, s>>>(a);
+    else
+        fp4_dequant_kernel<uint32_t><<<groups((pieces + 255) / 256), 256, 0, s>>>(a);
     tm.mark("fp4_dequant");
     return hipGetLastError();
 }
