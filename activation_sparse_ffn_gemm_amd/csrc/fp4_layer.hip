@@ -3,16 +3,19 @@
 // time, at a quarter of them).
 //  1. g = x Wg^T and u = x Wu^T in one kernel, the product of few tokens, whose
 //     results are a = g u where g's gate is open. u is formed of every neuron:
-//     up to 2^26 weights that is sooner done than a second launch that waits for
-//     the gates and gathers rows (one token, 1% open, 2304 x 6144: 11.6 against
-//     18.1 us of the layer; 4096 x 8192: 14.5 against 25.2, 20% open 21 against 94). Past that
-//     the gates go first and a second kernel reads wu's rows of the open ones
-//     (4096 x 32768, 1% open: 43 against 47). More than one tile of tokens takes
-//     the product of many tokens, its contraction in parts, and a small kernel
-//     that adds the parts and forms a.
+//     a second launch that waits for the gates and gathers wu's rows of the open
+//     ones reads fewer bytes and takes longer (one token, 1% open, 2304 x 6144: 15.4
+//     against 10.3 us of the layer; 4096 x 8192 22.4 against 13.4; 20% open 90 against
+//     21; only at 4096 x 32768 38.7 against 44.5, with 10% open 93 against 60). More
+//     than few tokens take the product of many tokens, its contraction in one or two
+//     parts, and a small kernel that adds the parts and forms a (4.2 us at 64 x
+//     6144, a launch and a trip; forming it where it is read, once for each slice of
+//     columns, takes 5.8 more there).
 //  2. down: a workgroup takes a slice of a token's columns; its waves share the
 //     neurons, gather the slice of wd's row for the open gates, and their sums
-//     meet in LDS in a fixed order.
+//     meet in LDS in a fixed order. Two trips to memory, the gates' and the rows':
+//     one token 4.6 us (18 workgroups), 64 tokens 8.4 (320).
+// The layer of 2304 x 6144, 1% open: one token 9.9 us, 64 tokens 23.6.
 #include "fp4.hpp"
 
 namespace {
@@ -49,71 +52,6 @@ __global__ __launch_bounds__(64) void fp4_act_kernel(const float *gu, int parts,
     }
     *(floatx4_t *)(a + q) = floatx4_t{fp4_act(g[0], u[0]), fp4_act(g[1], u[1]),
                                       fp4_act(g[2], u[2]), fp4_act(g[3], u[3])};
-}
-
-// A wave takes 64 neurons of a token, whose gates are in a: it goes through the
-// open ones, all lanes on a row of wu.
-struct UpArgs {
-    const void *x;
-    int64_t ldx;
-    int dt, T, d, f;
-    Fp4 w;
-    float *a;
-};
-__global__ __launch_bounds__(64 * LW) void fp4_up_kernel(UpArgs p)
-{
-    constexpr int DEEP = 4; // pieces of 512 columns in flight
-    const int lane = threadIdx.x & 63, nc = p.f / 64, shift = 31 - __builtin_clz(p.w.group);
-    const int item = (int)blockIdx.x * LW + wave_id();
-    if (item >= p.T * nc)
-        return;
-    const int t = item / nc, n = item % nc * 64;
-    float *ap = p.a + (int64_t)t * p.f + n + lane;
-    const float g = *ap;
-    const void *x = row_ptr(p.x, p.dt, p.ldx, t);
-    float a = __uint_as_float(FP4_CLOSED);
-    for (uint64_t open = __ballot(!(g <= 0.f)); open; open &= open - 1) {
-        const int i = __builtin_ctzll(open);
-        const uint8_t *row = p.w.q + (int64_t)(n + i) * p.w.pitch;
-        float u = 0.f;
-        for (int j0 = 8 * lane; j0 < p.d + 8 * lane; j0 += 512 * DEEP) {
-            uint32_t q[DEEP];
-            uint16_t s[DEEP];
-            uint4 lo[DEEP], hi[DEEP];
-#pragma unroll
-            for (int k = 0; k < DEEP; ++k) { // (d is a multiple of 64; past it: not counted)
-                const int j = min(j0 + 512 * k, p.d - 8);
-                q[k] = *(const uint32_t *)(row + j / 2);
-                s[k] = p.w.scale[(int64_t)(j >> shift) * p.f + n + i];
-                if (p.dt == TWELL_BF16) {
-                    lo[k] = ldg16u((const uint16_t *)x + j);
-                } else {
-                    lo[k] = ldg16u((const float *)x + j);
-                    hi[k] = ldg16u((const float *)x + j + 4);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < DEEP; ++k) {
-                float c[8], xv[8], v = 0.f;
-                fp4x8_to_f32(q[k], c);
-                if (p.dt == TWELL_BF16) {
-                    elem<TWELL_BF16>::widen(lo[k], xv);
-                } else {
-                    elem<TWELL_F32>::widen(lo[k], xv);
-                    elem<TWELL_F32>::widen(hi[k], xv + 4);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v = fmaf(c[e], xv[e], v);
-                if (j0 + 512 * k < p.d)
-                    u = fmaf(v, bf16_to_f32(s[k]), u);
-            }
-        }
-        u = wave_sum(u);
-        if (lane == i)
-            a = fp4_act(g, u);
-    }
-    *ap = a;
 }
 
 // LPR: lanes of a row, eight columns each (a slice is 8 LPR columns)
@@ -219,15 +157,9 @@ hipError_t launch_fp4_layer(const twell_mat_t *x, const twell_fp4_t *wg, const t
         tm.mark("fp4_gates");
         fp4_act_kernel<<<(uint32_t)(((int64_t)T * f / 4 + 63) / 64), 64, 0, s>>>(gu, parts, T, f, a);
         tm.mark("fp4_act");
-    } else if ((int64_t)f * d <= 1 << 26) { // (see the top)
+    } else {
         fp4_rows(acts, g, &u, a, f, TWELL_F32, s);
         tm.mark("fp4_gate_up");
-    } else {
-        fp4_rows(acts, g, nullptr, a, f, TWELL_F32, s);
-        tm.mark("fp4_gate");
-        const UpArgs p = {x->data, x->ld, (int)x->dtype, T, d, f, u, a};
-        fp4_up_kernel<<<(uint32_t)((T * (f / 64) + LW - 1) / LW), 64 * LW, 0, s>>>(p);
-        tm.mark("fp4_up");
     }
     const LayerArgs p = {T, d, f, fp4_arg(wd), a, y};
     // a slice of 512 columns reads the gates' list least often, one of 128 fills the

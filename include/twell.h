@@ -518,8 +518,7 @@ size_t twell_fp4_matmul_dx_workspace_bytes(twell_dtype dy_dtype, int32_t T, int3
  *   g = x wg_t^T,  u = x wu_t^T,  y = sum over neurons i with g_i > 0 of
  *   g_i u_i wd[i]
  * in float32 throughout (g and u are not rounded to a storage type; a NaN of g
- * counts as positive). wd's rows are read only where a gate is open; u is formed
- * of every neuron unless few tokens meet more than 2^26 weights a matrix.
+ * counts as positive). wd's rows are read only where a gate is open.
  *   x [T][d_model] float32 or bfloat16, 0 <= T <= TWELL_DECODE_T, rows any
  *   stride apart; wg_t, wu_t, wd [d_ff][d_model] of one group, d_model and d_ff
  *   within the layer's limits (d_model <= 4096); y [T][d_model] float32.

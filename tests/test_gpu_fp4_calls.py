@@ -108,7 +108,7 @@ def test_layer_of_many_tokens(T, d, f, group, dtype):
 
 @pytest.mark.parametrize("T", (1, 3, 5, 17))
 def test_layer_of_many_weights(T):
-    """Past 2^26 weights few tokens gather wu's rows."""
+    """Few tokens by the most weights that the layer is given here."""
     d, f, group = 4096, 16512, 64
     for dtype in (BF, F32):
         g = gen(3)
