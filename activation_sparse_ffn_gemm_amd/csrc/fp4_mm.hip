@@ -469,11 +469,12 @@ struct JoinArgs {
     void *out;
     int64_t ldo;
     int dto;
+    uint32_t grid; // workgroups
 };
 __global__ __launch_bounds__(64) void fp4_join_kernel(JoinArgs a)
 {
     const int64_t n4 = (a.N + 3) / 4, total = n4 * a.T, stride = (int64_t)a.T * a.pitch;
-    for (int64_t q = (int64_t)blockIdx.x * 64 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 64) {
+    for (int64_t q = (int64_t)blockIdx.x * 64 + threadIdx.x; q < total; q += (int64_t)a.grid * 64) {
         const int64_t t = q / n4;
         const int n = (int)(q % n4) * 4;
         const float *src = a.part + t * a.pitch + n;
@@ -491,10 +492,11 @@ __global__ __launch_bounds__(64) void fp4_join_kernel(JoinArgs a)
         store4(a.out, a.dto, a.ldo, t, n, a.N, sum);
     }
 }
-void join(const JoinArgs &a, hipStream_t s)
+void join(JoinArgs a, hipStream_t s)
 {
     const int64_t wgs = ((int64_t)((a.N + 3) / 4) * a.T + 63) / 64;
-    fp4_join_kernel<<<(uint32_t)(wgs < 1 << 24 ? wgs : 1 << 24), 64, 0, s>>>(a);
+    a.grid = (uint32_t)(wgs < 1 << 24 ? wgs : 1 << 24);
+    fp4_join_kernel<<<a.grid, 64, 0, s>>>(a);
 }
 
 template <int TB> void cols_tb(const ColsArgs &a, hipStream_t s)
@@ -1023,7 +1025,7 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
         tm.mark("fp4_pack");
     uint8_t *ws2 = (uint8_t *)ws + up256(fp4_pack_bytes(x));
     const int dto = out->dtype, planes = planes_of(x);
-    JoinArgs j = {(float *)ws2, 1, a.T, dx ? w.cols : w.rows, 0, out->data, out->ld, dto};
+    JoinArgs j = {(float *)ws2, 1, a.T, dx ? w.cols : w.rows, 0, out->data, out->ld, dto, 0};
     if (!dx && few_fwd(a.T, planes, w.rows, w.nkb)) {
         fp4_rows(a, w, nullptr, out->data, out->ld, dto, s);
         tm.mark("fp4_rows");

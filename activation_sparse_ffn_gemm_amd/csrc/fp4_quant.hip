@@ -79,10 +79,13 @@ struct QuantArgs {
     uint8_t *q;
     uint16_t *scale;
     int64_t pitch, tiles;
+    uint32_t grid;
 };
 
 // Workgroups of a launch (their threads are numbered in 32 bits): further tiles
-// are taken by the same ones.
+// are taken by the same ones. The kernels are told their number: one that asks
+// for it gets 256 bytes of arguments more, and a launch costs the host 0.5 us
+// more for 150 bytes.
 inline uint32_t groups(int64_t tiles) { return (uint32_t)(tiles < 1 << 22 ? tiles : 1 << 22); }
 
 // A workgroup takes QR rows by QB blocks of columns; 16 lanes hold a block of a
@@ -96,7 +99,7 @@ template <int G> __global__ __launch_bounds__(256) void fp4_quant_kernel(QuantAr
     const int nbt = (a.nkb + QB - 1) / QB;
     const int l16 = threadIdx.x & 15, sub = threadIdx.x >> 4, cb = sub % QB, rr = sub / QB;
     constexpr int STEP = 16 / QB;
-    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    for (int64_t tile = blockIdx.x; tile < a.tiles; tile += a.grid) {
         const int b0 = (int)(tile % nbt) * QB, b = b0 + cb, j = b * FP4_BLK + l16 * 8;
         const int64_t r0 = tile / nbt * QR;
         if (b < a.nkb) {
@@ -142,6 +145,7 @@ struct DequantArgs {
     void *out;
     int64_t ld;
     int cn; // pieces of a row
+    uint32_t grid;
     int64_t pieces;
 };
 // One thread takes 16 bytes of results of each of DR rows: eight bfloat16 or four
@@ -151,7 +155,7 @@ template <class T> __global__ __launch_bounds__(256) void fp4_dequant_kernel(Deq
 {
     constexpr int N = 16 / sizeof(T);
     const int shift = 31 - __builtin_clz(a.w.group);
-    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < a.pieces; i0 += (int64_t)gridDim.x * 256) {
+    for (int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x; i0 < a.pieces; i0 += (int64_t)a.grid * 256) {
         const int64_t rg = row_of(i0, a.cn);
         const int j = (int)(i0 - rg * a.cn) * N;
         const int64_t r0 = rg * DR;
@@ -228,10 +232,10 @@ DEVI void pack8(const void *x, int dt, int64_t ld, int64_t t, int c, int C, int 
 
 // Rows of bfloat16 padded to whole blocks, three rows a float32 row (see Acts).
 __global__ __launch_bounds__(256) void fp4_pack_kernel(const void *x, int dt, int64_t ld, int C,
-                                                       int nkb, int64_t pieces, uint8_t *out)
+                                                       int nkb, int64_t pieces, uint32_t grid, uint8_t *out)
 {
     const int n = nkb * (FP4_BLK / 8);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)grid * 256) {
         const int64_t t = row_of(i, n);
         pack8(x, dt, ld, t, (int)(i - t * n), C, nkb, out);
     }
@@ -257,8 +261,9 @@ Acts fp4_pack(const twell_mat_t *x, void *ws, hipStream_t s, bool *packed)
     if (!*packed)
         return {(const uint8_t *)x->data, x->ld * 2, x->rows, 1, nkb, 0};
     const int64_t pieces = (int64_t)nkb * (FP4_BLK / 8) * x->rows;
-    fp4_pack_kernel<<<groups((pieces + 255) / 256), 256, 0, s>>>(x->data, x->dtype, x->ld, x->cols,
-                                                                 nkb, pieces, (uint8_t *)ws);
+    const uint32_t grid = groups((pieces + 255) / 256);
+    fp4_pack_kernel<<<grid, 256, 0, s>>>(x->data, x->dtype, x->ld, x->cols, nkb, pieces, grid,
+                                         (uint8_t *)ws);
     return {(const uint8_t *)ws, row * planes, x->rows, planes, nkb, row};
 }
 
@@ -267,14 +272,15 @@ hipError_t launch_fp4_quant(const twell_mat_t *x, const twell_fp4_t *o, twell_ti
 {
     Timer tm(timing, s);
     QuantArgs a = {x->data, x->ld, x->dtype, x->rows, x->cols, fp4_blocks(x->cols),
-                   o->q, o->scale, fp4_pitch(x->cols), 0};
+                   o->q, o->scale, fp4_pitch(x->cols), 0, 0};
     a.tiles = (int64_t)((a.nkb + QB - 1) / QB) * ((a.R + QR - 1) / QR);
+    a.grid = groups(a.tiles);
     if (o->group == 32)
-        fp4_quant_kernel<32><<<groups(a.tiles), 256, 0, s>>>(a);
+        fp4_quant_kernel<32><<<a.grid, 256, 0, s>>>(a);
     else if (o->group == 64)
-        fp4_quant_kernel<64><<<groups(a.tiles), 256, 0, s>>>(a);
+        fp4_quant_kernel<64><<<a.grid, 256, 0, s>>>(a);
     else
-        fp4_quant_kernel<128><<<groups(a.tiles), 256, 0, s>>>(a);
+        fp4_quant_kernel<128><<<a.grid, 256, 0, s>>>(a);
     tm.mark("fp4_quant");
     return hipGetLastError();
 }
@@ -285,11 +291,11 @@ hipError_t launch_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twel
     Timer tm(timing, s);
     const int n = out->dtype == TWELL_BF16 ? 8 : 4, cn = (int)(((int64_t)w->cols + n - 1) / n);
     const int64_t pieces = (int64_t)cn * ((w->rows + DR - 1) / DR);
-    const DequantArgs a = {fp4_arg(w), out->data, out->ld, cn, pieces};
+    const DequantArgs a = {fp4_arg(w), out->data, out->ld, cn, groups((pieces + 255) / 256), pieces};
     if (out->dtype == TWELL_BF16)
-        fp4_dequant_kernel<uint16_t><<<groups((pieces + 255) / 256), 256, 0, s>>>(a);
+        fp4_dequant_kernel<uint16_t><<<a.grid, 256, 0, s>>>(a);
     else
-        fp4_dequant_kernel<uint32_t><<<groups((pieces + 255) / 256), 256, 0, s>>>(a);
+        fp4_dequant_kernel<uint32_t><<<a.grid, 256, 0, s>>>(a);
     tm.mark("fp4_dequant");
     return hipGetLastError();
 }
