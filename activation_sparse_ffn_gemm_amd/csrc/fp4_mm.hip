@@ -70,7 +70,14 @@ DEVI void store4(void *out, int dto, int64_t ldo, int64_t row, int n, int N, flo
 // LDS, NST blocks in turn, without a barrier: a wave waits for its own loads.
 // The W rows are the instruction's first operand and the activations its
 // second: a lane's four results are four rows of one column. A group's sum
-// starts from zero and joins the accumulator times the group's scales.
+// starts from zero and joins the accumulator times the group's scales: codes
+// widened as they are (two an instruction) cost a quarter of scaled ones, which
+// only many tokens pay back.
+// A short product is a launch and two trips to memory (1 x 6144 over 2304 3.9 us);
+// a long one is bound by memory (8 x 32768 over 4096, a scale for 32: 17 us, 75.5
+// MB, 4.4 TB/s; 1 x 8192 over 8192 9.5 us). In between, on few CUs, by the 28
+// vector instructions a set and block: 0.15 us of a wave beside another (2304 over
+// 6144 with a scale for 32, 5.9 us; for 128, 4.7).
 struct RowsArgs {
     const uint8_t *x;
     int64_t xrow;      // bytes from one column's row to the next
@@ -133,6 +140,9 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
     for (int i = 0; i < NB; ++i)
         acc[i] = floatx4_t{0.f, 0.f, 0.f, 0.f};
     const int xr = l16 % XR;
+    // Workgroups begin at different blocks: rows whose pitch is a large power of two
+    // would otherwise all be read from the same few memory channels at once. It goes
+    // by their rows, so that a token's sums do not depend on the tokens beside it.
     const uint32_t turn = (uint32_t)(a.tile0 + tile) & 7;
     for (int k0 = 0; k0 < a.w.nkb; k0 += SCB) {
         const int nk = min(SCB, a.w.nkb - k0);
@@ -311,7 +321,10 @@ template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
 // of one token are runs of eight columns.
 // A workgroup takes a block of 128 columns and one of `parts` runs of rows; its
 // waves take 32 rows at a time. The activations of CN rows are staged in LDS.
-// Parts are joined by a second launch.
+// Parts are joined by a second launch (2.3 us): a block of columns for each of 18
+// CUs alone would take the whole contraction one trip after another.
+// One token over 6144 x 2304 7.3 us, both launches and their trips; over 16384 x 4096
+// 16 us (35 MB).
 struct ColsArgs {
     const uint8_t *x;
     int64_t xrow;
@@ -461,7 +474,8 @@ template <int TB, int U> __global__ __launch_bounds__(64 * CWV) void fp4_cols_ke
     }
 }
 
-// out [T][N] = the sum of the parts, in order. Four columns a thread.
+// out [T][N] = the sum of the parts, in order. Four columns a thread, eight parts in
+// flight (17 x 2304 of 12 parts 2.3 us, a launch and a trip; one after another 10).
 struct JoinArgs {
     const float *part;
     int parts, T, N;
@@ -569,9 +583,22 @@ int64_t part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
 // operand) by MI of tokens. W's codes become bfloat16 numbers times their scales
 // in registers, a fragment at a time beside the products of the one before, so
 // they cost LDS and memory a quarter of what values do.
-// The step's one barrier stands before its last row of products: by then every
-// read of its stage is done and the next stage's loads are in, and the next
-// step's first fragments are read beside that row.
+// A step's codes are read two rows of products ahead and its tokens one, so at the
+// step's one barrier, before its last two rows, all of it is in registers: its own
+// stage is loaded anew behind the barrier, NST steps ahead.
+// DX, of dY W: the contraction runs over W's rows, a step is 64 of them, 16 codes of a
+// row in a lane, and the transposing LDS read of 4-bit elements (lane c of 16 gets
+// code c of the 16 lanes' rows, as measured on the part) gives a lane its column's 16
+// rows. Their scales, 16 to a lane, are the same for the 16 lanes of a row group.
+// What bounds a large product is the matrix unit and the vector instructions that
+// scale the codes (two an element, three of dY W, where each of a pair has its own
+// scale), which take turns for the most part: busy 0.55 and 0.34 of the time of
+// 8192 x 5632 over 2048, 160 us, 1180 TF (the library's bfloat16 product of these sizes
+// without any codes: 164); dY W 155 us (library 131). Small ones: the steps' latency on
+// one or two workgroups a CU (512 x 5632 over 2048 21 us, 64 x 4096 over 4096 of dY W 14).
+// Tried without gain: two products at a time between the instructions of one, five
+// stages, 128 x 128 tiles of 2 x 2 or 2 x 4 waves (5 to 15% slower: codes are scaled
+// by two waves each).
 template <int BM_, int BN_, int WGM_, int WGN_, int NST_, int KS_, int SG_> struct TileCfg {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_, NST = NST_, KS = KS_;
     static constexpr int NWV = WGM * WGN, NT = 64 * NWV;

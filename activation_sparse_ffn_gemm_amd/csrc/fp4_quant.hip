@@ -89,8 +89,10 @@ struct QuantArgs {
 inline uint32_t groups(int64_t tiles) { return (uint32_t)(tiles < 1 << 22 ? tiles : 1 << 22); }
 
 // A workgroup takes QR rows by QB blocks of columns; 16 lanes hold a block of a
-// row, eight elements each. The scales of the QR rows, which are neighbours in
-// memory, meet in LDS and are written as runs.
+// row, eight elements each, and a thread's rows are all in flight. The scales of
+// the QR rows, which are neighbours in memory, meet in LDS and are written as runs.
+// Bound by memory: 5632 x 2048 float32 in 10.3 us (52.4 MB, 5.1 TB/s), 8192 x 5632 in
+// 41 (5.1); tiles of 32 rows, fewer workgroups with the same bytes each, took 14.3.
 constexpr int QR = 8, QB = 4;
 template <int G> __global__ __launch_bounds__(256) void fp4_quant_kernel(QuantArgs a)
 {
@@ -149,7 +151,9 @@ struct DequantArgs {
     int64_t pieces;
 };
 // One thread takes 16 bytes of results of each of DR rows: eight bfloat16 or four
-// float32 columns.
+// float32 columns. Bound by memory: 6144 x 2304 to bfloat16 in 7.4 us (36 MB, 4.9
+// TB/s). Threads are numbered over the whole matrix; a launch's threads by rows, a
+// second workgroup for the last 32 of 288 pieces, took 8.8. Results go past L2's order.
 constexpr int DR = 4;
 template <class T> __global__ __launch_bounds__(256) void fp4_dequant_kernel(DequantArgs a)
 {
@@ -230,7 +234,8 @@ DEVI void pack8(const void *x, int dt, int64_t ld, int64_t t, int c, int C, int 
     put(3 * t, hi), put(3 * t + 1, mid), put(3 * t + 2, lo);
 }
 
-// Rows of bfloat16 padded to whole blocks, three rows a float32 row (see Acts).
+// Rows of bfloat16 padded to whole blocks, three rows a float32 row (see Acts). A
+// launch and a trip to memory: 333 x 1090 float32 3 to 5 us, 17 x 6144 2.8.
 __global__ __launch_bounds__(256) void fp4_pack_kernel(const void *x, int dt, int64_t ld, int C,
                                                        int nkb, int64_t pieces, uint32_t grid, uint8_t *out)
 {
