@@ -12,9 +12,12 @@ bfloat16 copies, the projection on 8-bit copies (both orientations, one scale
 a 128 x 128 block), made once a step. The projection's two gradients are 8-bit
 products as well: of d_out quantised along both of its axes with W^T and with
 n2^T. Serving norms straight into 8 bits, so that the normed stream crosses
-HBM in one byte an element.
+HBM in one byte an element. `freeze` makes 4-bit copies of every weight, which
+`serve_fp4` serves from: few tokens straight from the codes, a prefill of the sparse
+layer from the values that they stand for.
 
     python examples/prenorm_block.py [--tokens 4096] [--d-model 1024] [--d-ff 2816] [--steps 5]
+        [--group 64]
 """
 import argparse
 import os
@@ -97,6 +100,22 @@ class PrenormBlock:
         n2, h2 = tw.rmsnorm_fwd(y, m["g2"], residual=h1, eps=self.eps, out_dtype=E4)
         return tw.fp8_matmul(n2, self.proj, fast_sums=True), h2
 
+    def freeze(self, group=128):
+        """Copies of the masters in 4 bits, one scale for `group` weights."""
+        self.w4 = {k: tw.fp4_quant(self.master[k], group=group) for k in ("wg", "wu", "wd", "proj")}
+
+    def serve_fp4(self, a, h0):
+        """serve() from the 4-bit copies."""
+        m, w = self.master, self.w4
+        n1, h1 = tw.rmsnorm_fwd(a, m["g1"], residual=h0, eps=self.eps)
+        if n1.shape[0] <= tw.DECODE_T:
+            y = tw.fp4_decode_fwd(n1, w["wg"], w["wu"], w["wd"])
+        else:
+            wg, wu, wd = (tw.fp4_dequant(w[k]) for k in ("wg", "wu", "wd"))
+            y = tw.ffn_fwd(n1, tw.gate_pack(n1, wg, status=self.status), wu, wd, status=self.status)
+        n2, h2 = tw.rmsnorm_fwd(y, m["g2"], residual=h1, eps=self.eps)
+        return tw.fp4_matmul(n2, w["proj"]), h2
+
     def check(self):
         code = int(self.status.item())
         if code:
@@ -138,6 +157,7 @@ def main(argv=None):
     p.add_argument("--density", type=float, default=0.01)
     p.add_argument("--steps", type=int, default=5)
     p.add_argument("--lr", type=float, default=0.02)
+    p.add_argument("--group", type=int, default=64, help="weights that share a 4-bit scale")
     o = p.parse_args(argv)
     block, a, h0 = make_case(o.tokens, o.d_model, o.d_ff, o.d_out, o.density, skew=0.02)
     target = torch.randn((o.tokens, o.d_out), device=a.device,
@@ -156,6 +176,16 @@ def main(argv=None):
     print(f"prefill of {o.tokens} tokens: {t * 1e3:.3f} ms, {o.tokens / t / 1e6:.2f} M tokens/s")
     t = _time(lambda: block.serve(a[:1], h0[:1]))
     print(f"one token: {t * 1e6:.0f} us")
+    block.freeze(o.group)
+    out4, _ = block.serve_fp4(a, h0)
+    few4, _ = block.serve_fp4(a[:1], h0[:1])
+    block.check()
+    gap = float((out4.float() - out.float()).norm() / out.float().norm())
+    alone = float((few4.float() - out4[:1].float()).norm() / out4[:1].float().norm())
+    print(f"weights in 4 bits: {gap:.2f} of the result's norm from the block as trained; one token "
+          f"alone against the same token in the prefill: {alone:.1e}")
+    t = _time(lambda: block.serve_fp4(a[:1], h0[:1]))
+    print(f"one token from 4 bits: {t * 1e6:.0f} us")
     return losses
 
 

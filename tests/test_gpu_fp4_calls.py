@@ -432,3 +432,27 @@ def test_block_in_four_bits(T, group):
     # a long prefill multiplies by the values themselves
     long = tw.fp4_dequant(w4["g"])
     assert torch.equal(long.cpu().double(), v["g"])
+
+
+def test_the_example_serves_from_four_bits():
+    """One token, several and a prefill: the calls it makes, on what the stages give."""
+    from test_gpu_prenorm_block import _example
+    block, a, h0 = _example().make_case(150, 256, 512, 136, density=0.05)
+    block.freeze(64)
+    w = block.w4
+    for T in (1, 20, 150):
+        out, h2 = block.serve_fp4(a[:T], h0[:T])
+        block.check()
+        n1, h1 = tw.rmsnorm_fwd(a[:T], block.master["g1"], residual=h0[:T], eps=block.eps)
+        v = [w[k].float().double().cpu() for k in ("wg", "wu", "wd")]
+        y, tol = ref.layer(n1, *v)
+        # the prefill's layer rounds the gates to bfloat16, half a step of each
+        if T > tw.DECODE_T:
+            n = n1.double().cpu()
+            h = (n @ v[0].t()).clamp(min=0)
+            tol = tol + ref.UBF * ((h * (n @ v[1].t())).abs() @ v[2].abs())
+        within(h2, h1.double().cpu() + y, tol + ref.U32 * (h1.double().cpu().abs() + y.abs()))
+        n2, _ = tw.rmsnorm_fwd(h2, block.master["g2"], eps=block.eps)
+        want, mag = ref.matmul(n2, w["proj"].float().double().cpu())
+        # n2 of the stored h2 is a step of bfloat16 from the example's at most
+        within(out, want, ref.bound(mag, want, 256, BF) + 2 * ref.UBF * mag)
