@@ -592,10 +592,10 @@ int64_t part_pitch(int N) { return ((int64_t)N + 3) / 4 * 4; }
 // rows. Their scales, 16 to a lane, are the same for the 16 lanes of a row group.
 // What bounds a large product is the matrix unit and the vector instructions that
 // scale the codes (two an element, three of dY W, where each of a pair has its own
-// scale), which take turns for the most part: busy 0.55 and 0.34 of the time of
+// scale), which take turns for the most part: busy 0.50 and 0.43 of the time of
 // 8192 x 5632 over 2048, 160 us, 1180 TF (the library's bfloat16 product of these sizes
 // without any codes: 164); dY W 155 us (library 131). Small ones: the steps' latency on
-// one or two workgroups a CU (512 x 5632 over 2048 21 us, 64 x 4096 over 4096 of dY W 14).
+// one or two workgroups a CU (512 x 5632 over 2048 20 us, 64 x 4096 over 4096 of dY W 14).
 // Tried without gain: two products at a time between the instructions of one, five
 // stages, 128 x 128 tiles of 2 x 2 or 2 x 4 waves (5 to 15% slower: codes are scaled
 // by two waves each).
