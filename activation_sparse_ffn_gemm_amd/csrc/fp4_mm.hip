@@ -1007,7 +1007,8 @@ int token_tiles(int T, int planes) { return (T + (planes == 3 ? 4 : 15)) / (plan
 bool few_fwd(int T, int planes, int64_t N, int nkb)
 {
     const int64_t mt = token_tiles(T, planes);
-    return mt <= 2 || mt * ((N + 15) / 16) * nkb <= 22000;
+    // (of no blocks the tiles store the zeros: rows_one's launches are for few tokens)
+    return mt <= 2 || (nkb > 0 && mt * ((N + 15) / 16) * nkb <= 22000);
 }
 bool few_dx(int T, int planes) { return token_tiles(T, planes) <= 2; }
 int planes_of(const twell_mat_t *x) { return x->dtype == TWELL_BF16 ? 1 : 3; }

@@ -386,6 +386,15 @@ def test_nothing_to_do():
     assert tw.fp4_dequant(none).shape == (0, 200)
 
 
+def test_sums_of_nothing_for_many_tokens():
+    """No columns, and more tokens than a launch of the few-token kernels has workgroups for."""
+    for T, dtype in ((300, BF), (5 * (1 << 22) + 7, F32)):
+        x, w4 = torch.empty(T, 0, device=DEV, dtype=dtype), tw.empty_fp4(2, 0, 64, DEV)
+        out = torch.full((T, 2), 7.0, device=DEV, dtype=dtype)
+        tw.fp4_matmul(x, w4, out=out, out_dtype=dtype)
+        assert not bool(out.any())
+
+
 def test_kernels_are_timed():
     t, seen = tw.KernelTimer(), {}
     w4, ms = coded(300, 520, 64, 1)[0], [coded(256, 192, 32, i)[0] for i in range(3)]
