@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "fp4.hpp"
+#include "fp4_plan.hpp"
 
 namespace {
 
@@ -319,19 +320,19 @@ template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
 // rows' scales (a bfloat16 number each, for six-bit scales exactly). Tile j of
 // the eight 16 x 16 tiles is columns j, 8 + j, 16 + j ..., and a lane's results
 // of one token are runs of eight columns.
-// A workgroup takes a block of 128 columns and one of `parts` runs of rows; its
-// waves take 32 rows at a time. The activations of CN rows are staged in LDS.
+// A workgroup takes a block of 128 columns and one of plan.parts runs of rows; its
+// waves take 32 rows at a time. The activations of a step's rows are staged in LDS.
 // Parts are joined by a second launch (2.3 us): a block of columns for each of 18
 // CUs alone would take the whole contraction one trip after another.
-// One token over 6144 x 2304 7.3 us, both launches and their trips; over 16384 x 4096
-// 16 us (35 MB).
+// One token over 6144 x 2304 7.5 us, both launches and their trips (16 tokens 8.6, ten
+// of float32 12.6 with their packing); over 16384 x 4096 15.4 us (35 MB).
 struct ColsArgs {
     const uint8_t *x;
     int64_t xrow;
     int T, planes, nkx; // nkx: blocks of 128 that the activations are padded to
     Fp4 w;
     float *part; // [parts][T][128 nkb]
-    int parts, per; // rows of a part: a multiple of CN
+    ColsPlan plan;
     void *out; // of one part
     int64_t ldo;
     int dto;
@@ -363,8 +364,9 @@ DEVI void turn8(uint32_t *v)
 }
 
 // TB: 16-column tiles of activations (five float32 tokens each); U: sets of 32
-// rows that a wave has in flight.
-constexpr int CWV = 8, CN = 32 * CWV;
+// rows that a wave has in flight, plan.sets. A part is whole steps of them, so only
+// the last one ends inside a step, at the matrix's end.
+constexpr int CWV = FP4_CWV, CN = FP4_CN;
 template <int TB, int U> __global__ __launch_bounds__(64 * CWV) void fp4_cols_kernel(ColsArgs a)
 {
     constexpr int ROWS = CN * U, XROW = ROWS * 2, XB = 16 * TB * XROW;
@@ -372,12 +374,12 @@ template <int TB, int U> __global__ __launch_bounds__(64 * CWV) void fp4_cols_ke
     __shared__ __attribute__((aligned(16))) uint8_t L[XB > OB ? XB : OB];
     const int lane = threadIdx.x & 63, w = wave_id(), l16 = lane & 15, q4 = lane >> 4;
     // an XCD takes a run of neighbouring blocks: two share W's 128-byte lines
-    const int total = a.w.nkb * a.parts, each = (total + NXCD - 1) / NXCD;
+    const int total = a.w.nkb * a.plan.parts, each = (total + NXCD - 1) / NXCD;
     const int at = (int)blockIdx.x / NXCD, id = (int)(blockIdx.x % NXCD) * each + at;
     if (at >= each || id >= total)
         return;
     const int part = id / a.w.nkb, kb = id % a.w.nkb;
-    const int n_lo = part * a.per, n_hi = min(n_lo + a.per, a.w.rows);
+    const int n_lo = part * a.plan.per, n_hi = min(n_lo + a.plan.per, a.w.rows);
     const bool three = a.planes == 3;
     const uint8_t *wq = a.w.q + (int64_t)kb * FP4_BYTES + l16 * 4;
     const uint16_t *sc = a.w.scale + (int64_t)((kb * FP4_BLK + l16 * 8) / a.w.group) * a.w.rows;
@@ -465,7 +467,7 @@ template <int TB, int U> __global__ __launch_bounds__(64 * CWV) void fp4_cols_ke
         const int m = three ? t * 5 + c : t * 16 + c;
         if (m < a.T && (!three || c < 5)) {
             const floatx4_t o = three ? (sum(3 * c + 2) + sum(3 * c + 1)) + sum(3 * c) : sum(c);
-            if (a.parts == 1)
+            if (a.plan.parts == 1)
                 store4(a.out, a.dto, a.ldo, m, kb * FP4_BLK + k, a.w.cols, o);
             else
                 *(floatx4_t *)(a.part + ((int64_t)part * a.T + m) * a.w.nkb * FP4_BLK +
@@ -515,8 +517,8 @@ void join(JoinArgs a, hipStream_t s)
 
 template <int TB> void cols_tb(const ColsArgs &a, hipStream_t s)
 {
-    const uint32_t grid = (uint32_t)((a.w.nkb * a.parts + NXCD - 1) / NXCD * NXCD);
-    if (a.per > CN)
+    const uint32_t grid = (uint32_t)((a.w.nkb * a.plan.parts + NXCD - 1) / NXCD * NXCD);
+    if (a.plan.sets == 2)
         fp4_cols_kernel<TB, 2><<<grid, 64 * CWV, 0, s>>>(a);
     else
         fp4_cols_kernel<TB, 1><<<grid, 64 * CWV, 0, s>>>(a);
@@ -527,15 +529,6 @@ void cols(const ColsArgs &a, hipStream_t s)
         cols_tb<1>(a, s);
     else
         cols_tb<2>(a, s);
-}
-
-// Parts of the contraction: about a workgroup a CU, of at least CN rows each.
-int cols_parts(int N, int nkb, int *per)
-{
-    const int most = (N + CN - 1) / CN, want = nkb < 256 ? 256 / nkb : 1;
-    const int parts = most < want ? (most > 0 ? most : 1) : want;
-    *per = ((N + parts - 1) / parts + CN - 1) / CN * CN;
-    return *per ? (N + *per - 1) / *per : 1;
 }
 
 // Which tiles, and in how many parts of the contraction: the least of the times
@@ -1036,7 +1029,7 @@ size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
     if (!dx && few_fwd(x->rows, planes, rows, fp4_blocks(cols)))
         return pack;
     if (dx && few_dx(x->rows, planes)) {
-        int per, parts = cols_parts(rows, fp4_blocks(cols), &per);
+        const int parts = cols_plan(rows, fp4_blocks(cols)).parts;
         return parts == 1 ? pack : up256(pack) + (size_t)parts * x->rows * pitch * 4;
     }
     const int n = dx ? cols : rows, nkb = fp4_blocks(dx ? rows : cols);
@@ -1063,9 +1056,9 @@ int launch_fp4_mm(const twell_mat_t *x, const twell_fp4_t *w4, const twell_mat_t
         fp4_rows(a, w, nullptr, out->data, out->ld, dto, s);
         tm.mark("fp4_rows");
     } else if (dx && few_dx(a.T, planes)) {
-        ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T, a.planes, a.nkb, w,
-                      (float *)ws2, 0, 0, out->data, out->ld, dto};
-        c.parts = j.parts = cols_parts(w.rows, w.nkb, &c.per);
+        const ColsArgs c = {a.data, a.planes == 3 ? a.plane : a.pitch, a.T, a.planes, a.nkb, w,
+                      (float *)ws2, cols_plan(w.rows, w.nkb), out->data, out->ld, dto};
+        j.parts = c.plan.parts;
         j.pitch = (int64_t)w.nkb * FP4_BLK;
         cols(c, s);
         tm.mark("fp4_cols");
