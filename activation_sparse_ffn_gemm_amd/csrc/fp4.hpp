@@ -94,10 +94,13 @@ size_t fp4_pack_bytes(const twell_mat_t *x); // 0: taken where it is
 Acts fp4_pack(const twell_mat_t *x, void *ws, hipStream_t s, bool *packed);
 
 // The sparse layer's a = g u of an open gate (NaN opens too). A closed gate's is
-// the one float that a sum with +0 is not.
+// the one float that a sum with +0 of two floats is not: -0. The product is rounded
+// before the sum, not fused with it: fused, one that underflows from below would
+// round to -0 after it.
 constexpr uint32_t FP4_CLOSED = 0x80000000u;
 DEVI float fp4_act(float g, float u)
 {
+#pragma clang fp contract(off)
     return !(g <= 0.f) ? g * u + 0.f : __uint_as_float(FP4_CLOSED);
 }
 
