@@ -88,6 +88,7 @@ struct RowsArgs {
     int64_t ldo;
     int dto, tile0; // first tile of rows of this launch
     int tiles;      // tiles of rows of this launch
+    int turn;       // log2 of the neighbouring rows that begin at the same block of k
     const uint8_t *q2; // BOTH: the up weights, of w's sizes
     const uint16_t *scale2;
 };
@@ -143,8 +144,9 @@ __global__ __launch_bounds__(64 * WV) void fp4_rows_kernel(RowsArgs a)
     const int xr = l16 % XR;
     // Workgroups begin at different blocks: rows whose pitch is a large power of two
     // would otherwise all be read from the same few memory channels at once. It goes
-    // by their rows, so that a token's sums do not depend on the tokens beside it.
-    const uint32_t turn = (uint32_t)(a.tile0 + tile) & 7;
+    // by the rows, in runs that do not depend on the number of tokens, and with it the
+    // order of a token's sums does not depend on the tokens beside it here.
+    const uint32_t turn = (uint32_t)n0 >> a.turn & 7;
     for (int k0 = 0; k0 < a.w.nkb; k0 += SCB) {
         const int nk = min(SCB, a.w.nkb - k0);
         const int n = (nk - w + WV - 1) / WV; // this wave's blocks
@@ -286,9 +288,10 @@ template <int G, int NB, int XR, int WV, int NST, bool BOTH> void rows_one(RowsA
 // another ends (1 x 32768 over 4096: 13.8 against 14.3). Sixteen columns of
 // activations take four times the loads of a set: four sets share them there
 // (16 x 32768 over 4096: 14.9 against 16.0; one set 28.8).
-template <int G, int XR> void rows_x(const RowsArgs &a, hipStream_t s)
+template <int G, int XR> void rows_x(RowsArgs a, hipStream_t s)
 {
-    const bool wide = a.w.rows >= 16384;
+    const bool wide = a.w.rows >= 16384, two = wide || a.w.rows > 16 * 256;
+    a.turn = a.q2 ? (wide ? 5 : 4) : wide ? 6 : two ? 5 : 4; // the most rows of a workgroup
     if (a.q2) {
         if (XR == 16 && wide)
             rows_one<G, 4, XR, 4, 2, true>(a, s);
@@ -296,7 +299,7 @@ template <int G, int XR> void rows_x(const RowsArgs &a, hipStream_t s)
             rows_one<G, 2, XR, 4, 2, true>(a, s);
     } else if (wide) {
         rows_one<G, XR == 16 ? 4 : 2, XR, 4, 2, false>(a, s);
-    } else if (a.w.rows > 16 * 256) {
+    } else if (two) {
         rows_one<G, 2, XR, 8, 2, false>(a, s);
     } else {
         rows_one<G, 1, XR, 8, 2, false>(a, s);
@@ -1012,7 +1015,7 @@ void fp4_rows(const Acts &x, const Fp4 &w, const Fp4 *up, void *out, int64_t ldo
               hipStream_t s)
 {
     const RowsArgs a = {x.data, x.planes == 3 ? x.plane : x.pitch, x.T, x.planes, x.T * x.planes,
-                        w, out, ldo, dto, 0, 0, up ? up->q : nullptr, up ? up->scale : nullptr};
+                        w, out, ldo, dto, 0, 0, 0, up ? up->q : nullptr, up ? up->scale : nullptr};
     if (w.group == 32)
         rows_group<32>(a, s);
     else if (w.group == 64)
