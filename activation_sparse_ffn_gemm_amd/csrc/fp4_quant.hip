@@ -41,12 +41,13 @@ DEVI GroupScale fp4_scale(uint32_t amax_bits)
 // its grid point t is the quotient's own, or the next where the quotient lies
 // just before that one; the sign of v - t s, exact in a fused step, says which,
 // and t moved to that side rounds like the quotient. (The float quotient would
-// be rounded twice.) As e4m3_quotient, on its grid.
+// be rounded twice.) As e4m3_quotient, on its grid, but for where the minus stands:
+// of an exact quotient the rest is -0, and the sum keeps the sign of a zero.
 DEVI float e2m1_quotient(float v, GroupScale g)
 {
     constexpr float DELTA = 0x1p-16f, SMALL = 0x1p-120f;
     const float t = __uint_as_float(__float_as_uint(v * g.inv) & 0xffe00000u);
-    const float rest = __builtin_amdgcn_fmed3f(fmaf(-t, g.s, v), -SMALL, SMALL);
+    const float rest = __builtin_amdgcn_fmed3f(-fmaf(t, g.s, -v), -SMALL, SMALL);
     return fmaf(rest, DELTA / SMALL, t);
 }
 DEVI uint32_t quant8_fp4(const float *v, GroupScale g)

@@ -449,10 +449,10 @@ size_t twell_fp8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K);
  * The library writes scale = amax / 6 over the group, amax held within
  * [2^-64, 2^127], rounded to six significant bits (ties to even): each value
  * times its scale is then a bfloat16 number. A code is that of the value
- * nearest to w / scale, ties to even, at most 6. A group that holds a NaN or
- * an infinity gets the scale NaN and codes of zero, so that all of it stands
- * for NaN. Groups past `cols` get the scale of a group of zeros (a product takes
- * any finite one there).
+ * nearest to w / scale, ties to even, at most 6, with w's sign, a zero's too. A
+ * group that holds a NaN or an infinity gets the scale NaN and codes of zero, so
+ * that all of it stands for NaN. Groups past `cols` get the scale of a group of
+ * zeros (a product takes any finite one there).
  * Other scales are taken as well; where one times a value is no bfloat16
  * number, products of many tokens and dY W take it rounded to the nearest.
  */
