@@ -1,13 +1,15 @@
 """How the gradient of few tokens through weights in 4 bits spreads W's rows over
 workgroups, on the CPU: the plan that the library takes, gone through step by step
 as its kernel does, and seen through the call's workspace."""
+import os
 import shutil
 import subprocess
 
 import pytest
 
 from activation_sparse_ffn_gemm_amd import _lib as tw
-from test_sanitizers import CSRC
+
+CSRC = os.path.join(tw.PKG, "csrc")
 
 # Every row of W in exactly one step of one part: a step takes CN * sets rows from
 # its first one on, as far as the matrix goes.
