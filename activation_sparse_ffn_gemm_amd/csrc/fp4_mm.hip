@@ -325,6 +325,8 @@ template <int G> void rows_group(const RowsArgs &a, hipStream_t s)
 // of one token are runs of eight columns.
 // A workgroup takes a block of 128 columns and one of plan.parts runs of rows; its
 // waves take 32 rows at a time. The activations of a step's rows are staged in LDS.
+// What bounds it is trips to memory: at 6144 x 4096 (14 MB) vector instructions are 0.21
+// of the issue slots, the matrix unit 0.02 busy, and waves wait for half of their time.
 // Parts are joined by a second launch (2.3 us): a block of columns for each of 18
 // CUs alone would take the whole contraction one trip after another.
 // One token over 6144 x 2304 7.5 us, both launches and their trips (16 tokens 8.6, ten
@@ -993,12 +995,19 @@ TilePlan dx_plan(int T, int K, int nkb, int planes)
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
-// Whether the few-token kernels take a product: of X W^T over N rows of nkb blocks
-// up to two 16-column tiles of activations (24 tokens over 6144 x 2304: 8.1 against
-// 11.4 us), or while all tiles together are little work (64 tokens over 1024 x 1024:
-// 3.7 against 8.3, over 6144 x 2304 11.8 against 13.2, over 4096 x 4096 16.0 against
-// 14.4); of dY W up to two tiles (24 tokens over 6144 x 2304: 10.8 against 12.9, 48:
-// 15.3 against 13.6).
+// Whether the few-token kernels take a product. Measured, us, by them and by the tile
+// kernels: of X W^T over N rows of nkb blocks
+// - up to two 16-column tiles of activations: 32 tokens over 6144 x 2304 7.1 and 11.1,
+//   over 4096 x 4096 8.1 and 10.7, over 1024 x 1024 3.0 and 7.1;
+// - more of them while all are little work, their tiles times rows / 16 times blocks at
+//   most 22000: 64 tokens over 1024 x 1024 (2048) 3.5 and 8.1, 48 over 6144 x 2304
+//   (20736) 9.9 and 11.7, ten of float32 as many (13824) 12.7 and 13.5; past it 64 over
+//   4096 x 4096 (32768) 15.5 and 14.0, 128 over 2048 x 5632 (45056) 17.9 and 14.5. The
+//   work alone does not see how many workgroups a CU gets: on the wrong side of the
+//   limit lie 64 tokens over 6144 x 2304 (27648) 10.4 and 12.8, 33 over 11264 x 1024
+//   (16896) 11.9 and 8.4, 128 over 2816 x 1024 (11264) 12.4 and 8.7.
+// Of dY W up to two tiles: 32 tokens over 6144 x 2304 10.9 and 12.3, over 4096 x 4096
+// 10.9 and 11.6, over 1024 x 1024 7.3 and 7.4 (48 over 6144 x 2304 15.3 and 13.0).
 int token_tiles(int T, int planes) { return (T + (planes == 3 ? 4 : 15)) / (planes == 3 ? 5 : 16); }
 bool few_fwd(int T, int planes, int64_t N, int nkb)
 {
@@ -1024,7 +1033,7 @@ void fp4_rows(const Acts &x, const Fp4 &w, const Fp4 *up, void *out, int64_t ldo
         rows_group<128>(a, s);
 }
 
-// Workspace: the packed activations, then the parts' sums or the weights' values.
+// Workspace: the packed activations, then the parts' sums.
 size_t fp4_mm_workspace(const twell_mat_t *x, int rows, int cols, bool dx)
 {
     const size_t pack = fp4_pack_bytes(x), pitch = (size_t)fp4_blocks(cols) * FP4_BLK;

@@ -453,8 +453,9 @@ size_t twell_fp8_matmul_workspace_bytes(int32_t M, int32_t N, int32_t K);
  * group that holds a NaN or an infinity gets the scale NaN and codes of zero, so
  * that all of it stands for NaN. Groups past `cols` get the scale of a group of
  * zeros (a product takes any finite one there).
- * Other scales are taken as well; where one times a value is no bfloat16
- * number, products of many tokens and dY W take it rounded to the nearest.
+ * Other scales are taken as well, NaN or numbers whose sixfold is finite. Where one
+ * of more than six bits times a value is no bfloat16 number, products of many
+ * tokens and dY W take it rounded to the nearest.
  */
 #define TWELL_FP4_BLOCK 128 /* columns that a row is padded to */
 #define TWELL_FP4_MAX_K (1 << 21) /* longest contraction of a product */
@@ -481,9 +482,10 @@ int twell_fp4_dequant(const twell_fp4_t *w, const twell_mat_t *out, twell_timing
 
 /*
  * out[t][n] = sum over k of x[t][k] w[n][k] for w in 4 bits: x [T][w.cols],
- * out [T][w.rows], each float32 or bfloat16 with rows any stride apart. Every
- * product is exact (float32 activations are taken as three bfloat16 numbers
- * that add up to them; values up to 2^110 in size), sums are float32, out is
+ * out [T][w.rows], each float32 or bfloat16 with rows any stride apart. With scales
+ * of six bits every product is exact for activations of zero or 2^-100 to 2^110 in
+ * size (float32 ones are taken as three bfloat16 numbers that add up to them; of
+ * smaller ones what lies below 2^-126 may be lost). Sums are float32, out is
  * rounded once. out must not overlap x. w.cols <= TWELL_FP4_MAX_K, and at most
  * 2^23 pieces of 16 tokens by 128 results.
  *   workspace: twell_fp4_matmul_workspace_bytes(...) bytes are enough for any
