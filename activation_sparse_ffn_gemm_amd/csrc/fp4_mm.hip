@@ -1001,7 +1001,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 //   over 4096 x 4096 8.1 and 10.7, over 1024 x 1024 3.0 and 7.1;
 // - more of them while all are little work, their tiles times rows / 16 times blocks at
 //   most 22000: 64 tokens over 1024 x 1024 (2048) 3.5 and 8.1, 48 over 6144 x 2304
-//   (20736) 9.9 and 11.7, ten of float32 as many (13824) 12.7 and 13.5; past it 64 over
+//   (20736) 9.9 and 11.7, 11 of float32 there (20736 too) 12.7 and 13.5; past it 64 over
 //   4096 x 4096 (32768) 15.5 and 14.0, 128 over 2048 x 5632 (45056) 17.9 and 14.5. The
 //   work alone does not see how many workgroups a CU gets: on the wrong side of the
 //   limit lie 64 tokens over 6144 x 2304 (27648) 10.4 and 12.8, 33 over 11264 x 1024
